@@ -44,7 +44,8 @@ extern "C" {
 #define SPECOPTIM_ERR_NOT_CONVERGED   4 /* SVD hit svd_max_sweeps; old factors kept   */
 #define SPECOPTIM_ERR_NOT_IMPLEMENTED 5
 #define SPECOPTIM_ERR_TIMEOUT         6 /* a bounded device-side wait gave up         */
-#define SPECOPTIM_ERR_BOUNDS          7 /* an index check failed (checked build only) */
+#define SPECOPTIM_ERR_BOUNDS          7 /* a token id or target outside the vocabulary;
+                                            in the checked build also a mask index     */
 
 /* GEMM arithmetic of the projection (key design 3, projection equation) */
 #define SPECOPTIM_PREC_TF32 0  /* tcgen05 kind::tf32 tensor cores, fp32 accumulate */

@@ -9,7 +9,9 @@ library every call raises.
 Method: "Communication-Efficient LLM Adaptation over Decentralized GPU Meshes"
 (arXiv 2609.14339), key designs 1 (activation mask), 2 (anchor EMA) and 3
 (spectral-correction optimizer); key design 4 (PowerSGD-compressed outer
-synchronisation) is bound in the ``dpsync`` submodule.
+synchronisation) is bound in the ``dpsync`` submodule, the operators of the
+pipeline's end stages (embedding, residual norm with an 8-bit checkpoint,
+vocabulary head's loss) in the ``stage_ends`` submodule.
 """
 from __future__ import annotations
 
@@ -24,7 +26,7 @@ OK, ERR_INVALID_ARG, ERR_MISALIGNED, ERR_CUDA, ERR_NOT_CONVERGED, ERR_NOT_IMPLEM
 PREC_TF32, PREC_FP32 = 0, 1
 
 _STATUS = {1: "invalid argument", 2: "misaligned pointer", 3: "CUDA error", 4: "SVD not converged",
-           5: "not implemented", 6: "device-side wait timed out", 7: "index check failed (checked build)"}
+           5: "not implemented", 6: "device-side wait timed out", 7: "index check failed"}
 
 
 class SpecOptimError(RuntimeError):
@@ -50,7 +52,7 @@ class DPConfig(ctypes.Structure):
 
 
 # (name, restype, argtypes) of every exported entry point of include/specoptim.h,
-# include/mask_fused.h and include/dpsync.h
+# include/mask_fused.h, include/dpsync.h and include/stage_ends.h
 _vp, _i32, _i64, _u32, _u64, _f32, _f64 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                            ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float,
                                            ctypes.c_double)
@@ -99,6 +101,18 @@ SIGNATURES = [
     ("dpsync_decompress_many", _int, [ctypes.POINTER(_vp), _i32, ctypes.POINTER(_vp), _f32, _vp]),
     ("dpsync_outer_step_many", _int, [ctypes.POINTER(_vp), _i32, ctypes.POINTER(_vp), _f32, _vp]),
     ("dpsync_get_state", _int, [_vp, _vp, _vp, _vp, _vp, _vp]),
+    ("embed_lookup", _int, [_vp, _i32, _vp, _i32, _i64, _i64, _i32, _f32, _vp, _i32, _vp]),
+    ("embed_grad_workspace", _i64, [_i64, _i64, _i32]),
+    ("embed_grad", _int, [_vp, _i32, _vp, _i32, _i64, _i64, _i32, _i64, _f32, _vp, _i32, _i32, _vp, _i64, _vp]),
+    ("resnorm_forward", _int, [_vp, _vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _vp]),
+    ("resnorm_recompute", _int, [_vp, _vp, _vp, _vp, _i32, _vp, _i64, _i32, _vp]),
+    ("resnorm_backward_workspace", _i64, [_i64, _i32]),
+    ("resnorm_backward", _int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _i64, _vp]),
+    ("head_loss_workspace", _i64, [_i64, _i64, _i32]),
+    ("head_loss", _int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp]),
+    ("head_loss_grad_workspace", _i64, [_i64, _i64, _i32]),
+    ("head_loss_grad", _int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _i32, _i32,
+                              _vp, _i64, _vp]),
 ]
 
 _lib = None

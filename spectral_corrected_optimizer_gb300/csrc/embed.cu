@@ -1,0 +1,545 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens
+// (include/stage_ends.h): the first stage of the training pipeline.
+//
+//   out[t]  = scale * table[ids[t]]
+//   grad[v] = scale * sum over t with ids[t] = v of dy[t]
+//
+// The gradient sorts (id, token) pairs with a stable radix sort (9 bits a
+// pass), cuts the sorted list into chunks of equal length and gives each chunk
+// to one block, whatever the ids' distribution: a block sums runs of equal ids
+// in registers, in token order; a run that lies in one chunk goes straight to
+// its row, one that crosses chunks leaves fp32 partial sums that a last kernel
+// adds in chunk order.  So a frequent token costs as much as rare ones and the
+// result does not depend on timing.  Rows without a token are zero-filled by
+// further blocks of the same launch.
+#include <algorithm>
+#include <string>
+
+#include "rowvec.cuh"
+
+namespace spco {
+namespace {
+
+// ---- lookup ----------------------------------------------------------------------
+
+// A block takes U tokens at a time: their ids first, then U independent row
+// loads per thread, so a gather of 65536 rows keeps U x 16 or 32 bytes per
+// thread in flight.
+template <typename TI, typename TO, typename ID, bool VEC, int U>
+__global__ void __launch_bounds__(256) lookup_kernel(const TI *__restrict__ table, const ID *__restrict__ ids,
+                                                     int64_t tokens, int64_t vocab, int dim, float scale,
+                                                     TO *__restrict__ out, unsigned *flag) {
+    const int vecs = (dim + 7) / 8;
+    for (int64_t t0 = (int64_t)blockIdx.x * U; t0 < tokens; t0 += (int64_t)gridDim.x * U) {
+        int64_t id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            id[u] = t0 + u < tokens ? (int64_t)ids[t0 + u] : -1;
+            if (t0 + u < tokens && (id[u] < 0 || id[u] >= vocab)) {
+                if (threadIdx.x == 0) atomicExch(flag, kSiteTokenId);
+                id[u] = -1;
+            }
+        }
+        for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+            const int n = dim - v * 8;
+            float x[U][8];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (id[u] >= 0) {
+                    load8<VEC>(table + id[u] * dim + v * 8, n, x[u]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t0 + u >= tokens) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[u][i] *= id[u] >= 0 ? scale : 0.f;
+                store8<VEC>(out + (t0 + u) * dim + v * 8, n, x[u]);
+            }
+        }
+    }
+}
+
+template <typename TI, typename TO, typename ID>
+void launch_lookup(const void *table, const void *ids, int64_t tokens, int64_t vocab, int dim, float scale,
+                   void *out, cudaStream_t st) {
+    const TI *tb = static_cast<const TI *>(table);
+    const ID *id = static_cast<const ID *>(ids);
+    TO *o = static_cast<TO *>(out);
+    const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim, 8), 32));
+    const bool vec = dim % 8 == 0 && aligned16(table) && aligned16(out);
+    const int64_t resident = (int64_t)num_sms() * 8;
+    // few tokens: one per block, so that every row has an SM of its own
+    if (tokens <= resident) {
+        const int grid = (int)tokens;
+        if (vec) lookup_kernel<TI, TO, ID, true, 1><<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
+        else lookup_kernel<TI, TO, ID, false, 1><<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
+    } else {
+        const int grid = (int)std::min<int64_t>(ceil_div(tokens, 4), resident * 4);
+        if (vec) lookup_kernel<TI, TO, ID, true, 4><<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
+        else lookup_kernel<TI, TO, ID, false, 4><<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
+    }
+}
+
+template <typename TI, typename TO>
+void launch_lookup(const void *table, const void *ids, int id_bytes, int64_t tokens, int64_t vocab, int dim,
+                   float scale, void *out, cudaStream_t st) {
+    if (id_bytes == 8) launch_lookup<TI, TO, int64_t>(table, ids, tokens, vocab, dim, scale, out, st);
+    else launch_lookup<TI, TO, int32_t>(table, ids, tokens, vocab, dim, scale, out, st);
+}
+
+// ---- stable radix sort of (id, token) ---------------------------------------------
+
+constexpr int kBits = 9, kBins = 1 << kBits;
+constexpr int kSortThreads = 256, kSortItems = 8, kTile = kSortThreads * kSortItems;
+constexpr int kSortWarps = kSortThreads / 32, kWarpItems = kTile / kSortWarps;
+
+// The sort key of a token: its id, or `vocab` (behind every row) for a token
+// that contributes nothing.
+template <typename ID>
+__device__ __forceinline__ uint32_t key_of(const ID *ids, int64_t t, int64_t vocab, int64_t padding, unsigned *flag) {
+    const int64_t id = (int64_t)ids[t];
+    if (id >= 0 && id < vocab) return id == padding ? (uint32_t)vocab : (uint32_t)id;
+    if (flag) atomicExch(flag, kSiteTokenId);
+    return (uint32_t)vocab;
+}
+
+// digits of one tile of kTile keys, counted into hist[block][bin]
+template <typename ID, bool FIRST>
+__global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const ID *__restrict__ ids, int64_t vocab,
+                                                                 int64_t padding, const uint32_t *__restrict__ keys,
+                                                                 int64_t n, int shift, uint32_t *__restrict__ hist,
+                                                                 unsigned *flag) {
+    __shared__ uint32_t cnt[kBins];
+    for (int b = threadIdx.x; b < kBins; b += kSortThreads) cnt[b] = 0;
+    __syncthreads();
+    const int64_t base = (int64_t)blockIdx.x * kTile;
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+        const int64_t t = base + i * kSortThreads + threadIdx.x;
+        if (t < n) {
+            const uint32_t k = FIRST ? key_of(ids, t, vocab, padding, flag) : keys[t];
+            atomicAdd(&cnt[(k >> shift) & (kBins - 1)], 1u);
+        }
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < kBins; b += kSortThreads) hist[(int64_t)blockIdx.x * kBins + b] = cnt[b];
+}
+
+// Moves one tile to its place in the order of this digit.  Each block adds up
+// the table of counts itself (a scan kernel of its own would cost a launch):
+// its bins' totals give where a bin starts, the blocks before it where its own
+// share starts.  Within the tile each warp owns consecutive keys and ranks 32
+// of them at a time by matching digits, so equal digits keep their order.
+template <typename ID, bool FIRST>
+__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(
+    const ID *__restrict__ ids, int64_t vocab, int64_t padding, const uint32_t *__restrict__ keys,
+    const uint32_t *__restrict__ vals, int64_t n, int shift, const uint32_t *__restrict__ hist, int blocks,
+    uint32_t *__restrict__ keys_out, uint32_t *__restrict__ vals_out) {
+    __shared__ uint32_t where[kSortWarps][kBins];
+    __shared__ uint32_t warp_total[kSortWarps];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    for (int b = tid; b < kSortWarps * kBins; b += kSortThreads) (&where[0][0])[b] = 0;
+    // two neighbouring bins per thread
+    uint32_t total[2] = {0, 0}, before[2] = {0, 0};
+    const uint2 *h2 = reinterpret_cast<const uint2 *>(hist);
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b) {
+        const uint2 c = h2[(int64_t)b * (kBins / 2) + tid];
+        total[0] += c.x;
+        total[1] += c.y;
+        if (b < (int)blockIdx.x) {
+            before[0] += c.x;
+            before[1] += c.y;
+        }
+    }
+    __syncthreads();
+    // per-warp counts of the tile's digits
+    const int64_t base = (int64_t)blockIdx.x * kTile + w * kWarpItems;
+    uint32_t key[kWarpItems / 32];
+#pragma unroll
+    for (int i = 0; i < kWarpItems / 32; ++i) {
+        const int64_t t = base + i * 32 + lane;
+        key[i] = t < n ? (FIRST ? key_of(ids, t, vocab, padding, (unsigned *)nullptr) : keys[t]) : 0u;
+        if (t < n) atomicAdd(&where[w][(key[i] >> shift) & (kBins - 1)], 1u);
+    }
+    // exclusive sum of the bins' totals over the block
+    const uint32_t mine = total[0] + total[1];
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_total[w] = incl;
+    __syncthreads();
+    uint32_t start = incl - mine;
+    for (int i = 0; i < w; ++i) start += warp_total[i];
+    // where[w][bin] = first position of this warp's keys of the bin
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int b = 2 * tid + j;
+        uint32_t at = start + (j ? total[0] : 0u) + before[j];
+        for (int i = 0; i < kSortWarps; ++i) {
+            const uint32_t c = where[i][b];
+            where[i][b] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarpItems / 32; ++i) {
+        const int64_t t = base + i * 32 + lane;
+        const bool in = t < n;
+        const uint32_t d = in ? (key[i] >> shift) & (kBins - 1) : kBins;  // kBins: no key
+        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        if (in) {
+            const uint32_t rank = __popc(peers & ((1u << lane) - 1u));
+            const uint32_t to = where[w][d] + rank;
+            keys_out[to] = key[i];
+            vals_out[to] = FIRST ? (uint32_t)t : vals[t];
+        }
+        __syncwarp();
+        if (in && (peers >> lane) == 1u) where[w][d] += __popc(peers);  // the last of the peers
+        __syncwarp();
+    }
+}
+
+// ---- segmented sums ----------------------------------------------------------------
+
+struct Sorted {
+    const uint32_t *keys, *vals;
+    int64_t n;
+    int chunk;
+    int64_t chunks;
+};
+
+template <typename TG, bool VEC>
+__device__ __forceinline__ void put_row(TG *grad, int64_t row, int dim, int col, float scale, bool accumulate,
+                                        float (&a)[8]) {
+    TG *p = grad + row * dim + col;
+    const int n = dim - col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] *= scale;
+    if (accumulate) {
+        float old[8];
+        if (VEC) {  // not through the read-only path: this kernel writes these rows
+            const volatile uint32_t *u = reinterpret_cast<const volatile uint32_t *>(p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (sizeof(TG) == 4) old[i] = __uint_as_float(u[i]);
+                else old[i] = (i & 1) ? hi_f(u[i / 2]) : lo_f(u[i / 2]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) old[i] = i < n ? to_f(p[i]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] += old[i];
+    }
+    store8<VEC>(p, n, a);
+}
+
+constexpr int kMaxChunk = 64, kBatch = 8, kZeroRows = 64;
+
+// Blocks [0, chunks * col_blocks): one chunk of the sorted list, 8 columns per
+// thread.  Blocks after them: kZeroRows rows each, zero-filled where the list
+// has no such id.  partial: [chunks][2][dim], slot 0 for a run that began
+// before the chunk, slot 1 for one that begins in it and goes on.
+template <typename TD, typename TG, bool VEC>
+__global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const TD *__restrict__ dy, int64_t vocab,
+                                                          int dim, int col_blocks, float scale, bool accumulate,
+                                                          TG *__restrict__ grad, float *__restrict__ partial) {
+    __shared__ uint32_t sk[kMaxChunk + 2], sv[kMaxChunk];
+    const int tid = threadIdx.x;
+    const int64_t work = s.chunks * col_blocks;
+    if ((int64_t)blockIdx.x >= work) {
+        __shared__ uint8_t present[kZeroRows];
+        const int64_t row0 = ((int64_t)blockIdx.x - work) * kZeroRows;
+        for (int i = tid; i < kZeroRows; i += blockDim.x) {
+            const int64_t row = row0 + i;
+            int64_t lo = 0, hi = s.n;  // first position with key >= row
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) >> 1;
+                if ((int64_t)s.keys[mid] < row) lo = mid + 1;
+                else hi = mid;
+            }
+            present[i] = row >= vocab || (lo < s.n && (int64_t)s.keys[lo] == row);
+        }
+        __syncthreads();
+        const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < kZeroRows; ++i) {
+            if (present[i]) continue;
+            for (int col = tid * 8; col < dim; col += blockDim.x * 8)
+                store8<VEC>(grad + (row0 + i) * dim + col, dim - col, zero);
+        }
+        return;
+    }
+    const int64_t c = (int64_t)blockIdx.x / col_blocks;
+    const int col = ((int)((int64_t)blockIdx.x % col_blocks) * (int)blockDim.x + tid) * 8;
+    const int64_t p0 = c * s.chunk;
+    const int len = (int)(s.n - p0 < s.chunk ? s.n - p0 : s.chunk);
+    // keys of the chunk and of its two neighbours (~0: none)
+    for (int i = tid; i < len + 2; i += blockDim.x) {
+        const int64_t p = p0 + i - 1;
+        sk[i] = p >= 0 && p < s.n ? s.keys[p] : ~0u;
+    }
+    for (int i = tid; i < len; i += blockDim.x) sv[i] = s.vals[p0 + i];
+    __syncthreads();
+    if (col >= dim) return;
+    const int n = dim - col;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    bool began = sk[0] != sk[1];  // whether the current run begins in this chunk
+    for (int i0 = 0; i0 < len; i0 += kBatch) {
+        float x[kBatch][8];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (i0 + u < len) load8<VEC>(dy + (int64_t)sv[i0 + u] * dim + col, n, x[u]);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u;
+            if (i >= len) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += x[u][j];
+            const uint32_t k = sk[i + 1], next = sk[i + 2];
+            const bool run_ends = next != k;
+            if (!run_ends && i + 1 < len) continue;
+            if ((int64_t)k < vocab) {
+                if (began && run_ends) {
+                    put_row<TG, VEC>(grad, k, dim, col, scale, accumulate, acc);
+                } else {
+                    float *slot = partial + (c * 2 + (began ? 1 : 0)) * dim + col;
+                    store8<VEC>(slot, n, acc);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+            began = true;
+        }
+    }
+}
+
+// One block per chunk and column block: if a run begins in the chunk and goes
+// on, its partial sums are added in chunk order and written to its row.
+template <typename TG, bool VEC>
+__global__ void __launch_bounds__(256) segment_join_kernel(const Sorted s, int64_t vocab, int dim, float scale,
+                                                           bool accumulate, TG *__restrict__ grad,
+                                                           const float *__restrict__ partial) {
+    const int64_t c = blockIdx.x;
+    const int64_t p0 = c * s.chunk, p1 = p0 + s.chunk;
+    if (p1 >= s.n) return;
+    const uint32_t k = s.keys[p1 - 1];
+    if ((int64_t)k >= vocab || s.keys[p1] != k) return;
+    if (s.keys[p0] == k && p0 > 0 && s.keys[p0 - 1] == k) return;  // the run began earlier
+    const int col = ((int)blockIdx.y * (int)blockDim.x + threadIdx.x) * 8;
+    if (col >= dim) return;
+    int64_t lo = p1, hi = s.n;  // first position behind the run
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (s.keys[mid] <= k) lo = mid + 1;
+        else hi = mid;
+    }
+    const int64_t last = (lo - 1) / s.chunk;  // chunk of the run's last token
+    const int n = dim - col;
+    float acc[8];
+    load8<VEC>(partial + (c * 2 + 1) * dim + col, n, acc);
+#pragma unroll 4
+    for (int64_t i = c + 1; i <= last; ++i) {
+        float x[8];
+        load8<VEC>(partial + i * 2 * dim + col, n, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += x[j];
+    }
+    put_row<TG, VEC>(grad, k, dim, col, scale, accumulate, acc);
+}
+
+// Tokens per chunk: as many blocks as fill the GPU four times over, between 8
+// tokens (a shorter chunk would leave more partial sums than it saves) and 64.
+int chunk_len(int64_t tokens, int col_blocks) {
+    const int64_t want = tokens * col_blocks / ((int64_t)num_sms() * 4);
+    int len = 8;
+    while (len < kMaxChunk && len < want) len *= 2;
+    return len;
+}
+
+struct GradPlan {
+    int threads, col_blocks, chunk, passes;
+    int64_t chunks, sort_blocks;
+    int64_t off_hist, off_k0, off_v0, off_k1, off_v1, off_partial, bytes;
+};
+
+GradPlan plan_grad(int64_t tokens, int64_t vocab, int32_t dim) {
+    GradPlan p{};
+    p.threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim, 8), 32));
+    p.col_blocks = (int)ceil_div(dim, (int64_t)p.threads * 8);
+    p.chunk = chunk_len(tokens, p.col_blocks);
+    p.chunks = ceil_div(tokens, p.chunk);
+    p.sort_blocks = ceil_div(tokens, kTile);
+    int bits = 1;
+    while ((vocab >> bits) > 0) ++bits;  // keys run up to `vocab` itself
+    p.passes = (bits + kBits - 1) / kBits;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    p.off_hist = take(p.sort_blocks * kBins * 4);
+    p.off_k0 = take(tokens * 4);
+    p.off_v0 = take(tokens * 4);
+    p.off_k1 = take(tokens * 4);
+    p.off_v1 = take(tokens * 4);
+    p.off_partial = take(p.chunks * 2 * dim * 4);
+    p.bytes = at;
+    return p;
+}
+
+template <typename ID>
+int sort_tokens(const GradPlan &p, const ID *ids, int64_t tokens, int64_t vocab, int64_t padding, char *ws,
+                cudaStream_t st, Sorted *out) {
+    uint32_t *hist = reinterpret_cast<uint32_t *>(ws + p.off_hist);
+    uint32_t *k[2] = {reinterpret_cast<uint32_t *>(ws + p.off_k0), reinterpret_cast<uint32_t *>(ws + p.off_k1)};
+    uint32_t *v[2] = {reinterpret_cast<uint32_t *>(ws + p.off_v0), reinterpret_cast<uint32_t *>(ws + p.off_v1)};
+    const int blocks = (int)p.sort_blocks;
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * kBits, to = pass & 1, from = to ^ 1;
+        if (pass == 0) {
+            SPCO_LAUNCH("embed_sort_hist", st, sort_hist_kernel<ID, true><<<blocks, kSortThreads, 0, st>>>(
+                                                   ids, vocab, padding, nullptr, tokens, shift, hist, device_flag_ptr()));
+            SPCO_LAUNCH("embed_sort_scatter", st,
+                        sort_scatter_kernel<ID, true><<<blocks, kSortThreads, 0, st>>>(
+                            ids, vocab, padding, nullptr, nullptr, tokens, shift, hist, blocks, k[to], v[to]));
+        } else {
+            SPCO_LAUNCH("embed_sort_hist", st, sort_hist_kernel<ID, false><<<blocks, kSortThreads, 0, st>>>(
+                                                   nullptr, vocab, padding, k[from], tokens, shift, hist, nullptr));
+            SPCO_LAUNCH("embed_sort_scatter", st,
+                        sort_scatter_kernel<ID, false><<<blocks, kSortThreads, 0, st>>>(
+                            nullptr, vocab, padding, k[from], v[from], tokens, shift, hist, blocks, k[to], v[to]));
+        }
+        out->keys = k[to];
+        out->vals = v[to];
+    }
+    SPECOPTIM_LAUNCHED("embed_grad sort");
+    out->n = tokens;
+    out->chunk = p.chunk;
+    out->chunks = p.chunks;
+    return SPECOPTIM_OK;
+}
+
+template <typename TD, typename TG, bool VEC>
+int sum_segments(const GradPlan &p, const Sorted &s, const void *dy, int64_t vocab, int dim, float scale,
+                 bool accumulate, void *grad, float *partial, cudaStream_t st) {
+    const int64_t work = s.chunks * p.col_blocks + (accumulate ? 0 : ceil_div(vocab, kZeroRows));
+    if (work > INT32_MAX) return fail(SPECOPTIM_ERR_NOT_IMPLEMENTED, "embed_grad: tokens x dim too large for one launch");
+    if (work > 0)
+        SPCO_LAUNCH("embed_segment_sum", st,
+                    segment_sum_kernel<TD, TG, VEC><<<(unsigned)work, p.threads, 0, st>>>(
+                        s, static_cast<const TD *>(dy), vocab, dim, p.col_blocks, scale, accumulate,
+                        static_cast<TG *>(grad), partial));
+    if (s.chunks > 1)
+        SPCO_LAUNCH("embed_segment_join", st,
+                    segment_join_kernel<TG, VEC><<<dim3((unsigned)s.chunks, p.col_blocks), p.threads, 0, st>>>(
+                        s, vocab, dim, scale, accumulate, static_cast<TG *>(grad), partial));
+    SPECOPTIM_LAUNCHED("embed_grad sums");
+    return SPECOPTIM_OK;
+}
+
+int check_sizes(int64_t tokens, int64_t vocab, int32_t dim, const char *what) {
+    if (tokens < 0 || tokens > (int64_t)1 << 30)
+        return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": tokens outside [0, 2^30]");
+    if (vocab < 1 || vocab > (int64_t)1 << 30)
+        return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": vocab outside [1, 2^30]");
+    if (dim < 1 || dim > 1 << 20) return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": dim outside [1, 2^20]");
+    return SPECOPTIM_OK;
+}
+
+}  // namespace
+}  // namespace spco
+
+using namespace spco;
+
+extern "C" int embed_lookup(const void *table, int32_t table_type, const void *ids, int32_t id_bytes, int64_t tokens,
+                            int64_t vocab, int32_t dim, float scale, void *out, int32_t out_type, void *stream) {
+    return entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "embed_lookup")) return rc;
+        if (!type_ok(table_type) || !type_ok(out_type))
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_lookup: types must be STAGE_BF16 or STAGE_FP32");
+        if (id_bytes != 4 && id_bytes != 8)
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_lookup: id_bytes must be 4 or 8");
+        if (tokens == 0) return SPECOPTIM_OK;
+        if (!table || !ids || !out) return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_lookup: null pointer");
+        if (!aligned_to(table, type_bytes(table_type)) || !aligned_to(out, type_bytes(out_type)) ||
+            !aligned_to(ids, id_bytes))
+            return fail(SPECOPTIM_ERR_MISALIGNED, "embed_lookup: pointers must be aligned to their elements");
+        if (int rc = bind_device()) return rc;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        SPCO_LAUNCH("embed_lookup", st, {
+            if (table_type == STAGE_BF16 && out_type == STAGE_BF16)
+                launch_lookup<bf16, bf16>(table, ids, id_bytes, tokens, vocab, dim, scale, out, st);
+            else if (table_type == STAGE_BF16)
+                launch_lookup<bf16, float>(table, ids, id_bytes, tokens, vocab, dim, scale, out, st);
+            else if (out_type == STAGE_BF16)
+                launch_lookup<float, bf16>(table, ids, id_bytes, tokens, vocab, dim, scale, out, st);
+            else
+                launch_lookup<float, float>(table, ids, id_bytes, tokens, vocab, dim, scale, out, st);
+        });
+        SPECOPTIM_LAUNCHED("lookup_kernel");
+        return SPECOPTIM_OK;
+    });
+}
+
+extern "C" int64_t embed_grad_workspace(int64_t tokens, int64_t vocab, int32_t dim) {
+    int64_t bytes = -1;
+    entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "embed_grad")) return rc;
+        bytes = plan_grad(tokens, vocab, dim).bytes;
+        return SPECOPTIM_OK;
+    });
+    return bytes;
+}
+
+extern "C" int embed_grad(const void *ids, int32_t id_bytes, const void *dy, int32_t dy_type, int64_t tokens,
+                          int64_t vocab, int32_t dim, int64_t padding_idx, float scale, void *grad,
+                          int32_t grad_type, int32_t accumulate, void *workspace, int64_t workspace_bytes,
+                          void *stream) {
+    return entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "embed_grad")) return rc;
+        if (!type_ok(dy_type) || !type_ok(grad_type))
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_grad: types must be STAGE_BF16 or STAGE_FP32");
+        if (id_bytes != 4 && id_bytes != 8)
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_grad: id_bytes must be 4 or 8");
+        if (padding_idx < -1 || padding_idx >= vocab)
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_grad: padding_idx outside [-1, vocab)");
+        if (!grad || (tokens > 0 && (!ids || !dy)))
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_grad: null pointer");
+        if (!aligned_to(dy, type_bytes(dy_type)) || !aligned_to(grad, type_bytes(grad_type)) ||
+            !aligned_to(ids, id_bytes) || !aligned16(workspace))
+            return fail(SPECOPTIM_ERR_MISALIGNED, "embed_grad: pointers must be aligned to their elements, the workspace to 16 bytes");
+        const GradPlan p = plan_grad(tokens, vocab, dim);
+        if (tokens > 0 && (!workspace || workspace_bytes < p.bytes))
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_grad: the workspace is smaller than embed_grad_workspace() says");
+        if (int rc = bind_device()) return rc;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        char *ws = static_cast<char *>(workspace);
+        Sorted s{nullptr, nullptr, 0, p.chunk, 0};
+        if (tokens > 0) {
+            const int rc = id_bytes == 8 ? sort_tokens(p, static_cast<const int64_t *>(ids), tokens, vocab, padding_idx, ws, st, &s)
+                                         : sort_tokens(p, static_cast<const int32_t *>(ids), tokens, vocab, padding_idx, ws, st, &s);
+            if (rc) return rc;
+        }
+        float *partial = reinterpret_cast<float *>(ws + p.off_partial);
+        const bool vec = dim % 8 == 0 && aligned16(dy) && aligned16(grad);
+        const bool acc = accumulate != 0;
+        auto go = [&](auto td, auto tg) -> int {
+            using TD = decltype(td);
+            using TG = decltype(tg);
+            return vec ? sum_segments<TD, TG, true>(p, s, dy, vocab, dim, scale, acc, grad, partial, st)
+                       : sum_segments<TD, TG, false>(p, s, dy, vocab, dim, scale, acc, grad, partial, st);
+        };
+        if (dy_type == STAGE_BF16) return grad_type == STAGE_BF16 ? go(bf16{}, bf16{}) : go(bf16{}, float{});
+        return grad_type == STAGE_BF16 ? go(float{}, bf16{}) : go(float{}, float{});
+    });
+}

@@ -1,0 +1,466 @@
+// Softmax cross entropy of the vocabulary head and its gradients
+// (include/stage_ends.h): the last stage of the training pipeline.
+//
+//   l_i = h_i W^T,  row_loss_i = log sum_v exp(l_iv) - l_i,target,
+//   d = (softmax(l) - onehot) * factor,  dh = d W,  dW = d^T h
+//
+// Order of the work (N tokens with a target, V rows of W, width D):
+//   1. the tokens that have a target are counted and listed, their rows of h
+//      copied together: a token without one costs nothing afterwards;
+//   2. one product over the whole vocabulary leaves the maximum and the sum of
+//      exponentials of each row and 128 logits; they are joined into the row's
+//      loss and normalisation (2 N V D flops);
+//   3. for each piece of the vocabulary, logits are formed again and turned
+//      into softmax - onehot of the piece (bf16, 2 N V D flops), which feeds
+//      the two gradient products (4 N V D).  A launch runs piece i's
+//      probabilities beside piece i-1's products, so two piece buffers exist
+//      and no [N][V] tensor does.  dh sums up in fp32 over the pieces.
+// The products are in head_gemm.cu.
+#include <algorithm>
+#include <cstring>
+#include <string>
+
+#include "head_gemm.cuh"
+
+namespace spco {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ---- the rows that have a target ---------------------------------------------------------
+
+// One block: lists the tokens with a target in token order.  row_of[r] = token
+// of row r, at[t] = row of token t (-1: none), target[r].
+template <typename ID>
+__global__ void __launch_bounds__(1024) head_rows_kernel(const ID *__restrict__ targets, int64_t ignore, int tokens,
+                                                         int vocab, int mean, HeadState *state, int *__restrict__ row_of,
+                                                         int *__restrict__ at, int *__restrict__ target,
+                                                         float *__restrict__ row_loss, unsigned *flag) {
+    __shared__ int warp_count[32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int rows = 0;
+    for (int t0 = 0; t0 < tokens; t0 += 1024) {
+        const int t = t0 + threadIdx.x;
+        const int64_t y = t < tokens ? (int64_t)targets[t] : ignore;
+        const bool inside = y >= 0 && y < vocab;
+        if (y != ignore && !inside) atomicExch(flag, kSiteTarget);
+        const bool has = y != ignore && inside;
+        const unsigned ballot = __ballot_sync(0xffffffffu, has);
+        __syncthreads();  // the previous step's counts have been read
+        if (lane == 0) warp_count[w] = __popc(ballot);
+        __syncthreads();
+        int before = rows;
+        for (int i = 0; i < 32; ++i) {
+            const int c = warp_count[i];
+            if (i < w) before += c;
+            rows += c;
+        }
+        if (t < tokens) {
+            const int r = before + __popc(ballot & ((1u << lane) - 1u));
+            at[t] = has ? r : -1;
+            if (has) {
+                row_of[r] = t;
+                target[r] = (int)y;
+            } else {
+                row_loss[t] = 0.f;
+            }
+        }
+    }
+    if (threadIdx.x == 0) {
+        state->rows = rows;
+        state->blocks_done = 0;
+        state->inv_count = mean ? 1.f / (float)max(rows, 1) : 1.f;
+    }
+}
+
+// 8 bf16 values of a row from column 8 v, zero behind dim
+__device__ __forceinline__ uint4 row_vec(const uint16_t *row, int v, int dim, bool vec) {
+    if (vec) return __ldg(reinterpret_cast<const uint4 *>(row) + v);
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = v * 8 + i < dim ? row[v * 8 + i] : 0u;
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float s) {
+    return fmaf(hi_f(a), hi_f(b), fmaf(lo_f(a), lo_f(b), s));
+}
+
+// Copies the listed rows of h together, ld values each (a multiple of 8, zero
+// behind dim), zero rows up to the next multiple of the tile height.  On the
+// way the logit of each row's target is formed as an fp32 dot product: the
+// loss is the difference between it and the log-sum-exp, and the tensor cores'
+// long accumulation (dim / 16 steps, each cut off rather than rounded) leaves a
+// large logit 2^-24 dim / 32 of itself short.
+__global__ void __launch_bounds__(256) head_gather_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ w,
+                                                          const int *__restrict__ row_of, const int *__restrict__ target,
+                                                          const HeadState *__restrict__ state, int dim, int ld,
+                                                          int h_vec, int w_vec, uint16_t *__restrict__ out,
+                                                          float *__restrict__ target_logit) {
+    __shared__ float red[2][8];
+    const int rows = state->rows, end = (rows + kHeadTileM - 1) / kHeadTileM * kHeadTileM;
+    int parity = 0;
+    for (int r = blockIdx.x; r < end; r += gridDim.x, parity ^= 1) {
+        uint4 *d = reinterpret_cast<uint4 *>(out + (int64_t)r * ld);
+        if (r >= rows) {
+            for (int v = threadIdx.x; v < ld / 8; v += blockDim.x) d[v] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint16_t *hr = h + (int64_t)row_of[r] * dim, *wr = w + (int64_t)target[r] * dim;
+        float s = 0.f;
+        for (int v = threadIdx.x; v < ld / 8; v += blockDim.x) {
+            const uint4 a = row_vec(hr, v, dim, h_vec), b = row_vec(wr, v, dim, w_vec);
+            s += dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, 0.f))));
+            d[v] = a;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if ((threadIdx.x & 31) == 0) red[parity][threadIdx.x >> 5] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 1; i < (int)blockDim.x / 32; ++i) s += red[parity][i];
+            target_logit[r] = s;
+        }
+    }
+}
+
+// Rows of W with ld values each: the tensor copies need rows of 16-byte multiples.
+__global__ void __launch_bounds__(256) head_pad_kernel(const uint16_t *__restrict__ src, int64_t rows, int dim, int ld,
+                                                       uint16_t *__restrict__ dst) {
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int v = threadIdx.x; v < ld / 8; v += blockDim.x)
+            reinterpret_cast<uint4 *>(dst + r * ld)[v] = row_vec(src + r * dim, v, dim, false);
+}
+
+// ---- joining the row statistics ------------------------------------------------------------
+
+// 32 rows per block, 8 threads per row: each joins every eighth part, then the
+// eight are joined in order.  The parts' sums leave the target out: S of them
+// gives softmax - 1 = -S / (S + e_target) and the loss log(1 + S / e_target)
+// without the cancellation that a well-predicted token (S small) would meet in
+// 1 - p and in lse - l.  The last block to finish adds up the blocks' loss
+// sums, in block order.
+__global__ void __launch_bounds__(256) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
+                                                       const float *__restrict__ target_logit,
+                                                       const int *__restrict__ row_of, HeadState *state,
+                                                       float4 *__restrict__ norm, float *__restrict__ row_loss,
+                                                       float *__restrict__ block_loss, float *__restrict__ loss) {
+    __shared__ float sm[8][33], ss[8][33];
+    __shared__ bool last;
+    const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int rows = state->rows, row = blockIdx.x * 32 + c;
+    float m = -INFINITY, s = 0.f;
+    if (row < rows) {
+#pragma unroll 8
+        for (int p = w; p < parts; p += 8) {
+            const float2 x = stats[(int64_t)p * row_cap + row];
+            const float top = fmaxf(m, x.x), ref = top == -INFINITY ? 0.f : top;
+            s = s * exp2f((m - ref) * kLog2e) + x.y * exp2f((x.x - ref) * kLog2e);
+            m = top;
+        }
+    }
+    sm[w][c] = m;
+    ss[w][c] = s;
+    __syncthreads();
+    if (w == 0) {
+        for (int i = 1; i < 8; ++i) {
+            const float top = fmaxf(m, sm[i][c]), ref = top == -INFINITY ? 0.f : top;
+            s = s * exp2f((m - ref) * kLog2e) + ss[i][c] * exp2f((sm[i][c] - ref) * kLog2e);
+            m = top;
+        }
+        float l = 0.f;
+        if (row < rows) {
+            const float lt = target_logit[row], above = m - lt;
+            const float total = s + expf(-above);
+            norm[row] = make_float4(m, 1.f / total, -s / total, 0.f);
+            // exp(20) S stays far from overflow; beyond it log(total) is no longer a small correction
+            l = above < 20.f ? log1pf(s * expf(above)) : above + logf(total);
+            row_loss[row_of[row]] = l;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (c == 0) {
+            block_loss[blockIdx.x] = l;
+            __threadfence();
+            last = atomicAdd(&state->blocks_done, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!last || w != 0) return;
+    __threadfence();
+    float l = 0.f;
+    for (int b = c; b < (int)gridDim.x; b += 32) l += __ldcg(block_loss + b);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (c == 0) *loss = l * state->inv_count;
+}
+
+// dh[t] = factor * sum over the parts of the token's row; zero without a target
+template <bool VEC>
+__global__ void __launch_bounds__(256) head_dh_kernel(const float *__restrict__ sums, int parts, int row_cap, int ld,
+                                                      const int *__restrict__ at, const HeadState *__restrict__ state,
+                                                      float grad_scale, int tokens, int dim, bf16 *__restrict__ dh) {
+    const float factor = grad_scale * state->inv_count;
+    for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
+        const int r = at[t];
+        for (int col = threadIdx.x * 8; col < dim; col += blockDim.x * 8) {
+            float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (r >= 0) {
+#pragma unroll 4
+                for (int p = 0; p < parts; ++p) {
+                    float x[8];
+                    load8<true>(sums + ((int64_t)p * row_cap + r) * ld + col, 8, x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) a[i] += x[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] *= factor;
+            }
+            store8<VEC>(dh + (int64_t)t * dim + col, dim - col, a);
+        }
+    }
+}
+
+// ---- plan ------------------------------------------------------------------------------------
+
+// Bytes of one piece buffer: about the L2, so that a piece is read back from
+// there while it is in use; but at least 4096 vocabulary rows, so that adding
+// up dh stays small beside the products.
+constexpr int64_t kPieceBytes = 128 << 20;
+constexpr int kPieceMin = 4096;
+
+struct HeadPlan {
+    int row_cap, ld, parts, piece, pieces, splits, dh_ld;
+    int64_t off_state, off_row_of, off_at, off_target, off_tlogit, off_norm, off_block_loss, off_stats, off_h, off_w,
+        off_p0, off_p1, off_dh, bytes;
+};
+
+HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
+    HeadPlan p{};
+    p.row_cap = (int)round_up(std::max<int64_t>(tokens, 1), kHeadTileM);
+    p.ld = (int)round_up(dim, 8);
+    p.parts = (int)(2 * ceil_div(vocab, kHeadTileN));
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += round_up(bytes, 1024);
+        return here;
+    };
+    const int64_t cap = p.row_cap;
+    p.off_state = take(sizeof(HeadState));
+    p.off_row_of = take(cap * 4);
+    p.off_at = take(cap * 4);
+    p.off_target = take(cap * 4);
+    p.off_tlogit = take(cap * 4);
+    p.off_norm = take(cap * 16);
+    p.off_block_loss = take(ceil_div(cap, 32) * 4);
+    p.off_stats = take((int64_t)p.parts * cap * 8);
+    p.off_h = take(cap * p.ld * 2);
+    p.off_w = p.ld != dim ? take(vocab * p.ld * 2) : 0;
+    if (grad) {
+        const int64_t all = round_up(vocab, kHeadTileN);
+        const int64_t fit = kPieceBytes / (cap * 2) / kHeadTileN * kHeadTileN;
+        p.piece = (int)std::min(all, std::max<int64_t>(fit, kPieceMin));
+        p.pieces = (int)ceil_div(vocab, p.piece);
+        // few rows: the long sum over the vocabulary is split until the GPU has a tile per SM
+        p.dh_ld = (int)round_up(dim, 32);
+        const int64_t tiles = (cap / kHeadTileM) * ceil_div(dim, kHeadTileN);
+        const int64_t blocks = ceil_div(std::min<int64_t>(vocab, p.piece), 64);
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / tiles, blocks / 8));
+        p.off_p0 = take(cap * p.piece * 2);
+        p.off_p1 = p.pieces > 1 ? take(cap * p.piece * 2) : p.off_p0;
+        p.off_dh = take((int64_t)p.splits * cap * p.dh_ld * 4);
+    }
+    p.bytes = at;
+    return p;
+}
+
+int check_sizes(int64_t tokens, int64_t vocab, int32_t dim, const char *what) {
+    if (tokens < 0 || tokens > (int64_t)1 << 24)
+        return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": tokens outside [0, 2^24]");
+    if (vocab < 1 || vocab > (int64_t)1 << 24)
+        return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": vocab outside [1, 2^24]");
+    if (dim < 1 || dim > 1 << 16) return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": dim outside [1, 65536]");
+    return SPECOPTIM_OK;
+}
+
+struct HeadCall {
+    const void *h, *w, *targets;
+    int32_t id_bytes;
+    int64_t ignore, tokens, vocab;
+    int32_t dim, mean;
+    float *loss, *row_loss;
+    char *ws;
+    int64_t ws_bytes;
+    cudaStream_t st;
+};
+
+int check_call(const HeadCall &c, const HeadPlan &p, const std::string &what) {
+    if (c.id_bytes != 4 && c.id_bytes != 8) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": id_bytes must be 4 or 8");
+    if (!c.w || !c.loss || !c.ws || (c.tokens > 0 && (!c.h || !c.targets || !c.row_loss)))
+        return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": null pointer");
+    if (!aligned_to(c.h, 2) || !aligned_to(c.targets, c.id_bytes) || !aligned_to(c.loss, 4) ||
+        !aligned_to(c.row_loss, 4) || !aligned16(c.w) || !aligned16(c.ws))
+        return fail(SPECOPTIM_ERR_MISALIGNED, what + ": w and the workspace must be 16-byte aligned, the rest to its elements");
+    if (c.ws_bytes < p.bytes)
+        return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": the workspace is smaller than " + what + "_workspace() says");
+    return SPECOPTIM_OK;
+}
+
+// Steps 1 and 2: afterwards loss, row_loss and the rows' norms exist.
+int run_loss(const HeadCall &c, const HeadPlan &p, HeadGemm *g) {
+    std::memset(g, 0, sizeof(*g));
+    HeadState *state = reinterpret_cast<HeadState *>(c.ws + p.off_state);
+    int *row_of = reinterpret_cast<int *>(c.ws + p.off_row_of), *at = reinterpret_cast<int *>(c.ws + p.off_at);
+    int *target = reinterpret_cast<int *>(c.ws + p.off_target);
+    float *tlogit = reinterpret_cast<float *>(c.ws + p.off_tlogit);
+    float4 *norm = reinterpret_cast<float4 *>(c.ws + p.off_norm);
+    uint16_t *hc = reinterpret_cast<uint16_t *>(c.ws + p.off_h);
+    const uint16_t *w = static_cast<const uint16_t *>(c.w);
+    const int tokens = (int)c.tokens, vocab = (int)c.vocab;
+    if (c.id_bytes == 8)
+        SPCO_LAUNCH("head_rows", c.st,
+                    head_rows_kernel<<<1, 1024, 0, c.st>>>(static_cast<const int64_t *>(c.targets), c.ignore, tokens,
+                                                           vocab, c.mean, state, row_of, at, target, c.row_loss,
+                                                           device_flag_ptr()));
+    else
+        SPCO_LAUNCH("head_rows", c.st,
+                    head_rows_kernel<<<1, 1024, 0, c.st>>>(static_cast<const int32_t *>(c.targets), c.ignore, tokens,
+                                                           vocab, c.mean, state, row_of, at, target, c.row_loss,
+                                                           device_flag_ptr()));
+    const int copy_threads = (int)std::min<int64_t>(256, round_up(p.ld / 8, 32));
+    SPCO_LAUNCH("head_gather", c.st,
+                head_gather_kernel<<<std::min(p.row_cap, num_sms() * 16), copy_threads, 0, c.st>>>(
+                    static_cast<const uint16_t *>(c.h), w, row_of, target, state, c.dim, p.ld,
+                    c.dim % 8 == 0 && aligned16(c.h), c.dim % 8 == 0, hc, tlogit));
+    if (p.ld != c.dim) {
+        uint16_t *wc = reinterpret_cast<uint16_t *>(c.ws + p.off_w);
+        SPCO_LAUNCH("head_pad", c.st,
+                    head_pad_kernel<<<(unsigned)std::min<int64_t>(c.vocab, num_sms() * 16), copy_threads, 0, c.st>>>(
+                        w, c.vocab, c.dim, p.ld, wc));
+        w = wc;
+    }
+    SPECOPTIM_LAUNCHED("head_gather_kernel");
+    if (int rc = make_tmap_2d_bf16(&g->tm_h, hc, p.row_cap, p.ld, p.ld, 64)) return rc;
+    if (int rc = make_tmap_2d_bf16(&g->tm_w, w, c.vocab, p.ld, p.ld, 64)) return rc;
+    g->tm_p[0] = g->tm_p[1] = g->tm_h;  // replaced where pieces exist
+    g->vocab = vocab;
+    g->dim = c.dim;
+    g->row_cap = p.row_cap;
+    g->state = state;
+    g->target = target;
+    g->stats = reinterpret_cast<float2 *>(c.ws + p.off_stats);
+    g->norm = norm;
+    g->jobs = 1;
+    g->job[0] = HeadJob{HEAD_STATS, 0, 0, vocab, 1, 0};
+    const int64_t tiles = (int64_t)(p.row_cap / kHeadTileM) * (p.parts / 2);
+    if (int rc = head_gemm(*g, (int)std::min<int64_t>(tiles, INT32_MAX), "head_stats", c.st)) return rc;
+    SPCO_LAUNCH("head_lse", c.st,
+                head_lse_kernel<<<p.row_cap / 32, 256, 0, c.st>>>(
+                    g->stats, p.parts, p.row_cap, tlogit, row_of, state, norm, c.row_loss,
+                    reinterpret_cast<float *>(c.ws + p.off_block_loss), c.loss));
+    SPECOPTIM_LAUNCHED("head_lse_kernel");
+    return SPECOPTIM_OK;
+}
+
+}  // namespace
+}  // namespace spco
+
+using namespace spco;
+
+extern "C" int64_t head_loss_workspace(int64_t tokens, int64_t vocab, int32_t dim) {
+    int64_t bytes = -1;
+    entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "head_loss")) return rc;
+        bytes = plan_head(tokens, vocab, dim, false).bytes;
+        return SPECOPTIM_OK;
+    });
+    return bytes;
+}
+
+extern "C" int64_t head_loss_grad_workspace(int64_t tokens, int64_t vocab, int32_t dim) {
+    int64_t bytes = -1;
+    entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "head_loss_grad")) return rc;
+        bytes = plan_head(tokens, vocab, dim, true).bytes;
+        return SPECOPTIM_OK;
+    });
+    return bytes;
+}
+
+extern "C" int head_loss(const void *h, const void *w, const void *targets, int32_t id_bytes, int64_t ignore_index,
+                         int64_t tokens, int64_t vocab, int32_t dim, int32_t mean, float *loss, float *row_loss,
+                         void *workspace, int64_t workspace_bytes, void *stream) {
+    return entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "head_loss")) return rc;
+        const HeadPlan p = plan_head(tokens, vocab, dim, false);
+        const HeadCall c{h, w, targets, id_bytes, ignore_index, tokens, vocab, dim, mean, loss, row_loss,
+                         static_cast<char *>(workspace), workspace_bytes, static_cast<cudaStream_t>(stream)};
+        if (int rc = check_call(c, p, "head_loss")) return rc;
+        if (int rc = bind_device()) return rc;
+        HeadGemm g;
+        return run_loss(c, p, &g);
+    });
+}
+
+extern "C" int head_loss_grad(const void *h, const void *w, const void *targets, int32_t id_bytes,
+                              int64_t ignore_index, int64_t tokens, int64_t vocab, int32_t dim, int32_t mean,
+                              float grad_scale, float *loss, float *row_loss, void *dh, void *dw, int32_t dw_type,
+                              int32_t accumulate, void *workspace, int64_t workspace_bytes, void *stream) {
+    return entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "head_loss_grad")) return rc;
+        const HeadPlan p = plan_head(tokens, vocab, dim, true);
+        const HeadCall c{h, w, targets, id_bytes, ignore_index, tokens, vocab, dim, mean, loss, row_loss,
+                         static_cast<char *>(workspace), workspace_bytes, static_cast<cudaStream_t>(stream)};
+        if (int rc = check_call(c, p, "head_loss_grad")) return rc;
+        if (!dw || (tokens > 0 && !dh)) return fail(SPECOPTIM_ERR_INVALID_ARG, "head_loss_grad: null pointer");
+        if (!type_ok(dw_type))
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "head_loss_grad: dw_type must be STAGE_BF16 or STAGE_FP32");
+        if (!aligned_to(dh, 2) || !aligned_to(dw, type_bytes(dw_type)))
+            return fail(SPECOPTIM_ERR_MISALIGNED, "head_loss_grad: dh and dw must be aligned to their elements");
+        if (int rc = bind_device()) return rc;
+        HeadGemm g;
+        if (int rc = run_loss(c, p, &g)) return rc;
+        g.piece_ld = p.piece;
+        g.piece[0] = reinterpret_cast<bf16 *>(c.ws + p.off_p0);
+        g.piece[1] = reinterpret_cast<bf16 *>(c.ws + p.off_p1);
+        for (int b = 0; b < 2; ++b)
+            if (int rc = make_tmap_2d_bf16(&g.tm_p[b], g.piece[b], p.row_cap, p.piece, p.piece, 64)) return rc;
+        g.dh = reinterpret_cast<float *>(c.ws + p.off_dh);
+        g.dh_ld = p.dh_ld;
+        g.dw = dw;
+        g.dw_bf16 = dw_type == STAGE_BF16;
+        g.dw_add = accumulate != 0;
+        g.dw_vec = dim % 8 == 0 && aligned16(dw);
+        g.grad_scale = grad_scale;
+        const int64_t m_tiles = p.row_cap / kHeadTileM, d_tiles = ceil_div(dim, kHeadTileN);
+        for (int i = 0; i <= p.pieces; ++i) {
+            g.jobs = 0;
+            int64_t tiles = 0;
+            if (i < p.pieces) {
+                const int v0 = i * p.piece, width = (int)std::min<int64_t>(p.piece, vocab - v0);
+                g.job[g.jobs++] = HeadJob{HEAD_PROB, i & 1, v0, width, 1, 0};
+                tiles += m_tiles * ceil_div(width, kHeadTileN);
+            }
+            if (i > 0) {
+                const int v0 = (i - 1) * p.piece, width = (int)std::min<int64_t>(p.piece, vocab - v0);
+                g.job[g.jobs++] = HeadJob{HEAD_DH, (i - 1) & 1, v0, width, p.splits, i > 1};
+                g.job[g.jobs++] = HeadJob{HEAD_DW, (i - 1) & 1, v0, width, 1, 0};
+                tiles += m_tiles * d_tiles * p.splits + ceil_div(width, kHeadTileM) * d_tiles;
+            }
+            if (int rc = head_gemm(g, (int)std::min<int64_t>(tiles, INT32_MAX), "head_grad", c.st)) return rc;
+        }
+        if (tokens > 0) {
+            const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim, 8), 32));
+            const int grid = (int)std::min<int64_t>(tokens, num_sms() * 16);
+            const bool vec = dim % 8 == 0 && aligned16(dh);
+            auto *k = vec ? &head_dh_kernel<true> : &head_dh_kernel<false>;
+            SPCO_LAUNCH("head_dh", c.st,
+                        k<<<grid, threads, 0, c.st>>>(g.dh, p.splits, p.row_cap, p.dh_ld,
+                                                      reinterpret_cast<const int *>(c.ws + p.off_at), g.state,
+                                                      grad_scale, (int)tokens, dim, static_cast<bf16 *>(dh)));
+            SPECOPTIM_LAUNCHED("head_dh_kernel");
+        }
+        return SPECOPTIM_OK;
+    });
+}

@@ -71,6 +71,17 @@ __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 
+// the same with 16-bit operands (kind::f16)
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // arrive on `bar` once every previously issued tcgen05.mma of this thread completed
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile(
@@ -110,6 +121,22 @@ constexpr uint32_t tf32_idesc(int M, int N) {
     return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Shared-memory matrix descriptor of an operand whose rows run along M or N
+// (MN-major), 128-byte swizzle: blocks of 64 values (128 bytes) along M or N,
+// one k per 128-byte row; 8-k groups 1024 bytes apart (stride byte offset),
+// neighbouring 64-value blocks block_bytes apart (leading byte offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(block_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor of kind::f16 with bf16 operands: D fp32, M x N; a_mn /
+// b_mn: that operand is MN-major.
+__host__ __device__ constexpr uint32_t bf16_idesc(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 // ---- host --------------------------------------------------------------------------
 
 // 2D fp32 tensor map of a rows x cols matrix (leading dimension ld floats, a
@@ -121,6 +148,9 @@ int make_tmap_2d(CUtensorMap *map, const float *ptr, int64_t rows, int64_t cols,
 // (rows of the box land densely in shared memory, box_cols * 4 a multiple of 16).
 int make_tmap_2d_ex(CUtensorMap *map, const float *ptr, int64_t rows, int64_t cols, int64_t ld,
                     uint32_t box_cols, uint32_t box_rows, bool swizzle128);
+// 2D bf16 tensor map of a rows x cols matrix (leading dimension ld values, a
+// multiple of 8; 16-byte aligned base), 128-byte swizzle, box 64 values x box_rows.
+int make_tmap_2d_bf16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows);
 bool tmap_encoder_available();
 
 }  // namespace spco
