@@ -1,20 +1,23 @@
 // tcgen05 products of the vocabulary head (include/stage_ends.h, head_loss*):
 // bf16 operands (kind::f16), fp32 accumulation in TMEM.
 //
-//   l  = H W^T                 logits of a 128 x 256 tile, never stored: the
+//   l  = H W^T                 logits of a 256 x 256 tile, never stored: the
 //                              epilogue reduces them to row statistics
 //                              (HEAD_STATS) or turns them into a piece of
 //                              softmax - onehot (HEAD_PROB)
 //   dh = P W,  dw = P^T H      P a piece [rows][vocabulary rows of the piece]
 //
-// One persistent CTA per SM walks the tiles of up to three jobs (the next
-// piece's probabilities beside the previous piece's two products, which do not
-// depend on each other): warp 0 loads, one lane of warp 1 issues the MMAs, warps
-// 2-9 run the epilogues from one of two TMEM accumulators while the other is
-// being filled.  H, W and the pieces are read in 64 x 64 boxes with 128-byte
-// swizzle; the same box serves an operand whose rows run along K (one row per M
-// or N index) and one whose rows run along M or N (one row per k), so none of
-// the four products needs a transposed copy.
+// Persistent pairs of CTAs (cta_group::2), one pair per two SMs, walk the tiles
+// of up to three jobs (the next piece's probabilities beside the previous
+// piece's two products, which do not depend on each other).  A pair owns a
+// 256 x 256 tile: each CTA loads half of A's and half of B's rows (32 KB per 64
+// k, where a CTA alone would load 48 KB for half the tile) and keeps half of the
+// tile's rows in TMEM.  Warp 0 loads, one lane of rank 0's warp 1 issues the
+// MMAs, warps 2-9 run the epilogues from one of two TMEM accumulators while the
+// other is being filled.  H, W and the pieces are read in boxes 64 values wide with
+// 128-byte swizzle: 128 rows high where an operand's rows run along K (one row
+// per M or N index), 64 rows high where they run along M or N (one row per k),
+// so none of the products needs a transposed copy.
 //
 // Every wait on an mbarrier is bounded, as in gemm_tc.cu.
 #include <algorithm>
@@ -25,15 +28,17 @@
 namespace spco {
 namespace {
 
-constexpr int BM = kHeadTileM, BN = kHeadTileN, BK = 64;
-constexpr int STAGES = 4;
+constexpr int BM = kHeadTileM, BN = kHeadTileN, BK = 64;  // of a pair of CTAs
+constexpr int CM = BM / 2, CN = BN / 2;                    // one CTA's rows of A and of B
+constexpr int STAGES = 6;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = (2 + EPI_WARPS) * 32;
 constexpr uint32_t BOX_BYTES = 64 * 64 * 2;
-constexpr uint32_t A_BYTES = BM * BK * 2;
-constexpr uint32_t STAGE_BYTES = A_BYTES + BN * BK * 2;
+constexpr uint32_t A_BYTES = CM * BK * 2;
+constexpr uint32_t STAGE_BYTES = A_BYTES + CN * BK * 2;
 constexpr uint32_t TMEM_COLS = 2 * BN;
-constexpr size_t SMEM_BYTES = (size_t)STAGES * STAGE_BYTES + 1024 + 256;
+constexpr uint32_t OUT_BYTES = 32 * 128;  // one warp's block of 32 rows on its way out
+constexpr size_t SMEM_BYTES = (size_t)STAGES * STAGE_BYTES + EPI_WARPS * OUT_BYTES + 1024 + 256;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -45,47 +50,117 @@ __device__ __forceinline__ float ex2(float x) {
 
 // One tile of a job: where its operands start and how far k runs.
 struct Tile {
-    int kind, piece, job;
+    int kind, piece;
     int m, n;        // first row (M) and column (N) of the tile
     int k0, kb;      // first k, number of 64-k blocks
     int v0, width;   // vocabulary rows of the job's piece
     int split, add;
+    int rank;        // of this CTA in its pair
 };
 
+// The tiles of one pair.  The two gradient products' tiles are few and long (a
+// tile of dw runs over all rows, one of dh over the whole piece): they come
+// first and are dealt out in turn.  The logits tiles are many and short; each
+// pair takes as many as bring its load up to the others' (a load is counted in
+// 64-k blocks and a tile's own cost as two of them).  Alone (HEAD_STATS) they
+// are dealt out in turn too, so that neighbouring pairs share W's rows in L2.
 struct Walk {
     int rows, m_tiles, d_tiles;
-    int tiles[kHeadJobs], total;
+    int long_tiles, dw_tiles, dh_tiles;  // of the jobs HEAD_DW and HEAD_DH
+    int first_short, shorts, longs;      // this pair's logits tiles and long tiles
+    int pair, pairs;
+    int dw_job, dh_job, short_job;       // -1: none
+    bool in_turn;
 };
 
-__device__ __forceinline__ Walk make_walk(const HeadGemm &g) {
+constexpr int kTileCost = 2;
+
+__device__ __forceinline__ Walk make_walk(const HeadGemm &g, int pair, int pairs) {
     Walk w;
+    w.pair = pair;
+    w.pairs = pairs;
     w.rows = g.state->rows;
     w.m_tiles = (w.rows + BM - 1) / BM;
     w.d_tiles = (g.dim + BN - 1) / BN;
-    w.total = 0;
+    w.dw_job = w.dh_job = w.short_job = -1;
+    w.dw_tiles = w.dh_tiles = 0;
+    int n_short = 0, dw_cost = 0, dh_cost = 0;
 #pragma unroll
     for (int j = 0; j < kHeadJobs; ++j) {
-        int t = 0;
-        if (j < g.jobs) {
-            const HeadJob &q = g.job[j];
-            if (q.kind <= HEAD_PROB) t = w.m_tiles * ((q.width + BN - 1) / BN);
-            else if (q.kind == HEAD_DH) t = w.m_tiles * w.d_tiles * q.splits;
-            else t = ((q.width + BM - 1) / BM) * w.d_tiles;
+        if (j >= g.jobs) break;
+        const HeadJob &q = g.job[j];
+        if (q.kind <= HEAD_PROB) {
+            w.short_job = j;
+            n_short = w.m_tiles * ((q.width + BN - 1) / BN);
+        } else if (q.kind == HEAD_DH) {
+            w.dh_job = j;
+            w.dh_tiles = w.m_tiles * w.d_tiles * q.splits;
+            dh_cost = (q.width + BK - 1) / BK / q.splits + kTileCost;
+        } else {
+            w.dw_job = j;
+            w.dw_tiles = ((q.width + BM - 1) / BM) * w.d_tiles;
+            dw_cost = (w.rows + BK - 1) / BK + kTileCost;
         }
-        w.tiles[j] = t;
-        w.total += t;
+    }
+    w.long_tiles = w.dw_tiles + w.dh_tiles;
+    w.longs = pair < w.long_tiles ? (w.long_tiles - pair + pairs - 1) / pairs : 0;
+    w.in_turn = w.long_tiles == 0;
+    w.first_short = pair;
+    w.shorts = pair < n_short ? (n_short - pair + pairs - 1) / pairs : 0;
+    if (!w.in_turn) {
+        // pairs below r1 have one dw tile more, pairs below r2 one long tile more:
+        // three runs of pairs with equal loads
+        const int r1 = w.dw_tiles % pairs, r2 = w.long_tiles % pairs;
+        const int cost = (g.dim + BK - 1) / BK + kTileCost;
+        const int64_t total = (int64_t)w.dw_tiles * dw_cost + (int64_t)w.dh_tiles * dh_cost + (int64_t)n_short * cost;
+        const int edge[4] = {0, min(r1, r2), max(r1, r2), pairs};
+        int64_t share[3], all = 0;  // `pairs` times what a pair of the run lacks to the mean load
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int n_dw = w.dw_tiles / pairs + (edge[k] < r1), n_long = w.long_tiles / pairs + (edge[k] < r2);
+            const int64_t load = (int64_t)n_dw * dw_cost + (int64_t)(n_long - n_dw) * dh_cost;
+            share[k] = max((int64_t)0, total - load * pairs);
+            all += share[k] * (edge[k + 1] - edge[k]);
+        }
+        // integers throughout: a pair's last tile and the next one's first come from the same quotient
+        const int shift = max(0, 24 - __clzll(all));  // all < 2^40, n_short < 2^23
+        int64_t sum = 0;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            share[k] >>= shift;
+            sum += share[k] * (edge[k + 1] - edge[k]);
+        }
+        auto first_of = [&](int p) -> int {
+            if (p >= pairs || sum == 0) return p >= pairs ? n_short : 0;
+            int64_t before = 0;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) before += share[k] * (max(edge[k], min(edge[k + 1], p)) - edge[k]);
+            return (int)(before * n_short / sum);
+        };
+        w.first_short = first_of(pair);
+        w.shorts = first_of(pair + 1) - w.first_short;
     }
     return w;
 }
 
-__device__ __forceinline__ Tile tile_at(const HeadGemm &g, const Walk &w, int t) {
-    int j = 0;
-    while (j + 1 < g.jobs && t >= w.tiles[j]) t -= w.tiles[j++];
+__device__ __forceinline__ int tile_count(const Walk &w) { return w.longs + w.shorts; }
+
+// the pair's i-th tile
+__device__ __forceinline__ Tile tile_at(const HeadGemm &g, const Walk &w, int i, int rank) {
+    int t, j;
+    if (i < w.longs) {
+        t = w.pair + i * w.pairs;
+        j = t < w.dw_tiles ? w.dw_job : w.dh_job;
+        if (t >= w.dw_tiles) t -= w.dw_tiles;
+    } else {
+        t = w.first_short + (i - w.longs) * (w.in_turn ? w.pairs : 1);
+        j = w.short_job;
+    }
     const HeadJob &q = g.job[j];
     Tile x;
     x.kind = q.kind;
     x.piece = q.piece;
-    x.job = j;
+    x.rank = rank;
     x.v0 = q.v0;
     x.width = q.width;
     x.split = 0;
@@ -118,7 +193,7 @@ __device__ __forceinline__ Tile tile_at(const HeadGemm &g, const Walk &w, int t)
 
 __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Walk &w, const Tile &x, uint32_t acc, int q,
                                                int lane, int half) {
-    const int row = x.m + q * 32 + lane;
+    const int row = x.m + x.rank * CM + q * 32 + lane;
     const int target = row < w.rows ? g.target[row] : -1;
     float m = -INFINITY, s = 0.f;
     for (int c = 0; c < BN / 2 / 32; ++c) {
@@ -154,13 +229,50 @@ __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Walk &w,
     if (row < w.rows) g.stats[(int64_t)(x.n / (BN / 2) + half) * g.row_cap + row] = make_float2(m, s);
 }
 
+// A warp's way out: 32 rows of 128 bytes (64 bf16 or 32 fp32 columns) are laid
+// out in shared memory with the 128-byte swizzle and stored, or added, by one
+// tensor copy, which also clips what lies outside the tensor.  Each thread
+// writes its own row; the swizzle spreads a warp's 16-byte pieces over the banks.
+struct WayOut {
+    unsigned char *buf;
+    int lane;
+
+    __device__ __forceinline__ void ready() const {  // the last copy has read the buffer
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+    }
+    __device__ __forceinline__ void put(int piece16, uint4 v) const {
+        *reinterpret_cast<uint4 *>(buf + lane * 128 + ((piece16 ^ (lane & 7)) << 4)) = v;
+    }
+    __device__ __forceinline__ void put_bf16(int first16, const float (&v)[32]) const {  // 4 pieces
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            put(first16 + i, make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                        pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7])));
+    }
+    __device__ __forceinline__ void put_fp32(const float (&v)[32]) const {  // 8 pieces
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            put(i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                              __float_as_uint(v[4 * i + 3])));
+    }
+    __device__ __forceinline__ void send(const CUtensorMap *map, int x, int y, bool add) const {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (add) tma_add_2d(map, buf, x, y);
+            else tma_store_2d(map, buf, x, y);
+            bulk_commit();
+        }
+    }
+};
+
 __device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Walk &w, const Tile &x, uint32_t acc, int q,
-                                              int lane, int half) {
-    const int row = x.m + q * 32 + lane;
+                                              int half, const WayOut &out) {
+    const int row0 = x.m + x.rank * CM + q * 32, row = row0 + out.lane;
     const bool in = row < w.rows;
     const int target = in ? g.target[row] - x.v0 : -1;  // column within the piece
     const float4 norm = in ? g.norm[row] : make_float4(0.f, 0.f, 0.f, 0.f);
-    bf16 *out = g.piece[x.piece] + (int64_t)row * g.piece_ld + x.n;
     for (int c = 0; c < BN / 2 / 32; ++c) {
         const int col0 = half * (BN / 2) + c * 32, p0 = x.n + col0;
         float v[32];
@@ -172,18 +284,15 @@ __device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Walk &w, 
             if (p0 + i == target) p = norm.z;
             v[i] = in && p0 + i < x.width ? p : 0.f;
         }
-        uint4 *o = reinterpret_cast<uint4 *>(out + col0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+        if ((c & 1) == 0) out.ready();
+        out.put_bf16((c & 1) * 4, v);
+        if (c & 1) out.send(&g.tm_p_st[x.piece], 0, (p0 / 64) * g.row_cap + row0, false);
     }
 }
 
 __device__ __forceinline__ void epilogue_dh(const HeadGemm &g, const Walk &w, const Tile &x, uint32_t acc, int q,
-                                            int lane, int half) {
-    const int row = x.m + q * 32 + lane;
-    float *out = g.dh + ((int64_t)x.split * g.row_cap + row) * g.dh_ld + x.n;
+                                            int half, const WayOut &out) {
+    const int row0 = x.m + x.rank * CM + q * 32;
     for (int c = 0; c < BN / 2 / 32; ++c) {
         const int col0 = half * (BN / 2) + c * 32;
         if (x.n + col0 >= g.dim) break;
@@ -194,65 +303,41 @@ __device__ __forceinline__ void epilogue_dh(const HeadGemm &g, const Walk &w, co
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < 8 && row < w.rows; ++i) {  // dh_ld is a multiple of 32
-            float4 *o = reinterpret_cast<float4 *>(out + col0) + i;
-            float4 f = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            if (x.add) {
-                const float4 p = *o;
-                f = make_float4(f.x + p.x, f.y + p.y, f.z + p.z, f.w + p.w);
-            }
-            *o = f;
-        }
+        out.ready();
+        out.put_fp32(v);
+        // one addend per value and launch: the order of the sum is the order of the launches
+        out.send(&g.tm_dh, x.n + col0, x.split * g.row_cap + row0, x.add != 0);
     }
 }
 
-__device__ __forceinline__ void epilogue_dw(const HeadGemm &g, const Tile &x, uint32_t acc, int q, int lane, int half,
-                                            float factor) {
-    const int local = x.m + q * 32 + lane;
-    const int64_t row = x.v0 + local;
+// dw through shared memory and a tensor copy where its rows are multiples of 16
+// bytes; otherwise, and for adding to a bf16 gradient (one rounding of the
+// sum), value by value.
+__device__ __forceinline__ void epilogue_dw(const HeadGemm &g, const Tile &x, uint32_t acc, int q, int half,
+                                            float factor, const WayOut &out) {
+    const int local0 = x.m + x.rank * CM + q * 32, local = local0 + out.lane;
+    const int64_t row = (int64_t)x.v0 + local;
     for (int c = 0; c < BN / 2 / 32; ++c) {
         const int col0 = half * (BN / 2) + c * 32, col = x.n + col0;
-        if (col >= g.dim) break;
+        if (col >= g.dim || local0 >= x.width) break;
         float v[32];
         __syncwarp();
         tmem_ld32(acc + col0 + ((uint32_t)(q * 32) << 16), v);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = x.kb == 0 ? 0.f : v[i] * factor;
-        if (g.dw_vec) {  // dim % 8 == 0, 16-byte aligned: whole groups of 8
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (col + 8 * i >= g.dim || local >= x.width) break;
-                float a[8];
-                if (g.dw_bf16) {
-                    uint4 *o = reinterpret_cast<uint4 *>(static_cast<bf16 *>(g.dw) + row * g.dim + col) + i;
-                    if (g.dw_add) {
-                        const uint4 u = *o;
-                        a[0] = lo_f(u.x); a[1] = hi_f(u.x); a[2] = lo_f(u.y); a[3] = hi_f(u.y);
-                        a[4] = lo_f(u.z); a[5] = hi_f(u.z); a[6] = lo_f(u.w); a[7] = hi_f(u.w);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[8 * i + j] += a[j];
-                    }
-                    *o = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                    pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-                } else {
-                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(g.dw) + row * g.dim + col) + 2 * i;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float4 f = make_float4(v[8 * i + 4 * h], v[8 * i + 4 * h + 1], v[8 * i + 4 * h + 2],
-                                               v[8 * i + 4 * h + 3]);
-                        if (g.dw_add) {
-                            const float4 p = o[h];
-                            f = make_float4(f.x + p.x, f.y + p.y, f.z + p.z, f.w + p.w);
-                        }
-                        o[h] = f;
-                    }
-                }
-            }
-        } else {
+        if (g.dw_tma && g.dw_bf16) {
+            if ((c & 1) == 0) out.ready();
+            out.put_bf16((c & 1) * 4, v);
+            // the second half of the box may hold an earlier block where dim ends in the first: it is clipped
+            if ((c & 1) || col + 32 >= g.dim) out.send(&g.tm_dw, col - (c & 1) * 32, x.v0 + local0, false);
+        } else if (g.dw_tma) {
+            out.ready();
+            out.put_fp32(v);
+            out.send(&g.tm_dw, col, x.v0 + local0, g.dw_add != 0);
+        } else if (local < x.width) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                if (col + i >= g.dim || local >= x.width) break;
+                if (col + i >= g.dim) break;
                 const int64_t o = row * g.dim + col + i;
                 if (g.dw_bf16) {
                     bf16 *p = static_cast<bf16 *>(g.dw) + o;
@@ -268,16 +353,19 @@ __device__ __forceinline__ void epilogue_dw(const HeadGemm &g, const Tile &x, ui
 
 // ---- the kernel ------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                             ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES);
-    uint64_t *empty = full + STAGES;
-    uint64_t *tfull = empty + STAGES;
-    uint64_t *tempty = tfull + 2;
+    unsigned char *way_out = smem + STAGES * STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(way_out + EPI_WARPS * OUT_BYTES);  // rank 0's: both CTAs' loads
+    uint64_t *empty = full + STAGES;                                             // each CTA's own
+    uint64_t *tfull = empty + STAGES;                                            // each CTA's own
+    uint64_t *tempty = tfull + 2;                                                // rank 0's: both CTAs' epilogues
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -285,68 +373,69 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], EPI_WARPS * 32);
+            mbar_init(&tempty[a], 2 * EPI_WARPS);
         }
         fence_mbar_init();
-        prefetch_tmap(&g.tm_h);
-        prefetch_tmap(&g.tm_w);
-        prefetch_tmap(&g.tm_p[0]);
-        prefetch_tmap(&g.tm_p[1]);
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, TMEM_COLS);
-        tmem_relinquish();
-    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, TMEM_COLS);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers exist and its TMEM is allocated
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const Walk walk = make_walk(g);
+    const Walk walk = make_walk(g, blockIdx.x / 2, gridDim.x / 2);
+    const int tiles = tile_count(walk);
 
     if (warp == 0 && lane == 0) {
-        // ---------------- TMA producer
+        // ---------------- TMA producer: this CTA's half of A and of B
         uint32_t it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < walk.total && ok; t += gridDim.x) {
-            const Tile x = tile_at(g, walk, t);
-            const CUtensorMap *ma = x.kind <= HEAD_PROB ? &g.tm_h : &g.tm_p[x.piece];
-            const CUtensorMap *mb = x.kind == HEAD_DW ? &g.tm_h : &g.tm_w;
+        for (int t = 0; t < tiles && ok; ++t) {
+            const Tile x = tile_at(g, walk, t, rank);
+            const CUtensorMap *ma = x.kind <= HEAD_PROB ? &g.tm_h_k : x.kind == HEAD_DH ? &g.tm_p_k[x.piece] : &g.tm_p[x.piece];
+            const CUtensorMap *mb = x.kind <= HEAD_PROB ? &g.tm_w_k : x.kind == HEAD_DH ? &g.tm_w : &g.tm_h;
+            const int m = x.m + rank * CM, n = x.n + rank * CN;
             for (int kb = 0; kb < x.kb; ++kb, ++it) {
                 const int s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
-                if (!mbar_wait_bounded(&empty[s], ph ^ 1u, flag, 0x601u)) { ok = false; break; }
+                if (!mbar_wait_cluster(&empty[s], ph ^ 1u, flag, 0x601u)) { ok = false; break; }
                 unsigned char *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
                 const int k = x.k0 + kb * BK;
-                mbar_arrive_expect_tx(&full[s], STAGE_BYTES);
-#pragma unroll
-                for (int i = 0; i < BM / 64; ++i) {
-                    if (x.kind == HEAD_DW) tma_load_2d(sa + i * BOX_BYTES, ma, x.m + 64 * i, k, &full[s]);
-                    else tma_load_2d(sa + i * BOX_BYTES, ma, k, x.m + 64 * i, &full[s]);
-                }
-#pragma unroll
-                for (int i = 0; i < BN / 64; ++i) {
-                    if (x.kind <= HEAD_PROB) tma_load_2d(sb + i * BOX_BYTES, mb, k, x.v0 + x.n + 64 * i, &full[s]);
-                    else if (x.kind == HEAD_DH) tma_load_2d(sb + i * BOX_BYTES, mb, x.n + 64 * i, x.v0 + k, &full[s]);
-                    else tma_load_2d(sb + i * BOX_BYTES, mb, x.n + 64 * i, k, &full[s]);
+                const uint32_t bar = cluster_addr(&full[s], 0);
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
+                // k, m, n are multiples of 64: a column block of h and of the pieces
+                if (x.kind == HEAD_DW) {
+                    tma_load_2d_pair(sa, ma, 0, m / 64 * g.row_cap + k, bar);
+                    tma_load_2d_pair(sa + BOX_BYTES, ma, 0, (m / 64 + 1) * g.row_cap + k, bar);
+                    tma_load_2d_pair(sb, mb, 0, n / 64 * g.row_cap + k, bar);
+                    tma_load_2d_pair(sb + BOX_BYTES, mb, 0, (n / 64 + 1) * g.row_cap + k, bar);
+                } else {
+                    tma_load_2d_pair(sa, ma, 0, k / 64 * g.row_cap + m, bar);
+                    if (x.kind == HEAD_DH) {
+                        tma_load_2d_pair(sb, mb, n, x.v0 + k, bar);
+                        tma_load_2d_pair(sb + BOX_BYTES, mb, n + 64, x.v0 + k, bar);
+                    } else {
+                        tma_load_2d_pair(sb, mb, k, x.v0 + n, bar);
+                    }
                 }
             }
         }
-    } else if (warp == 1 && lane == 0) {
-        // ---------------- MMA issuer
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---------------- MMA issuer of the pair
         uint32_t it = 0, local = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < walk.total && ok; t += gridDim.x, ++local) {
-            const Tile x = tile_at(g, walk, t);
+        for (int t = 0; t < tiles && ok; ++t, ++local) {
+            const Tile x = tile_at(g, walk, t, rank);
             const bool a_mn = x.kind == HEAD_DW, b_mn = x.kind >= HEAD_DH;
             const uint32_t idesc = bf16_idesc(BM, BN, a_mn, b_mn);
             const uint32_t acc = local & 1u, aph = (local >> 1) & 1u;
-            if (!mbar_wait_bounded(&tempty[acc], aph ^ 1u, flag, 0x602u)) break;
+            if (!mbar_wait_cluster(&tempty[acc], aph ^ 1u, flag, 0x602u)) break;
             tc_fence_after();
             const uint32_t d = tmem_base + acc * BN;
             for (int kb = 0; kb < x.kb; ++kb, ++it) {
                 const int s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
-                if (!mbar_wait_bounded(&full[s], ph, flag, 0x603u)) { ok = false; break; }
+                if (!mbar_wait_cluster(&full[s], ph, flag, 0x603u)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BYTES;
 #pragma unroll
@@ -354,37 +443,42 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
                     // 16 k: 32 bytes along a K-major row, 16 rows of an MN-major block
                     const uint64_t da = a_mn ? smem_desc_mn_sw128(sa + k * 2048, BOX_BYTES) : smem_desc_sw128(sa + k * 32);
                     const uint64_t db = b_mn ? smem_desc_mn_sw128(sb + k * 2048, BOX_BYTES) : smem_desc_sw128(sb + k * 32);
-                    mma_f16(d, da, db, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                    mma_f16_pair(d, da, db, idesc, (kb > 0 || k > 0) ? 1u : 0u);
                 }
-                mma_commit(&empty[s]);
+                mma_commit_pair(&empty[s]);
             }
-            mma_commit(&tfull[acc]);
+            mma_commit_pair(&tfull[acc]);
         }
     } else if (warp >= 2) {
-        // ---------------- epilogue
+        // ---------------- epilogue of this CTA's rows
         const int q = warp % 4;           // TMEM lane quarter this warp may access
         const int half = (warp - 2) / 4;  // column half of the tile
         const float factor = g.grad_scale * g.state->inv_count;
+        const WayOut out{way_out + (warp - 2) * OUT_BYTES, lane};
         uint32_t local = 0;
-        for (int t = blockIdx.x; t < walk.total; t += gridDim.x, ++local) {
-            const Tile x = tile_at(g, walk, t);
+        for (int t = 0; t < tiles; ++t, ++local) {
+            const Tile x = tile_at(g, walk, t, rank);
             const uint32_t a = local & 1u, aph = (local >> 1) & 1u;
-            if (!mbar_wait_bounded(&tfull[a], aph, flag, 0x604u)) break;
+            if (!mbar_wait_cluster(&tfull[a], aph, flag, 0x604u)) break;
             tc_fence_after();
             const uint32_t acc = tmem_base + a * BN;
             if (x.kind == HEAD_STATS) epilogue_stats(g, walk, x, acc, q, lane, half);
-            else if (x.kind == HEAD_PROB) epilogue_prob(g, walk, x, acc, q, lane, half);
-            else if (x.kind == HEAD_DH) epilogue_dh(g, walk, x, acc, q, lane, half);
-            else epilogue_dw(g, x, acc, q, lane, half, factor);
+            else if (x.kind == HEAD_PROB) epilogue_prob(g, walk, x, acc, q, half, out);
+            else if (x.kind == HEAD_DH) epilogue_dh(g, walk, x, acc, q, half, out);
+            else epilogue_dw(g, x, acc, q, half, factor, out);
             tc_fence_before();
-            mbar_arrive(&tempty[a]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[a], 0));
         }
+        if (lane == 0) bulk_wait_all();  // the copies out have been written
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // no arrival is on its way to a CTA that has left
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, TMEM_COLS);
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
     }
 }
 
@@ -392,8 +486,8 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
 
 int head_gemm(const HeadGemm &g, int max_tiles, const char *name, cudaStream_t st) {
     if (int rc = set_smem_limit(reinterpret_cast<const void *>(&head_gemm_kernel), SMEM_BYTES)) return rc;
-    const int grid = std::max(1, std::min(max_tiles, num_sms()));
-    SPCO_LAUNCH(name, st, head_gemm_kernel<<<grid, THREADS, SMEM_BYTES, st>>>(g, device_flag_ptr()));
+    const int pairs = std::max(1, std::min(max_tiles, num_sms() / 2));
+    SPCO_LAUNCH(name, st, head_gemm_kernel<<<2 * pairs, THREADS, SMEM_BYTES, st>>>(g, device_flag_ptr()));
     SPECOPTIM_LAUNCHED("head_gemm_kernel");
     return SPECOPTIM_OK;
 }

@@ -32,26 +32,29 @@ struct HeadJob {
 
 constexpr int kHeadJobs = 3;
 
+// The compact rows of h and the pieces are stored in column blocks: 64 columns
+// of all rows, then the next 64 ([columns / 64][row_cap][64]), so that every box
+// the products load or store is one contiguous range of memory.
 struct HeadGemm {
-    CUtensorMap tm_h, tm_w, tm_p[2];
+    CUtensorMap tm_h_k, tm_w_k, tm_p_k[2];  // boxes of 64 k x 128 rows
+    CUtensorMap tm_h, tm_w, tm_p[2];        // boxes of 64 columns x 64 k
+    CUtensorMap tm_p_st[2];                 // stores: boxes of 64 columns x 32 rows
+    CUtensorMap tm_dh, tm_dw;               // stores: 32 fp32 or 64 bf16 columns x 32 rows
     HeadJob job[kHeadJobs];
     int jobs;
     int vocab, dim;
     int row_cap;               // rows of the compact buffers (a multiple of the tile height)
-    int piece_ld;              // columns of a piece buffer
     const HeadState *state;
     const int *target;         // [row_cap]
     float2 *stats;             // [2 * ceil(vocab / 256)][row_cap]
     const float4 *norm;        // [row_cap]: largest logit, 1 / sum, softmax - 1 at the target
-    bf16 *piece[2];            // [row_cap][piece_ld]
-    float *dh;                 // [splits][row_cap][dh_ld]
-    int dh_ld;
     void *dw;                  // [vocab][dim]
-    int dw_bf16, dw_add, dw_vec;
+    int dw_bf16, dw_add;
+    int dw_tma;                // dw is stored through tm_dw
     float grad_scale;
 };
 
-constexpr int kHeadTileM = 128, kHeadTileN = 256;
+constexpr int kHeadTileM = 256, kHeadTileN = 256;
 
 int head_gemm(const HeadGemm &g, int max_tiles, const char *name, cudaStream_t st);
 

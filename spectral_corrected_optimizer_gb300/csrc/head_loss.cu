@@ -30,39 +30,51 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ---- the rows that have a target ---------------------------------------------------------
 
 // One block: lists the tokens with a target in token order.  row_of[r] = token
-// of row r, at[t] = row of token t (-1: none), target[r].
+// of row r, at[t] = row of token t (-1: none), target[r].  A thread takes 8
+// neighbouring tokens at a time, so 8192 tokens cost one round.
+constexpr int kRowItems = 8;
 template <typename ID>
 __global__ void __launch_bounds__(1024) head_rows_kernel(const ID *__restrict__ targets, int64_t ignore, int tokens,
                                                          int vocab, int mean, HeadState *state, int *__restrict__ row_of,
                                                          int *__restrict__ at, int *__restrict__ target,
                                                          float *__restrict__ row_loss, unsigned *flag) {
-    __shared__ int warp_count[32];
+    __shared__ int warp_count[2][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int rows = 0;
-    for (int t0 = 0; t0 < tokens; t0 += 1024) {
-        const int t = t0 + threadIdx.x;
-        const int64_t y = t < tokens ? (int64_t)targets[t] : ignore;
-        const bool inside = y >= 0 && y < vocab;
-        if (y != ignore && !inside) atomicExch(flag, kSiteTarget);
-        const bool has = y != ignore && inside;
-        const unsigned ballot = __ballot_sync(0xffffffffu, has);
-        __syncthreads();  // the previous step's counts have been read
-        if (lane == 0) warp_count[w] = __popc(ballot);
+    int rows = 0, parity = 0;
+    for (int64_t t0 = 0; t0 < tokens; t0 += 1024 * kRowItems, parity ^= 1) {
+        const int64_t t = t0 + (int64_t)threadIdx.x * kRowItems;
+        int y[kRowItems], count = 0;
+#pragma unroll
+        for (int i = 0; i < kRowItems; ++i) {
+            const int64_t id = t + i < tokens ? (int64_t)targets[t + i] : ignore;
+            const bool inside = id >= 0 && id < vocab;
+            if (id != ignore && !inside) atomicExch(flag, kSiteTarget);
+            y[i] = id != ignore && inside ? (int)id : -1;
+            count += y[i] >= 0;
+        }
+        int incl = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) warp_count[parity][w] = incl;
         __syncthreads();
-        int before = rows;
+        int r = rows + incl - count;
         for (int i = 0; i < 32; ++i) {
-            const int c = warp_count[i];
-            if (i < w) before += c;
+            const int c = warp_count[parity][i];
+            if (i < w) r += c;
             rows += c;
         }
-        if (t < tokens) {
-            const int r = before + __popc(ballot & ((1u << lane) - 1u));
-            at[t] = has ? r : -1;
-            if (has) {
-                row_of[r] = t;
-                target[r] = (int)y;
+#pragma unroll
+        for (int i = 0; i < kRowItems; ++i) {
+            if (t + i >= tokens) break;
+            at[t + i] = y[i] >= 0 ? r : -1;
+            if (y[i] >= 0) {
+                row_of[r] = (int)(t + i);
+                target[r++] = y[i];
             } else {
-                row_loss[t] = 0.f;
+                row_loss[t + i] = 0.f;
             }
         }
     }
@@ -86,38 +98,38 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float s) {
     return fmaf(hi_f(a), hi_f(b), fmaf(lo_f(a), lo_f(b), s));
 }
 
-// Copies the listed rows of h together, ld values each (a multiple of 8, zero
-// behind dim), zero rows up to the next multiple of the tile height.  On the
-// way the logit of each row's target is formed as an fp32 dot product: the
-// loss is the difference between it and the log-sum-exp, and the tensor cores'
+// Copies the listed rows of h together, in column blocks of 64 (zero behind
+// dim), with zero rows up to the next multiple of the tile height.  On the way
+// the logit of each row's target is formed as an fp32 dot product: the loss is the difference between it and the log-sum-exp, and the tensor cores'
 // long accumulation (dim / 16 steps, each cut off rather than rounded) leaves a
 // large logit 2^-24 dim / 32 of itself short.
 __global__ void __launch_bounds__(256) head_gather_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ w,
                                                           const int *__restrict__ row_of, const int *__restrict__ target,
-                                                          const HeadState *__restrict__ state, int dim, int ld,
+                                                          const HeadState *__restrict__ state, int dim, int row_cap,
                                                           int h_vec, int w_vec, uint16_t *__restrict__ out,
                                                           float *__restrict__ target_logit) {
     __shared__ float red[2][8];
     const int rows = state->rows, end = (rows + kHeadTileM - 1) / kHeadTileM * kHeadTileM;
+    const int vecs = (dim + 63) / 64 * 8;
     int parity = 0;
     for (int r = blockIdx.x; r < end; r += gridDim.x, parity ^= 1) {
-        uint4 *d = reinterpret_cast<uint4 *>(out + (int64_t)r * ld);
-        if (r >= rows) {
-            for (int v = threadIdx.x; v < ld / 8; v += blockDim.x) d[v] = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        const uint16_t *hr = h + (int64_t)row_of[r] * dim, *wr = w + (int64_t)target[r] * dim;
+        const uint16_t *hr = r < rows ? h + (int64_t)row_of[r] * dim : nullptr;
+        const uint16_t *wr = r < rows ? w + (int64_t)target[r] * dim : nullptr;
         float s = 0.f;
-        for (int v = threadIdx.x; v < ld / 8; v += blockDim.x) {
-            const uint4 a = row_vec(hr, v, dim, h_vec), b = row_vec(wr, v, dim, w_vec);
-            s += dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, 0.f))));
-            d[v] = a;
+        for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+            uint4 a = make_uint4(0, 0, 0, 0);
+            if (hr && v * 8 < dim) {
+                a = row_vec(hr, v, dim, h_vec);
+                const uint4 b = row_vec(wr, v, dim, w_vec);
+                s += dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, 0.f))));
+            }
+            reinterpret_cast<uint4 *>(out + ((int64_t)(v / 8) * row_cap + r) * 64)[v % 8] = a;
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if ((threadIdx.x & 31) == 0) red[parity][threadIdx.x >> 5] = s;
         __syncthreads();
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 && r < rows) {
             for (int i = 1; i < (int)blockDim.x / 32; ++i) s += red[parity][i];
             target_logit[r] = s;
         }
@@ -134,25 +146,25 @@ __global__ void __launch_bounds__(256) head_pad_kernel(const uint16_t *__restric
 
 // ---- joining the row statistics ------------------------------------------------------------
 
-// 32 rows per block, 8 threads per row: each joins every eighth part, then the
-// eight are joined in order.  The parts' sums leave the target out: S of them
+// 32 rows per block, 32 threads per row: each joins every 32nd part, then the
+// 32 are joined in order.  The parts' sums leave the target out: S of them
 // gives softmax - 1 = -S / (S + e_target) and the loss log(1 + S / e_target)
 // without the cancellation that a well-predicted token (S small) would meet in
 // 1 - p and in lse - l.  The last block to finish adds up the blocks' loss
 // sums, in block order.
-__global__ void __launch_bounds__(256) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
+__global__ void __launch_bounds__(1024) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
                                                        const float *__restrict__ target_logit,
                                                        const int *__restrict__ row_of, HeadState *state,
                                                        float4 *__restrict__ norm, float *__restrict__ row_loss,
                                                        float *__restrict__ block_loss, float *__restrict__ loss) {
-    __shared__ float sm[8][33], ss[8][33];
+    __shared__ float sm[32][33], ss[32][33];
     __shared__ bool last;
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int rows = state->rows, row = blockIdx.x * 32 + c;
     float m = -INFINITY, s = 0.f;
     if (row < rows) {
 #pragma unroll 8
-        for (int p = w; p < parts; p += 8) {
+        for (int p = w; p < parts; p += 32) {
             const float2 x = stats[(int64_t)p * row_cap + row];
             const float top = fmaxf(m, x.x), ref = top == -INFINITY ? 0.f : top;
             s = s * exp2f((m - ref) * kLog2e) + x.y * exp2f((x.x - ref) * kLog2e);
@@ -163,7 +175,8 @@ __global__ void __launch_bounds__(256) head_lse_kernel(const float2 *__restrict_
     ss[w][c] = s;
     __syncthreads();
     if (w == 0) {
-        for (int i = 1; i < 8; ++i) {
+#pragma unroll 4
+        for (int i = 1; i < 32; ++i) {
             const float top = fmaxf(m, sm[i][c]), ref = top == -INFINITY ? 0.f : top;
             s = s * exp2f((m - ref) * kLog2e) + ss[i][c] * exp2f((sm[i][c] - ref) * kLog2e);
             m = top;
@@ -255,18 +268,18 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
     p.off_norm = take(cap * 16);
     p.off_block_loss = take(ceil_div(cap, 32) * 4);
     p.off_stats = take((int64_t)p.parts * cap * 8);
-    p.off_h = take(cap * p.ld * 2);
+    p.off_h = take(cap * round_up(dim, 64) * 2);
     p.off_w = p.ld != dim ? take(vocab * p.ld * 2) : 0;
     if (grad) {
         const int64_t all = round_up(vocab, kHeadTileN);
         const int64_t fit = kPieceBytes / (cap * 2) / kHeadTileN * kHeadTileN;
         p.piece = (int)std::min(all, std::max<int64_t>(fit, kPieceMin));
         p.pieces = (int)ceil_div(vocab, p.piece);
-        // few rows: the long sum over the vocabulary is split until the GPU has a tile per SM
+        // few rows: the long sum over the vocabulary is split until every pair of SMs has a tile
         p.dh_ld = (int)round_up(dim, 32);
         const int64_t tiles = (cap / kHeadTileM) * ceil_div(dim, kHeadTileN);
         const int64_t blocks = ceil_div(std::min<int64_t>(vocab, p.piece), 64);
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / tiles, blocks / 8));
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / tiles, blocks / 8));
         p.off_p0 = take(cap * p.piece * 2);
         p.off_p1 = p.pieces > 1 ? take(cap * p.piece * 2) : p.off_p0;
         p.off_dh = take((int64_t)p.splits * cap * p.dh_ld * 4);
@@ -281,6 +294,8 @@ int check_sizes(int64_t tokens, int64_t vocab, int32_t dim, const char *what) {
     if (vocab < 1 || vocab > (int64_t)1 << 24)
         return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": vocab outside [1, 2^24]");
     if (dim < 1 || dim > 1 << 16) return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": dim outside [1, 65536]");
+    if (round_up(tokens, kHeadTileM) * ceil_div(dim, 64) > INT32_MAX)
+        return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": tokens x dim above 2^37");
     return SPECOPTIM_OK;
 }
 
@@ -331,7 +346,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, HeadGemm *g) {
     const int copy_threads = (int)std::min<int64_t>(256, round_up(p.ld / 8, 32));
     SPCO_LAUNCH("head_gather", c.st,
                 head_gather_kernel<<<std::min(p.row_cap, num_sms() * 16), copy_threads, 0, c.st>>>(
-                    static_cast<const uint16_t *>(c.h), w, row_of, target, state, c.dim, p.ld,
+                    static_cast<const uint16_t *>(c.h), w, row_of, target, state, c.dim, p.row_cap,
                     c.dim % 8 == 0 && aligned16(c.h), c.dim % 8 == 0, hc, tlogit));
     if (p.ld != c.dim) {
         uint16_t *wc = reinterpret_cast<uint16_t *>(c.ws + p.off_w);
@@ -341,9 +356,11 @@ int run_loss(const HeadCall &c, const HeadPlan &p, HeadGemm *g) {
         w = wc;
     }
     SPECOPTIM_LAUNCHED("head_gather_kernel");
-    if (int rc = make_tmap_2d_bf16(&g->tm_h, hc, p.row_cap, p.ld, p.ld, 64)) return rc;
+    const int64_t h_lines = ceil_div(c.dim, 64) * p.row_cap;
+    if (int rc = make_tmap_2d_bf16(&g->tm_h_k, hc, h_lines, 64, 64, 128)) return rc;
+    if (int rc = make_tmap_2d_bf16(&g->tm_w_k, w, c.vocab, p.ld, p.ld, 128)) return rc;
+    if (int rc = make_tmap_2d_bf16(&g->tm_h, hc, h_lines, 64, 64, 64)) return rc;
     if (int rc = make_tmap_2d_bf16(&g->tm_w, w, c.vocab, p.ld, p.ld, 64)) return rc;
-    g->tm_p[0] = g->tm_p[1] = g->tm_h;  // replaced where pieces exist
     g->vocab = vocab;
     g->dim = c.dim;
     g->row_cap = p.row_cap;
@@ -356,7 +373,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, HeadGemm *g) {
     const int64_t tiles = (int64_t)(p.row_cap / kHeadTileM) * (p.parts / 2);
     if (int rc = head_gemm(*g, (int)std::min<int64_t>(tiles, INT32_MAX), "head_stats", c.st)) return rc;
     SPCO_LAUNCH("head_lse", c.st,
-                head_lse_kernel<<<p.row_cap / 32, 256, 0, c.st>>>(
+                head_lse_kernel<<<p.row_cap / 32, 1024, 0, c.st>>>(
                     g->stats, p.parts, p.row_cap, tlogit, row_of, state, norm, c.row_loss,
                     reinterpret_cast<float *>(c.ws + p.off_block_loss), c.loss));
     SPECOPTIM_LAUNCHED("head_lse_kernel");
@@ -421,17 +438,24 @@ extern "C" int head_loss_grad(const void *h, const void *w, const void *targets,
         if (int rc = bind_device()) return rc;
         HeadGemm g;
         if (int rc = run_loss(c, p, &g)) return rc;
-        g.piece_ld = p.piece;
-        g.piece[0] = reinterpret_cast<bf16 *>(c.ws + p.off_p0);
-        g.piece[1] = reinterpret_cast<bf16 *>(c.ws + p.off_p1);
-        for (int b = 0; b < 2; ++b)
-            if (int rc = make_tmap_2d_bf16(&g.tm_p[b], g.piece[b], p.row_cap, p.piece, p.piece, 64)) return rc;
-        g.dh = reinterpret_cast<float *>(c.ws + p.off_dh);
-        g.dh_ld = p.dh_ld;
+        const int64_t p_lines = (int64_t)(p.piece / 64) * p.row_cap;
+        for (int b = 0; b < 2; ++b) {
+            char *piece = c.ws + (b ? p.off_p1 : p.off_p0);
+            if (int rc = make_tmap_2d_bf16(&g.tm_p_k[b], piece, p_lines, 64, 64, 128)) return rc;
+            if (int rc = make_tmap_2d_bf16(&g.tm_p[b], piece, p_lines, 64, 64, 64)) return rc;
+            if (int rc = make_tmap_2d_bf16(&g.tm_p_st[b], piece, p_lines, 64, 64, 32)) return rc;
+        }
+        float *dh_sums = reinterpret_cast<float *>(c.ws + p.off_dh);
+        if (int rc = make_tmap_2d(&g.tm_dh, dh_sums, (int64_t)p.splits * p.row_cap, p.dh_ld, p.dh_ld, 32, 32)) return rc;
         g.dw = dw;
         g.dw_bf16 = dw_type == STAGE_BF16;
         g.dw_add = accumulate != 0;
-        g.dw_vec = dim % 8 == 0 && aligned16(dw);
+        g.dw_tma = aligned16(dw) && dim * type_bytes(dw_type) % 16 == 0 && !(g.dw_bf16 && g.dw_add);
+        if (g.dw_tma && g.dw_bf16) {
+            if (int rc = make_tmap_2d_bf16(&g.tm_dw, dw, vocab, dim, dim, 32)) return rc;
+        } else if (g.dw_tma) {
+            if (int rc = make_tmap_2d(&g.tm_dw, static_cast<float *>(dw), vocab, dim, dim, 32, 32)) return rc;
+        }
         g.grad_scale = grad_scale;
         const int64_t m_tiles = p.row_cap / kHeadTileM, d_tiles = ceil_div(dim, kHeadTileN);
         for (int i = 0; i <= p.pieces; ++i) {
@@ -456,7 +480,7 @@ extern "C" int head_loss_grad(const void *h, const void *w, const void *targets,
             const bool vec = dim % 8 == 0 && aligned16(dh);
             auto *k = vec ? &head_dh_kernel<true> : &head_dh_kernel<false>;
             SPCO_LAUNCH("head_dh", c.st,
-                        k<<<grid, threads, 0, c.st>>>(g.dh, p.splits, p.row_cap, p.dh_ld,
+                        k<<<grid, threads, 0, c.st>>>(dh_sums, p.splits, p.row_cap, p.dh_ld,
                                                       reinterpret_cast<const int *>(c.ws + p.off_at), g.state,
                                                       grad_scale, (int)tokens, dim, static_cast<bf16 *>(dh)));
             SPECOPTIM_LAUNCHED("head_dh_kernel");
