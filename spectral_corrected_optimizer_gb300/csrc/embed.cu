@@ -26,10 +26,10 @@ namespace {
 // loads per thread, so a gather of 65536 rows keeps U x 16 or 32 bytes per
 // thread in flight.
 template <typename TI, typename TO, typename ID, bool VEC, int U>
-__global__ void __launch_bounds__(256) lookup_kernel(const TI *__restrict__ table, const ID *__restrict__ ids,
+__global__ void __launch_bounds__(256) lookup_kernel(const Span<const TI> table, const ID *__restrict__ ids,
                                                      int64_t tokens, int64_t vocab, int dim, float scale,
-                                                     TO *__restrict__ out, unsigned *flag) {
-    const int vecs = (dim + 7) / 8;
+                                                     const Span<TO> out, unsigned *flag) {
+    const int vecs = VEC ? dim / 8 : (dim + 14) / 8;
     for (int64_t t0 = (int64_t)blockIdx.x * U; t0 < tokens; t0 += (int64_t)gridDim.x * U) {
         int64_t id[U];
 #pragma unroll
@@ -41,15 +41,16 @@ __global__ void __launch_bounds__(256) lookup_kernel(const TI *__restrict__ tabl
             }
         }
         for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
-            const int n = dim - v * 8;
             float x[U][8];
+            int col[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (id[u] >= 0) {
-                    load8<VEC>(table + id[u] * dim + v * 8, n, x[u]);
-                } else {
+                col[u] = v * 8 - (VEC ? 0 : (int)((out.lo + (t0 + u) * dim) & 7));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+                for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+                if (id[u] >= 0) {
+                    if (VEC) load8(table.p + id[u] * dim + col[u], x[u]);
+                    else load_any(table, table.lo + id[u] * dim + col[u], x[u]);
                 }
             }
 #pragma unroll
@@ -57,7 +58,9 @@ __global__ void __launch_bounds__(256) lookup_kernel(const TI *__restrict__ tabl
                 if (t0 + u >= tokens) break;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[u][i] *= id[u] >= 0 ? scale : 0.f;
-                store8<VEC>(out + (t0 + u) * dim + v * 8, n, x[u]);
+                const int64_t row = out.lo + (t0 + u) * dim;
+                if (VEC) store8(out.p + row + col[u], x[u]);
+                else store_any(out, row + col[u], row, row + dim, x[u]);
             }
         }
     }
@@ -66,22 +69,18 @@ __global__ void __launch_bounds__(256) lookup_kernel(const TI *__restrict__ tabl
 template <typename TI, typename TO, typename ID>
 void launch_lookup(const void *table, const void *ids, int64_t tokens, int64_t vocab, int dim, float scale,
                    void *out, cudaStream_t st) {
-    const TI *tb = static_cast<const TI *>(table);
+    const Span<const TI> tb(static_cast<const TI *>(table), vocab * dim);
+    const Span<TO> o(static_cast<TO *>(out), tokens * dim);
     const ID *id = static_cast<const ID *>(ids);
-    TO *o = static_cast<TO *>(out);
-    const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim, 8), 32));
+    const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim + 7, 8), 32));
     const bool vec = dim % 8 == 0 && aligned16(table) && aligned16(out);
     const int64_t resident = (int64_t)num_sms() * 8;
     // few tokens: one per block, so that every row has an SM of its own
-    if (tokens <= resident) {
-        const int grid = (int)tokens;
-        if (vec) lookup_kernel<TI, TO, ID, true, 1><<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
-        else lookup_kernel<TI, TO, ID, false, 1><<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
-    } else {
-        const int grid = (int)std::min<int64_t>(ceil_div(tokens, 4), resident * 4);
-        if (vec) lookup_kernel<TI, TO, ID, true, 4><<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
-        else lookup_kernel<TI, TO, ID, false, 4><<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
-    }
+    const bool few = tokens <= resident;
+    const int grid = (int)(few ? tokens : std::min<int64_t>(ceil_div(tokens, 4), resident * 4));
+    auto *k = few ? (vec ? &lookup_kernel<TI, TO, ID, true, 1> : &lookup_kernel<TI, TO, ID, false, 1>)
+                  : (vec ? &lookup_kernel<TI, TO, ID, true, 4> : &lookup_kernel<TI, TO, ID, false, 4>);
+    k<<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
 }
 
 template <typename TI, typename TO>
@@ -217,42 +216,40 @@ struct Sorted {
     int64_t chunks;
 };
 
+// First column of a thread's 8 in row `row` of the gradient: rows that are not
+// multiples of 16 bytes begin `phase` values into a 16-byte piece.
+template <typename TG, bool VEC> __device__ __forceinline__ int phase(const Span<TG> &grad, int64_t row, int dim) {
+    return VEC ? 0 : (int)((grad.lo + row * dim) & 7);
+}
+
 template <typename TG, bool VEC>
-__device__ __forceinline__ void put_row(TG *grad, int64_t row, int dim, int col, float scale, bool accumulate,
-                                        float (&a)[8]) {
-    TG *p = grad + row * dim + col;
-    const int n = dim - col;
+__device__ __forceinline__ void put_row(const Span<TG> &grad, int64_t row, int dim, int j, float scale,
+                                        bool accumulate, float (&a)[8]) {
+    const int64_t from = grad.lo + row * dim, at = from + j * 8 - phase<TG, VEC>(grad, row, dim);
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] *= scale;
-    if (accumulate) {
+    if (accumulate) {  // nobody else writes these values, so the read-only path is safe
         float old[8];
-        if (VEC) {  // not through the read-only path: this kernel writes these rows
-            const volatile uint32_t *u = reinterpret_cast<const volatile uint32_t *>(p);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (sizeof(TG) == 4) old[i] = __uint_as_float(u[i]);
-                else old[i] = (i & 1) ? hi_f(u[i / 2]) : lo_f(u[i / 2]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) old[i] = i < n ? to_f(p[i]) : 0.f;
-        }
+        if (VEC) load8(static_cast<const TG *>(grad.p) + at, old);
+        else load_any(grad.read(), at, old);
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] += old[i];
     }
-    store8<VEC>(p, n, a);
+    if (VEC) store8(grad.p + at, a);
+    else store_any(grad, at, from, from + dim, a);
 }
 
 constexpr int kMaxChunk = 64, kBatch = 8, kZeroRows = 64;
 
 // Blocks [0, chunks * col_blocks): one chunk of the sorted list, 8 columns per
 // thread.  Blocks after them: kZeroRows rows each, zero-filled where the list
-// has no such id.  partial: [chunks][2][dim], slot 0 for a run that began
-// before the chunk, slot 1 for one that begins in it and goes on.
+// has no such id.  partial: [chunks][2][pitch], slot 0 for a run that began
+// before the chunk, slot 1 for one that begins in it and goes on; its columns
+// are shifted as the run's row is.
 template <typename TD, typename TG, bool VEC>
-__global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const TD *__restrict__ dy, int64_t vocab,
+__global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const Span<const TD> dy, int64_t vocab,
                                                           int dim, int col_blocks, float scale, bool accumulate,
-                                                          TG *__restrict__ grad, float *__restrict__ partial) {
+                                                          const Span<TG> grad, float *__restrict__ partial, int pitch) {
     __shared__ uint32_t sk[kMaxChunk + 2], sv[kMaxChunk];
     const int tid = threadIdx.x;
     const int64_t work = s.chunks * col_blocks;
@@ -270,16 +267,17 @@ __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const 
             present[i] = row >= vocab || (lo < s.n && (int64_t)s.keys[lo] == row);
         }
         __syncthreads();
-        const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int i = 0; i < kZeroRows; ++i) {
             if (present[i]) continue;
-            for (int col = tid * 8; col < dim; col += blockDim.x * 8)
-                store8<VEC>(grad + (row0 + i) * dim + col, dim - col, zero);
+            for (int j = tid; j * 8 < dim + (VEC ? 0 : 7); j += blockDim.x) {
+                float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                put_row<TG, VEC>(grad, row0 + i, dim, j, 0.f, false, zero);
+            }
         }
         return;
     }
     const int64_t c = (int64_t)blockIdx.x / col_blocks;
-    const int col = ((int)((int64_t)blockIdx.x % col_blocks) * (int)blockDim.x + tid) * 8;
+    const int j = (int)((int64_t)blockIdx.x % col_blocks) * (int)blockDim.x + tid;
     const int64_t p0 = c * s.chunk;
     const int len = (int)(s.n - p0 < s.chunk ? s.n - p0 : s.chunk);
     // keys of the chunk and of its two neighbours (~0: none)
@@ -289,34 +287,33 @@ __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const 
     }
     for (int i = tid; i < len; i += blockDim.x) sv[i] = s.vals[p0 + i];
     __syncthreads();
-    if (col >= dim) return;
-    const int n = dim - col;
+    if (j * 8 >= pitch) return;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     bool began = sk[0] != sk[1];  // whether the current run begins in this chunk
     for (int i0 = 0; i0 < len; i0 += kBatch) {
         float x[kBatch][8];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-            if (i0 + u < len) load8<VEC>(dy + (int64_t)sv[i0 + u] * dim + col, n, x[u]);
+        for (int u = 0; u < kBatch; ++u) {
+            if (i0 + u >= len) continue;
+            const int64_t at = dy.lo + (int64_t)sv[i0 + u] * dim + j * 8 - phase<TG, VEC>(grad, sk[i0 + u + 1], dim);
+            if (VEC) load8(dy.p + at, x[u]);
+            else load_any(dy, at, x[u]);
+        }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int i = i0 + u;
             if (i >= len) break;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += x[u][j];
+            for (int k = 0; k < 8; ++k) acc[k] += x[u][k];
             const uint32_t k = sk[i + 1], next = sk[i + 2];
             const bool run_ends = next != k;
             if (!run_ends && i + 1 < len) continue;
             if ((int64_t)k < vocab) {
-                if (began && run_ends) {
-                    put_row<TG, VEC>(grad, k, dim, col, scale, accumulate, acc);
-                } else {
-                    float *slot = partial + (c * 2 + (began ? 1 : 0)) * dim + col;
-                    store8<VEC>(slot, n, acc);
-                }
+                if (began && run_ends) put_row<TG, VEC>(grad, k, dim, j, scale, accumulate, acc);
+                else store8(partial + (c * 2 + (began ? 1 : 0)) * pitch + j * 8, acc);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+            for (int l = 0; l < 8; ++l) acc[l] = 0.f;
             began = true;
         }
     }
@@ -326,16 +323,16 @@ __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const 
 // on, its partial sums are added in chunk order and written to its row.
 template <typename TG, bool VEC>
 __global__ void __launch_bounds__(256) segment_join_kernel(const Sorted s, int64_t vocab, int dim, float scale,
-                                                           bool accumulate, TG *__restrict__ grad,
-                                                           const float *__restrict__ partial) {
+                                                           bool accumulate, const Span<TG> grad,
+                                                           const float *__restrict__ partial, int pitch) {
     const int64_t c = blockIdx.x;
     const int64_t p0 = c * s.chunk, p1 = p0 + s.chunk;
     if (p1 >= s.n) return;
     const uint32_t k = s.keys[p1 - 1];
     if ((int64_t)k >= vocab || s.keys[p1] != k) return;
     if (s.keys[p0] == k && p0 > 0 && s.keys[p0 - 1] == k) return;  // the run began earlier
-    const int col = ((int)blockIdx.y * (int)blockDim.x + threadIdx.x) * 8;
-    if (col >= dim) return;
+    const int j = (int)blockIdx.y * (int)blockDim.x + threadIdx.x;
+    if (j * 8 >= pitch) return;
     int64_t lo = p1, hi = s.n;  // first position behind the run
     while (lo < hi) {
         const int64_t mid = (lo + hi) >> 1;
@@ -343,17 +340,16 @@ __global__ void __launch_bounds__(256) segment_join_kernel(const Sorted s, int64
         else hi = mid;
     }
     const int64_t last = (lo - 1) / s.chunk;  // chunk of the run's last token
-    const int n = dim - col;
     float acc[8];
-    load8<VEC>(partial + (c * 2 + 1) * dim + col, n, acc);
+    load8(partial + (c * 2 + 1) * pitch + j * 8, acc);
 #pragma unroll 4
     for (int64_t i = c + 1; i <= last; ++i) {
         float x[8];
-        load8<VEC>(partial + i * 2 * dim + col, n, x);
+        load8(partial + i * 2 * pitch + j * 8, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += x[j];
+        for (int l = 0; l < 8; ++l) acc[l] += x[l];
     }
-    put_row<TG, VEC>(grad, k, dim, col, scale, accumulate, acc);
+    put_row<TG, VEC>(grad, k, dim, j, scale, accumulate, acc);
 }
 
 // Tokens per chunk: as many blocks as fill the GPU four times over, between 8
@@ -366,15 +362,16 @@ int chunk_len(int64_t tokens, int col_blocks) {
 }
 
 struct GradPlan {
-    int threads, col_blocks, chunk, passes;
+    int threads, col_blocks, chunk, passes, pitch;
     int64_t chunks, sort_blocks;
     int64_t off_hist, off_k0, off_v0, off_k1, off_v1, off_partial, bytes;
 };
 
-GradPlan plan_grad(int64_t tokens, int64_t vocab, int32_t dim) {
+GradPlan plan_grad(int64_t tokens, int64_t vocab, int32_t dim, bool vec) {
     GradPlan p{};
-    p.threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim, 8), 32));
-    p.col_blocks = (int)ceil_div(dim, (int64_t)p.threads * 8);
+    p.pitch = vec ? dim : (int)round_up(dim + 7, 8);  // with the start of the piece it begins in
+    p.threads = (int)std::min<int64_t>(256, round_up(p.pitch / 8, 32));
+    p.col_blocks = (int)ceil_div(p.pitch, (int64_t)p.threads * 8);
     p.chunk = chunk_len(tokens, p.col_blocks);
     p.chunks = ceil_div(tokens, p.chunk);
     p.sort_blocks = ceil_div(tokens, kTile);
@@ -392,7 +389,7 @@ GradPlan plan_grad(int64_t tokens, int64_t vocab, int32_t dim) {
     p.off_v0 = take(tokens * 4);
     p.off_k1 = take(tokens * 4);
     p.off_v1 = take(tokens * 4);
-    p.off_partial = take(p.chunks * 2 * dim * 4);
+    p.off_partial = take(p.chunks * 2 * p.pitch * 4);
     p.bytes = at;
     return p;
 }
@@ -432,17 +429,18 @@ int sort_tokens(const GradPlan &p, const ID *ids, int64_t tokens, int64_t vocab,
 template <typename TD, typename TG, bool VEC>
 int sum_segments(const GradPlan &p, const Sorted &s, const void *dy, int64_t vocab, int dim, float scale,
                  bool accumulate, void *grad, float *partial, cudaStream_t st) {
+    const Span<const TD> in(static_cast<const TD *>(dy), s.n * dim);
+    const Span<TG> out(static_cast<TG *>(grad), vocab * dim);
     const int64_t work = s.chunks * p.col_blocks + (accumulate ? 0 : ceil_div(vocab, kZeroRows));
     if (work > INT32_MAX) return fail(SPECOPTIM_ERR_NOT_IMPLEMENTED, "embed_grad: tokens x dim too large for one launch");
     if (work > 0)
         SPCO_LAUNCH("embed_segment_sum", st,
                     segment_sum_kernel<TD, TG, VEC><<<(unsigned)work, p.threads, 0, st>>>(
-                        s, static_cast<const TD *>(dy), vocab, dim, p.col_blocks, scale, accumulate,
-                        static_cast<TG *>(grad), partial));
+                        s, in, vocab, dim, p.col_blocks, scale, accumulate, out, partial, p.pitch));
     if (s.chunks > 1)
         SPCO_LAUNCH("embed_segment_join", st,
                     segment_join_kernel<TG, VEC><<<dim3((unsigned)s.chunks, p.col_blocks), p.threads, 0, st>>>(
-                        s, vocab, dim, scale, accumulate, static_cast<TG *>(grad), partial));
+                        s, vocab, dim, scale, accumulate, out, partial, p.pitch));
     SPECOPTIM_LAUNCHED("embed_grad sums");
     return SPECOPTIM_OK;
 }
@@ -495,7 +493,7 @@ extern "C" int64_t embed_grad_workspace(int64_t tokens, int64_t vocab, int32_t d
     int64_t bytes = -1;
     entry([&]() -> int {
         if (int rc = check_sizes(tokens, vocab, dim, "embed_grad")) return rc;
-        bytes = plan_grad(tokens, vocab, dim).bytes;
+        bytes = plan_grad(tokens, vocab, dim, false).bytes;  // the larger one: alignment is not known yet
         return SPECOPTIM_OK;
     });
     return bytes;
@@ -518,7 +516,8 @@ extern "C" int embed_grad(const void *ids, int32_t id_bytes, const void *dy, int
         if (!aligned_to(dy, type_bytes(dy_type)) || !aligned_to(grad, type_bytes(grad_type)) ||
             !aligned_to(ids, id_bytes) || !aligned16(workspace))
             return fail(SPECOPTIM_ERR_MISALIGNED, "embed_grad: pointers must be aligned to their elements, the workspace to 16 bytes");
-        const GradPlan p = plan_grad(tokens, vocab, dim);
+        const bool vec = dim % 8 == 0 && aligned16(dy) && aligned16(grad);
+        const GradPlan p = plan_grad(tokens, vocab, dim, vec);
         if (tokens > 0 && (!workspace || workspace_bytes < p.bytes))
             return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_grad: the workspace is smaller than embed_grad_workspace() says");
         if (int rc = bind_device()) return rc;
@@ -531,7 +530,6 @@ extern "C" int embed_grad(const void *ids, int32_t id_bytes, const void *dy, int
             if (rc) return rc;
         }
         float *partial = reinterpret_cast<float *>(ws + p.off_partial);
-        const bool vec = dim % 8 == 0 && aligned16(dy) && aligned16(grad);
         const bool acc = accumulate != 0;
         auto go = [&](auto td, auto tg) -> int {
             using TD = decltype(td);

@@ -208,28 +208,34 @@ __global__ void __launch_bounds__(1024) head_lse_kernel(const float2 *__restrict
     if (c == 0) *loss = l * state->inv_count;
 }
 
-// dh[t] = factor * sum over the parts of the token's row; zero without a target
+// dh[t] = factor * sum over the parts of the token's row; zero without a target.
+// The sums' rows are read from where dh's 16-byte pieces begin (VEC: column 0).
 template <bool VEC>
-__global__ void __launch_bounds__(256) head_dh_kernel(const float *__restrict__ sums, int parts, int row_cap, int ld,
+__global__ void __launch_bounds__(256) head_dh_kernel(const Span<const float> sums, int parts, int row_cap, int ld,
                                                       const int *__restrict__ at, const HeadState *__restrict__ state,
-                                                      float grad_scale, int tokens, int dim, bf16 *__restrict__ dh) {
+                                                      float grad_scale, int tokens, int dim, const Span<bf16> dh) {
     const float factor = grad_scale * state->inv_count;
     for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
         const int r = at[t];
-        for (int col = threadIdx.x * 8; col < dim; col += blockDim.x * 8) {
+        const int64_t row = dh.lo + (int64_t)t * dim;
+        const int first = VEC ? 0 : -(int)(row & 7);
+        for (int col = first + (int)threadIdx.x * 8; col < dim; col += blockDim.x * 8) {
             float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (r >= 0) {
 #pragma unroll 4
                 for (int p = 0; p < parts; ++p) {
                     float x[8];
-                    load8<true>(sums + ((int64_t)p * row_cap + r) * ld + col, 8, x);
+                    const int64_t at = ((int64_t)p * row_cap + r) * ld + col;
+                    if (VEC) load8(sums.p + at, x);
+                    else load_any(sums, at, x);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) a[i] += x[i];
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) a[i] *= factor;
             }
-            store8<VEC>(dh + (int64_t)t * dim + col, dim - col, a);
+            if (VEC) store8(dh.p + row + col, a);
+            else store_any(dh, row + col, row, row + dim, a);
         }
     }
 }
@@ -480,9 +486,11 @@ extern "C" int head_loss_grad(const void *h, const void *w, const void *targets,
             const bool vec = dim % 8 == 0 && aligned16(dh);
             auto *k = vec ? &head_dh_kernel<true> : &head_dh_kernel<false>;
             SPCO_LAUNCH("head_dh", c.st,
-                        k<<<grid, threads, 0, c.st>>>(dh_sums, p.splits, p.row_cap, p.dh_ld,
+                        k<<<grid, threads, 0, c.st>>>(Span<const float>(dh_sums, (int64_t)p.splits * p.row_cap * p.dh_ld),
+                                                      p.splits, p.row_cap, p.dh_ld,
                                                       reinterpret_cast<const int *>(c.ws + p.off_at), g.state,
-                                                      grad_scale, (int)tokens, dim, static_cast<bf16 *>(dh)));
+                                                      grad_scale, (int)tokens, dim,
+                                                      Span<bf16>(static_cast<bf16 *>(dh), tokens * dim)));
             SPECOPTIM_LAUNCHED("head_dh_kernel");
         }
         return SPECOPTIM_OK;

@@ -9,8 +9,10 @@
 // All of it is one pass over the data: a block holds a row in registers (8
 // values per thread and step), so the row is read once, its mean square and
 // its groups' maxima are reduced by shuffles, and everything derived from it is
-// written from the same registers.  A group of 128 values lies in 16
-// neighbouring lanes.  What bounds both directions is the DRAM traffic.
+// written from the same registers.  What bounds both directions is the DRAM
+// traffic.  Where rows are multiples of 16 bytes a group of 128 values lies in 16
+// neighbouring lanes; otherwise (rowvec.cuh) a thread's 8 values may belong to
+// two groups, and the groups' maxima meet in shared memory.
 //
 // The norm statistics and every sum are fp32.  The checkpoint is the only
 // tensor below 16 bits: e4m3 with a scale per 128 values keeps each value to
@@ -26,6 +28,7 @@ namespace spco {
 namespace {
 
 constexpr int kGroup = STAGE_CKPT_GROUP;
+constexpr int kMaxThreads = 512, kMaxDim = kMaxThreads * 8 * 8, kMaxGroups = kMaxDim / kGroup;
 constexpr float kFp8Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
 
@@ -60,166 +63,258 @@ __device__ __forceinline__ void from_fp8x4(uint32_t u, float *v) {
     }
 }
 
-template <bool VEC> __device__ __forceinline__ void load_q8(const uint8_t *p, int n, float (&v)[8]) {
-    uint32_t u[2] = {0, 0};
-    if (VEC) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-        u[0] = w.x;
-        u[1] = w.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) u[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+// Columns col .. col + 7 of the row that begins at `row`, as far as they lie in
+// [0, dim): a vector where the piece lies in the row and on a boundary.
+template <typename T>
+__device__ __forceinline__ void store_span(const Span<T> &s, int64_t row, int col, int dim, const float (&v)[8]) {
+    if (((row + col) & 7) == 0) {
+        store_any(s, row + col, row, row + dim, v);
+        return;
     }
-    from_fp8x4(u[0], v);
-    from_fp8x4(u[1], v + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (col + i >= 0 && col + i < dim) s.p[row + col + i] = from_f<T>(v[i]);
+}
+__device__ __forceinline__ void store_q8(const Span<uint8_t> &s, int64_t row, int col, int dim, uint2 v) {
+    if (col >= 0 && col + 8 <= dim && ((row + col) & 7) == 0) {
+        *reinterpret_cast<uint2 *>(s.p + row + col) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (col + i >= 0 && col + i < dim) s.p[row + col + i] = (uint8_t)((i < 4 ? v.x : v.y) >> (8 * (i & 3)));
 }
 
-template <bool VEC> __device__ __forceinline__ void store_q8(uint8_t *p, int n, uint32_t lo, uint32_t hi) {
-    if (VEC) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
-    } else {
+// largest magnitude of v[from..to), infinite where one of them is a NaN (fmaxf
+// drops it): the group's scale then marks the group
+__device__ __forceinline__ float magnitude(const float (&v)[8], int from, int to) {
+    float m = 0.f;
+    bool bad = false;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+    for (int i = 0; i < 8; ++i) {
+        if (i < from || i >= to) continue;
+        m = fmaxf(m, fabsf(v[i]));
+        bad |= v[i] != v[i];
     }
+    return bad ? __int_as_float(0x7f800000) : m;
+}
+__device__ __forceinline__ float scale_of(float m) { return fmaxf(m / kFp8Max, kTinyScale); }
+
+__device__ __forceinline__ void unpack_q8(uint2 u, float (&v)[8]) {
+    from_fp8x4(u.x, v);
+    from_fp8x4(u.y, v + 4);
+}
+
+// The tensors of one call as spans, and their width.  All of a type that are 16
+// byte aligned begin each row at the same place between two boundaries.
+template <typename T> struct Forward {
+    Span<const T> x, r, gamma;
+    Span<T> s, y;
+    Span<uint8_t> q;
+    float *scale, *rstd;
+    int64_t rows;
+    int dim;
+    float eps;
+};
+
+// q of the 8 values and their group's (or two groups') scales
+__device__ __forceinline__ uint2 quantise8(const float (&s)[8], float inv_lo, float inv_hi, int cut) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = s[i] * (i < cut ? inv_lo : inv_hi);
+    return make_uint2(to_fp8x4(t[0], t[1], t[2], t[3]), to_fp8x4(t[4], t[5], t[6], t[7]));
 }
 
 template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(512) resnorm_forward_kernel(
-    const T *x, const T *r, const T *__restrict__ gamma, float eps, T *s_out, T *__restrict__ y,
-    uint8_t *__restrict__ q, float *__restrict__ scale, float *__restrict__ rstd, int64_t rows, int dim) {
+__global__ void __launch_bounds__(512) resnorm_forward_kernel(const Forward<T> a) {
     __shared__ float red[2][32];
-    const int groups = (dim + kGroup - 1) / kGroup;
-    int parity = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
+    __shared__ int group_max[VEC ? 1 : 3][VEC ? 1 : kMaxGroups + 1];
+    const int dim = a.dim, groups = (dim + kGroup - 1) / kGroup;
+    if (!VEC) {
+        for (int i = threadIdx.x; i < 3 * (kMaxGroups + 1); i += blockDim.x) (&group_max[0][0])[i] = 0;
+        __syncthreads();
+    }
+    int parity = 0, turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1, turn = turn == 2 ? 0 : turn + 1) {
         const int64_t base = row * dim;
+        const int first = VEC ? 0 : -(int)((a.y.lo + base) & 7);  // column where the row's first piece begins
         float s[NV][8];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (k * blockDim.x + threadIdx.x) * 8;
-            if (col < dim) {
-                load8<VEC>(x + base + col, dim - col, s[k]);
-            } else {
+            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[k][i] = 0.f;
-            }
+            for (int i = 0; i < 8; ++i) s[k][i] = 0.f;
+            if (col >= dim) continue;
+            if (VEC) load8(a.x.p + base + col, s[k]);
+            else load_any(a.x, a.x.lo + base + col, s[k]);
         }
-        if (r) {
+        if (a.r.p) {
             float b[NV][8];
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = (k * blockDim.x + threadIdx.x) * 8;
-                if (col < dim) {
-                    load8<VEC>(r + base + col, dim - col, b[k]);
-                } else {
+                const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) b[k][i] = 0.f;
-                }
+                for (int i = 0; i < 8; ++i) b[k][i] = 0.f;
+                if (col >= dim) continue;
+                if (VEC) load8(a.r.p + base + col, b[k]);
+                else load_any(a.r, a.r.lo + base + col, b[k]);
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = (k * blockDim.x + threadIdx.x) * 8;
+                const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
                 // the stream is held in T: norm and checkpoint are those of the rounded sum
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s[k][i] = to_f(from_f<T>(s[k][i] + b[k][i]));
-                if (col < dim) store8<VEC>(s_out + base + col, dim - col, s[k]);
+                if (col >= dim) continue;
+                if (VEC) store8(a.s.p + base + col, s[k]);
+                else store_span(a.s, a.s.lo + base, col, dim, s[k]);
             }
         }
         float ss = 0.f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(s[k][i], s[k][i], ss);
-        // the checkpoint needs no row sum: it is written while the sum is under way
-#pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (k * blockDim.x + threadIdx.x) * 8;
-            float m = 0.f;
-            bool bad = false;
+            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                m = fmaxf(m, fabsf(s[k][i]));
-                bad |= s[k][i] != s[k][i];
-            }
-            if (bad) m = __int_as_float(0x7f800000);  // fmaxf drops NaN: an infinite scale marks the group
-#pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float sc = fmaxf(m / kFp8Max, kTinyScale);
-            const float inv = 1.f / sc;
-            if (col < dim) {
-                const uint32_t lo = to_fp8x4(s[k][0] * inv, s[k][1] * inv, s[k][2] * inv, s[k][3] * inv);
-                const uint32_t hi = to_fp8x4(s[k][4] * inv, s[k][5] * inv, s[k][6] * inv, s[k][7] * inv);
-                store_q8<VEC>(q + base + col, dim - col, lo, hi);
-                if ((threadIdx.x & 15) == 0) scale[row * groups + col / kGroup] = sc;
+                if (!VEC && (col + i < 0 || col + i >= dim)) s[k][i] = 0.f;  // the neighbouring rows' values
+                ss = fmaf(s[k][i], s[k][i], ss);
             }
         }
+        if (VEC) {
+            // the checkpoint needs no row sum: it is written while the sum is under way
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = (k * blockDim.x + threadIdx.x) * 8;
+                float m = magnitude(s[k], 0, 8);
+#pragma unroll
+                for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float sc = scale_of(m), inv = 1.f / sc;
+                if (col >= dim) continue;
+                *reinterpret_cast<uint2 *>(a.q.p + a.q.lo + base + col) = quantise8(s[k], inv, inv, 8);
+                if ((threadIdx.x & 15) == 0) a.scale[row * groups + col / kGroup] = sc;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+                if (col >= dim) continue;
+                const int g = max(col, 0) / kGroup, cut = min(8, (g + 1) * kGroup - col);
+                atomicMax(&group_max[turn][g], __float_as_int(magnitude(s[k], 0, cut)));
+                if (cut < 8) atomicMax(&group_max[turn][g + 1], __float_as_int(magnitude(s[k], cut, 8)));
+            }
+            __syncwarp();  // one warp: block_sum has no barrier
+        }
         ss = block_sum(ss, red[parity]);
-        const float rs = 1.f / sqrtf(ss / (float)dim + eps);
-        if (threadIdx.x == 0) rstd[row] = rs;
+        const float rs = 1.f / sqrtf(ss / (float)dim + a.eps);
+        if (threadIdx.x == 0) a.rstd[row] = rs;
+        if (!VEC) {
+            // the previous row's maxima have been read by all; they are used again the row after next
+            int *stale = group_max[turn == 0 ? 2 : turn - 1];
+            for (int i = threadIdx.x; i < groups; i += blockDim.x) {
+                stale[i] = 0;
+                a.scale[row * groups + i] = scale_of(__int_as_float(group_max[turn][i]));
+            }
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+                if (col >= dim) continue;
+                const int g = max(col, 0) / kGroup, cut = min(8, (g + 1) * kGroup - col);
+                const float lo = 1.f / scale_of(__int_as_float(group_max[turn][g]));
+                const float hi = cut < 8 ? 1.f / scale_of(__int_as_float(group_max[turn][g + 1])) : lo;
+                store_q8(a.q, a.q.lo + base, col, dim, quantise8(s[k], lo, hi, cut));
+            }
+        }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (k * blockDim.x + threadIdx.x) * 8;
+            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
             if (col >= dim) continue;
             float g[8];
-            load8<VEC>(gamma + col, dim - col, g);
+            if (VEC) load8(a.gamma.p + col, g);
+            else load_any(a.gamma, a.gamma.lo + col, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[k][i] = s[k][i] * rs * g[i];
-            store8<VEC>(y + base + col, dim - col, s[k]);
+            if (VEC) store8(a.y.p + base + col, s[k]);
+            else store_span(a.y, a.y.lo + base, col, dim, s[k]);
         }
     }
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) resnorm_recompute_kernel(const uint8_t *__restrict__ q,
-                                                                const float *__restrict__ scale,
-                                                                const float *__restrict__ rstd,
-                                                                const T *__restrict__ gamma, T *__restrict__ y,
-                                                                int64_t rows, int dim) {
-    const int vecs = (dim + 7) / 8, groups = (dim + kGroup - 1) / kGroup;
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        const float rs = rstd[row];
-        for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
-            const int col = v * 8;
-            const float sc = scale[row * groups + col / kGroup];
-            float n[8], g[8];
-            load_q8<VEC>(q + row * dim + col, dim - col, n);
-            load8<VEC>(gamma + col, dim - col, g);
+template <typename T> struct Backward {
+    Span<const T> dy, ds, gamma;
+    Span<const uint8_t> q;
+    const float *scale, *rstd;
+    Span<T> dx, y;
+    float *partial;
+    int64_t rows;
+    int dim, pitch;
+};
+
+// n of 8 values: q times the scale of their group (or two groups) times rstd, 0
+// outside the row
+template <bool VEC>
+__device__ __forceinline__ void load_n(const Span<const uint8_t> &q, const float *scale, int64_t row, int groups,
+                                       int col, int dim, float rs, float (&n)[8]) {
+    const int64_t at = q.lo + row * dim + col;
+    unpack_q8(VEC ? __ldg(reinterpret_cast<const uint2 *>(q.p + at)) : load_any8(q, at), n);
+    const int g = VEC ? col / kGroup : max(col, 0) / kGroup, cut = VEC ? 8 : min(8, (g + 1) * kGroup - col);
+    const float lo = __ldg(scale + row * groups + g);
+    const float hi = !VEC && cut < 8 && g + 1 < groups ? __ldg(scale + row * groups + g + 1) : lo;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) n[i] = n[i] * sc * rs * g[i];
-            store8<VEC>(y + row * dim + col, dim - col, n);
+    for (int i = 0; i < 8; ++i) {
+        n[i] = n[i] * (i < cut ? lo : hi) * rs;
+        if (!VEC && (col + i < 0 || col + i >= dim)) n[i] = 0.f;
+    }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) resnorm_recompute_kernel(const Backward<T> a) {
+    const int dim = a.dim, groups = (dim + kGroup - 1) / kGroup;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const float rs = a.rstd[row];
+        const int first = VEC ? 0 : -(int)((a.y.lo + row * dim) & 7);
+        for (int col = first + (int)threadIdx.x * 8; col < dim; col += blockDim.x * 8) {
+            float n[8], g[8];
+            load_n<VEC>(a.q, a.scale, row, groups, col, dim, rs, n);
+            if (VEC) load8(a.gamma.p + col, g);
+            else load_any(a.gamma, a.gamma.lo + col, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[i] *= g[i];
+            if (VEC) store8(a.y.p + row * dim + col, n);
+            else store_span(a.y, a.y.lo + row * dim, col, dim, n);
         }
     }
 }
 
 // Each block keeps its columns' share of dgamma in registers over all its rows
-// and writes it once, to partial[block][dim].
+// and writes it once, to partial[block][pitch].  Where rows begin at different
+// places, a block's rows lie a multiple of 8 rows apart and so begin alike.
 template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(512) resnorm_backward_kernel(
-    const T *dy, const T *ds, const uint8_t *__restrict__ q, const float *__restrict__ scale,
-    const float *__restrict__ rstd, const T *__restrict__ gamma, T *dx, T *__restrict__ y,
-    float *__restrict__ partial, int64_t rows, int dim) {
+__global__ void __launch_bounds__(512) resnorm_backward_kernel(const Backward<T> a) {
     __shared__ float red[2][32];
-    const int groups = (dim + kGroup - 1) / kGroup;
+    const int dim = a.dim, groups = (dim + kGroup - 1) / kGroup;
+    const int first = VEC ? 0 : -(int)((a.dx.lo + (int64_t)blockIdx.x * dim) & 7);
     float dg[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dg[k][i] = 0.f;
     int parity = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
         const int64_t base = row * dim;
-        const float rs = rstd[row];
+        const float rs = a.rstd[row];
         float n[NV][8], d[NV][8];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (k * blockDim.x + threadIdx.x) * 8;
+            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
             if (col < dim) {
-                load8<VEC>(dy + base + col, dim - col, d[k]);
-                load_q8<VEC>(q + base + col, dim - col, n[k]);
-                const float sc = scale[row * groups + col / kGroup];
+                if (VEC) load8(a.dy.p + base + col, d[k]);
+                else load_any(a.dy, a.dy.lo + base + col, d[k]);
+                load_n<VEC>(a.q, a.scale, row, groups, col, dim, rs, n[k]);
+                if (!VEC) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) n[k][i] = n[k][i] * sc * rs;
+                    for (int i = 0; i < 8; ++i)
+                        if (col + i < 0 || col + i >= dim) d[k][i] = 0.f;
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[k][i] = n[k][i] = 0.f;
@@ -228,10 +323,11 @@ __global__ void __launch_bounds__(512) resnorm_backward_kernel(
         float t = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (k * blockDim.x + threadIdx.x) * 8;
+            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
             if (col >= dim) continue;
             float g[8];
-            load8<VEC>(gamma + col, dim - col, g);  // stays in L1 over the rows
+            if (VEC) load8(a.gamma.p + col, g);  // stays in L1 over the rows
+            else load_any(a.gamma, a.gamma.lo + col, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dg[k][i] = fmaf(d[k][i], n[k][i], dg[k][i]);
@@ -239,37 +335,51 @@ __global__ void __launch_bounds__(512) resnorm_backward_kernel(
                 t = fmaf(d[k][i], n[k][i], t);
                 g[i] *= n[k][i];
             }
-            if (y) store8<VEC>(y + base + col, dim - col, g);
+            if (!a.y.p) continue;
+            if (VEC) store8(a.y.p + base + col, g);
+            else store_span(a.y, a.y.lo + base, col, dim, g);
         }
         t = block_sum(t, red[parity]) / (float)dim;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (k * blockDim.x + threadIdx.x) * 8;
+            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
             if (col >= dim) continue;
             float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (ds) load8<VEC>(ds + base + col, dim - col, b);
+            if (a.ds.p) {
+                if (VEC) load8(a.ds.p + base + col, b);
+                else load_any(a.ds, a.ds.lo + base + col, b);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) b[i] = fmaf(rs, d[k][i] - n[k][i] * t, b[i]);
-            store8<VEC>(dx + base + col, dim - col, b);
+            if (VEC) store8(a.dx.p + base + col, b);
+            else store_span(a.dx, a.dx.lo + base, col, dim, b);
         }
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int col = (k * blockDim.x + threadIdx.x) * 8;
-        if (col < dim) store8<VEC>(partial + (int64_t)blockIdx.x * dim + col, dim - col, dg[k]);
+        const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+        if (col >= dim) continue;
+        float *out = a.partial + (int64_t)blockIdx.x * a.pitch;
+        if (VEC) {
+            store8(out + col, dg[k]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i >= 0 && col + i < dim) out[col + i] = dg[k][i];
+        }
     }
 }
 
 // dgamma[j] = sum over blocks of partial[block][j]: 32 columns per block, 8
 // threads per column, joined in a fixed order.
 __global__ void __launch_bounds__(256) dgamma_kernel(const float *__restrict__ partial, int blocks, int dim,
-                                                     float *__restrict__ dgamma) {
+                                                     int pitch, float *__restrict__ dgamma) {
     __shared__ float red[8][33];
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
     float a = 0.f;
     if (col < dim) {
 #pragma unroll 8
-        for (int b = w; b < blocks; b += 8) a += partial[(int64_t)b * dim + col];
+        for (int b = w; b < blocks; b += 8) a += partial[(int64_t)b * pitch + col];
     }
     red[w][c] = a;
     __syncthreads();
@@ -284,9 +394,8 @@ __global__ void __launch_bounds__(256) dgamma_kernel(const float *__restrict__ p
 struct Shape {
     int nv, threads;
 };
-constexpr int kMaxThreads = 512, kMaxDim = kMaxThreads * 8 * 8;
-Shape shape_of(int dim) {
-    const int64_t vecs = ceil_div(dim, 8);
+Shape shape_of(int dim, bool vec) {
+    const int64_t vecs = vec ? dim / 8 : (dim + 14) / 8;  // 8-value pieces that a row can touch
     int nv = 1;
     while (nv < 8 && (vecs > kMaxThreads * nv || (nv < 2 && vecs > 32))) nv *= 2;
     return {nv, (int)round_up(ceil_div(vecs, nv), 32)};
@@ -303,9 +412,10 @@ template <typename F> int with_nv(int nv, F &&f) {
 
 constexpr int kBackwardBlocksPerSm = 8;
 
+// A multiple of 8 where there are that many rows (see resnorm_backward_kernel)
 int backward_blocks(int64_t rows, const Shape &sh) {
     const int per_sm = std::max(1, std::min(kBackwardBlocksPerSm, 1024 / sh.threads));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms() * per_sm));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms() * per_sm / 8 * 8));
 }
 
 int check_sizes(int64_t rows, int32_t dim, int32_t type, const char *what) {
@@ -317,42 +427,33 @@ int check_sizes(int64_t rows, int32_t dim, int32_t type, const char *what) {
     return SPECOPTIM_OK;
 }
 
-template <typename T>
-int run_forward(const Shape &sh, bool vec, const void *x, const void *r, const void *gamma, float eps, void *s, void *y,
-                void *q, float *scale, float *rstd, int64_t rows, int dim, cudaStream_t st) {
+template <typename T> int run_forward(const Shape &sh, bool vec, const Forward<T> &a, cudaStream_t st) {
     return with_nv(sh.nv, [&](auto nv) -> int {
         constexpr int NV = decltype(nv)::value;
-        const int grid = (int)std::min<int64_t>(rows, (int64_t)num_sms() * 64);
+        const int grid = (int)std::min<int64_t>(a.rows, (int64_t)num_sms() * 64);
         auto *k = vec ? &resnorm_forward_kernel<T, true, NV> : &resnorm_forward_kernel<T, false, NV>;
-        SPCO_LAUNCH("resnorm_forward", st,
-                    k<<<grid, sh.threads, 0, st>>>(static_cast<const T *>(x), static_cast<const T *>(r),
-                                                   static_cast<const T *>(gamma), eps, static_cast<T *>(s),
-                                                   static_cast<T *>(y), static_cast<uint8_t *>(q), scale, rstd, rows,
-                                                   dim));
+        SPCO_LAUNCH("resnorm_forward", st, k<<<grid, sh.threads, 0, st>>>(a));
         SPECOPTIM_LAUNCHED("resnorm_forward_kernel");
         return SPECOPTIM_OK;
     });
 }
 
 template <typename T>
-int run_backward(const Shape &sh, bool vec, int blocks, const void *dy, const void *ds, const void *q,
-                 const float *scale, const float *rstd, const void *gamma, void *dx, float *dgamma, void *y,
-                 int64_t rows, int dim, float *partial, cudaStream_t st) {
+int run_backward(const Shape &sh, bool vec, int blocks, const Backward<T> &a, float *dgamma, cudaStream_t st) {
     return with_nv(sh.nv, [&](auto nv) -> int {
         constexpr int NV = decltype(nv)::value;
         auto *k = vec ? &resnorm_backward_kernel<T, true, NV> : &resnorm_backward_kernel<T, false, NV>;
-        SPCO_LAUNCH("resnorm_backward", st,
-                    k<<<blocks, sh.threads, 0, st>>>(static_cast<const T *>(dy), static_cast<const T *>(ds),
-                                                     static_cast<const uint8_t *>(q), scale, rstd,
-                                                     static_cast<const T *>(gamma), static_cast<T *>(dx),
-                                                     static_cast<T *>(y), partial, rows, dim));
+        SPCO_LAUNCH("resnorm_backward", st, k<<<blocks, sh.threads, 0, st>>>(a));
         SPECOPTIM_LAUNCHED("resnorm_backward_kernel");
         SPCO_LAUNCH("resnorm_dgamma", st,
-                    dgamma_kernel<<<(unsigned)ceil_div(dim, 32), 256, 0, st>>>(partial, blocks, dim, dgamma));
+                    dgamma_kernel<<<(unsigned)ceil_div(a.dim, 32), 256, 0, st>>>(a.partial, blocks, a.dim, a.pitch, dgamma));
         SPECOPTIM_LAUNCHED("dgamma_kernel");
         return SPECOPTIM_OK;
     });
 }
+
+// f(T{}) for the tensors' type
+template <typename F> int with_type(int32_t type, F &&f) { return type == STAGE_BF16 ? f(bf16{}) : f(float{}); }
 
 }  // namespace
 }  // namespace spco
@@ -374,10 +475,23 @@ extern "C" int resnorm_forward(const void *x, const void *r, const void *gamma, 
         if (int rc = bind_device()) return rc;
         const bool vec = dim % 8 == 0 && aligned16(x) && aligned16(r) && aligned16(gamma) && aligned16(y) &&
                          (!r || aligned16(s)) && aligned_to(q, 8);
-        const Shape sh = shape_of(dim);
-        cudaStream_t st = static_cast<cudaStream_t>(stream);
-        return type == STAGE_BF16 ? run_forward<bf16>(sh, vec, x, r, gamma, eps, s, y, q, scale, rstd, rows, dim, st)
-                                  : run_forward<float>(sh, vec, x, r, gamma, eps, s, y, q, scale, rstd, rows, dim, st);
+        const Shape sh = shape_of(dim, vec);
+        const int64_t n = rows * dim;
+        return with_type(type, [&](auto t) -> int {
+            using T = decltype(t);
+            const Forward<T> a{{static_cast<const T *>(x), n},
+                               {static_cast<const T *>(r), n},
+                               {static_cast<const T *>(gamma), dim},
+                               {static_cast<T *>(s), n},
+                               {static_cast<T *>(y), n},
+                               {static_cast<uint8_t *>(q), n},
+                               scale,
+                               rstd,
+                               rows,
+                               dim,
+                               eps};
+            return run_forward<T>(sh, vec, a, static_cast<cudaStream_t>(stream));
+        });
     });
 }
 
@@ -393,19 +507,29 @@ extern "C" int resnorm_recompute(const void *q, const float *scale, const float 
             return fail(SPECOPTIM_ERR_MISALIGNED, "resnorm_recompute: pointers must be aligned to their elements");
         if (int rc = bind_device()) return rc;
         const bool vec = dim % 8 == 0 && aligned16(gamma) && aligned16(y) && aligned_to(q, 8);
-        const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim, 8), 32));
+        const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim + 7, 8), 32));
         const int grid = (int)std::min<int64_t>(rows, (int64_t)num_sms() * 64);
+        const int64_t n = rows * dim;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
-        auto go = [&](auto t) -> int {
+        return with_type(type, [&](auto t) -> int {
             using T = decltype(t);
+            const Backward<T> a{{nullptr, 0},
+                                {nullptr, 0},
+                                {static_cast<const T *>(gamma), dim},
+                                {static_cast<const uint8_t *>(q), n},
+                                scale,
+                                rstd,
+                                {nullptr, 0},
+                                {static_cast<T *>(y), n},
+                                nullptr,
+                                rows,
+                                dim,
+                                dim};
             auto *k = vec ? &resnorm_recompute_kernel<T, true> : &resnorm_recompute_kernel<T, false>;
-            SPCO_LAUNCH("resnorm_recompute", st,
-                        k<<<grid, threads, 0, st>>>(static_cast<const uint8_t *>(q), scale, rstd,
-                                                    static_cast<const T *>(gamma), static_cast<T *>(y), rows, dim));
+            SPCO_LAUNCH("resnorm_recompute", st, k<<<grid, threads, 0, st>>>(a));
             SPECOPTIM_LAUNCHED("resnorm_recompute_kernel");
             return SPECOPTIM_OK;
-        };
-        return type == STAGE_BF16 ? go(bf16{}) : go(float{});
+        });
     });
 }
 
@@ -413,7 +537,9 @@ extern "C" int64_t resnorm_backward_workspace(int64_t rows, int32_t dim) {
     int64_t bytes = -1;
     entry([&]() -> int {
         if (int rc = check_sizes(rows, dim, STAGE_BF16, "resnorm_backward")) return rc;
-        bytes = (int64_t)backward_blocks(rows, shape_of(dim)) * dim * 4;
+        // of the two shapes the one with more blocks: the pointers' alignment is not known yet
+        bytes = (int64_t)std::max(backward_blocks(rows, shape_of(dim, true)), backward_blocks(rows, shape_of(dim, false))) *
+                round_up(dim, 8) * 4;
         return SPECOPTIM_OK;
     });
     return bytes;
@@ -431,17 +557,29 @@ extern "C" int resnorm_backward(const void *dy, const void *ds, const void *q, c
             !aligned_to(y, b) || !aligned_to(scale, 4) || !aligned_to(rstd, 4) || !aligned_to(dgamma, 4) ||
             !aligned16(workspace))
             return fail(SPECOPTIM_ERR_MISALIGNED, "resnorm_backward: pointers must be aligned to their elements, the workspace to 16 bytes");
-        const Shape sh = shape_of(dim);
-        const int blocks = backward_blocks(rows, sh);
-        if (workspace_bytes < (int64_t)blocks * dim * 4)
-            return fail(SPECOPTIM_ERR_INVALID_ARG, "resnorm_backward: the workspace is smaller than resnorm_backward_workspace() says");
-        if (int rc = bind_device()) return rc;
         const bool vec = dim % 8 == 0 && aligned16(dy) && aligned16(ds) && aligned16(gamma) && aligned16(dx) &&
                          aligned16(y) && aligned_to(q, 8);
-        float *partial = static_cast<float *>(workspace);
-        cudaStream_t st = static_cast<cudaStream_t>(stream);
-        return type == STAGE_BF16
-                   ? run_backward<bf16>(sh, vec, blocks, dy, ds, q, scale, rstd, gamma, dx, dgamma, y, rows, dim, partial, st)
-                   : run_backward<float>(sh, vec, blocks, dy, ds, q, scale, rstd, gamma, dx, dgamma, y, rows, dim, partial, st);
+        const Shape sh = shape_of(dim, vec);
+        const int blocks = backward_blocks(rows, sh), pitch = (int)round_up(dim, 8);
+        if (workspace_bytes < (int64_t)blocks * pitch * 4)
+            return fail(SPECOPTIM_ERR_INVALID_ARG, "resnorm_backward: the workspace is smaller than resnorm_backward_workspace() says");
+        if (int rc = bind_device()) return rc;
+        const int64_t n = rows * dim;
+        return with_type(type, [&](auto t) -> int {
+            using T = decltype(t);
+            const Backward<T> a{{static_cast<const T *>(dy), n},
+                                {static_cast<const T *>(ds), n},
+                                {static_cast<const T *>(gamma), dim},
+                                {static_cast<const uint8_t *>(q), n},
+                                scale,
+                                rstd,
+                                {static_cast<T *>(dx), n},
+                                {static_cast<T *>(y), n},
+                                static_cast<float *>(workspace),
+                                rows,
+                                dim,
+                                pitch};
+            return run_backward<T>(sh, vec, blocks, a, dgamma, static_cast<cudaStream_t>(stream));
+        });
     });
 }

@@ -1,6 +1,13 @@
 // Row vectors of the stage-end operators: 8 consecutive values of a row as
-// floats, loaded and stored in 16-byte pieces where the tensor allows it, value
-// by value otherwise; argument checks and the exception guard of their entries.
+// floats; argument checks and the exception guard of their entries.
+//
+// Where rows are multiples of 16 bytes (VEC), a thread's 8 values are one or two
+// 16-byte accesses.  Otherwise every row starts at another place between two
+// 16-byte boundaries: the threads then take the 8-value pieces of memory that
+// the row's output lies in (its first piece begins up to 7 values before the
+// row), store whole pieces as vectors and only the row's two ends value by
+// value, and read their inputs as the two pieces around them, shifted into
+// place (Span::load).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -31,45 +38,124 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// v = p[0..7] (positions >= n are 0); VEC: p is 16-byte aligned and n >= 8
-template <bool VEC> __device__ __forceinline__ void load8(const bf16 *p, int n, float (&v)[8]) {
-    if (VEC) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-        v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
-        v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
-    }
+// p[0..7] of a 16-byte aligned address
+__device__ __forceinline__ void load8(const bf16 *p, float (&v)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
+    v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
 }
-template <bool VEC> __device__ __forceinline__ void load8(const float *p, int n, float (&v)[8]) {
-    if (VEC) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.f;
-    }
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-template <bool VEC> __device__ __forceinline__ void store8(bf16 *p, int n, const float (&v)[8]) {
-    if (VEC) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                   pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = from_f<bf16>(v[i]);
-    }
+__device__ __forceinline__ void store8(bf16 *p, const float (&v)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                               pack_bf16(v[6], v[7]));
 }
-template <bool VEC> __device__ __forceinline__ void store8(float *p, int n, const float (&v)[8]) {
-    if (VEC) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = v[i];
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// A tensor of `count` values as 16-byte pieces: `p` is its address rounded down to
+// 16 bytes, its values have the indexes [lo, hi) from there.
+template <typename T> struct Span {
+    T *p;
+    int64_t lo, hi;
+
+    __host__ __device__ Span(T *q, int64_t count) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(q);
+        p = reinterpret_cast<T *>(a & ~uintptr_t(15));
+        lo = (int64_t)((a & 15) / sizeof(T));
+        hi = lo + count;
     }
+    __host__ __device__ Span(T *base, int64_t from, int64_t to) : p(base), lo(from), hi(to) {}
+    __host__ __device__ Span<const T> read() const { return Span<const T>(p, lo, hi); }
+};
+
+// words o .. o + 3 (o < 4) of 8
+__device__ __forceinline__ void pick_words(const uint32_t (&w)[8], int o, uint32_t (&r)[5]) {
+    uint32_t t[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) t[i] = (o & 2) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) r[i] = (o & 1) ? t[i + 1] : t[i];
+}
+
+// values i .. i + 7 of the span; 0 outside it
+__device__ __forceinline__ void load_any(const Span<const bf16> &s, int64_t i, float (&v)[8]) {
+    const int64_t a = i & ~(int64_t)7;
+    const int sh = (int)(i & 7);
+    if (a >= s.lo && a + (sh ? 16 : 8) <= s.hi) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(s.p + a);
+        const uint4 x = __ldg(q);
+        uint32_t r[5] = {x.x, x.y, x.z, x.w, 0};
+        if (sh) {
+            const uint4 y = __ldg(q + 1);
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            pick_words(w, sh >> 1, r);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t u = (sh & 1) ? __funnelshift_r(r[k], r[k + 1], 16) : r[k];
+            v[2 * k] = lo_f(u);
+            v[2 * k + 1] = hi_f(u);
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = i + k >= s.lo && i + k < s.hi ? to_f(s.p[i + k]) : 0.f;
+}
+__device__ __forceinline__ void load_any(const Span<const float> &s, int64_t i, float (&v)[8]) {
+    const int64_t a = i & ~(int64_t)3;
+    const int sh = (int)(i & 3);
+    if (a >= s.lo && a + (sh ? 12 : 8) <= s.hi) {
+        const float4 *q = reinterpret_cast<const float4 *>(s.p + a);
+        const float4 x = __ldg(q), y = __ldg(q + 1);
+        float w[12] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, 0.f, 0.f, 0.f, 0.f};
+        if (sh) {
+            const float4 z = __ldg(q + 2);
+            w[8] = z.x; w[9] = z.y; w[10] = z.z; w[11] = z.w;
+        }
+        float t[10];
+#pragma unroll
+        for (int k = 0; k < 10; ++k) t[k] = (sh & 2) ? w[k + 2] : w[k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = (sh & 1) ? t[k + 1] : t[k];
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = i + k >= s.lo && i + k < s.hi ? s.p[i + k] : 0.f;
+}
+// 8 bytes, packed
+__device__ __forceinline__ uint2 load_any8(const Span<const uint8_t> &s, int64_t i) {
+    const int64_t a = i & ~(int64_t)7;
+    const int sh = (int)(i & 7);
+    if (a >= s.lo && a + (sh ? 16 : 8) <= s.hi) {
+        const uint2 *q = reinterpret_cast<const uint2 *>(s.p + a);
+        const uint2 x = __ldg(q);
+        if (!sh) return x;
+        const uint2 y = __ldg(q + 1);
+        const uint32_t w0 = (sh & 4) ? x.y : x.x, w1 = (sh & 4) ? y.x : x.y, w2 = (sh & 4) ? y.y : y.x;
+        return make_uint2(__funnelshift_r(w0, w1, 8 * (sh & 3)), __funnelshift_r(w1, w2, 8 * (sh & 3)));
+    }
+    uint32_t u[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (i + k >= s.lo && i + k < s.hi) u[k / 4] |= (uint32_t)s.p[i + k] << (8 * (k & 3));
+    return make_uint2(u[0], u[1]);
+}
+
+// v to i .. i + 7 of those that lie in [from, to); i is a multiple of 8
+template <typename T>
+__device__ __forceinline__ void store_any(const Span<T> &s, int64_t i, int64_t from, int64_t to, const float (&v)[8]) {
+    if (i >= from && i + 8 <= to) {
+        store8(s.p + i, v);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (i + k >= from && i + k < to) s.p[i + k] = from_f<T>(v[k]);
 }
 
 inline size_t type_bytes(int32_t type) { return type == STAGE_BF16 ? 2 : 4; }

@@ -292,6 +292,54 @@ def test_residual_norm_backward_against_differences():
     assert bool(((dgamma.cpu().double() - fg).abs() <= 1e-5 * (fg.abs() + 1)).all())
 
 
+def shifted(t, by):
+    """The same values in a contiguous CUDA view that begins `by` elements behind a 16-byte boundary."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device="cuda")
+    view = buf[by:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("dim,by", [(256, 1), (131, 3), (9, 5)])
+def test_operators_on_unaligned_views(dtype, dim, by):
+    # tensors of one call that begin at different places between two 16-byte boundaries
+    x, r, gamma, g = norm_inputs(30, dim, dtype, True, seed=5)
+    kept, s, y = se().residual_norm(shifted(x, by), shifted(r, 2), shifted(gamma, 1), 1e-5)
+    plain = se().residual_norm(x.cuda(), r.cuda(), gamma.cuda(), 1e-5)
+    assert torch.equal(s, plain[1]) and torch.equal(kept.q.view(torch.uint8), plain[0].q.view(torch.uint8))
+    want_y, _ = ref.norm_forward(s.cpu(), gamma, 1e-5)
+    assert bool(((y.cpu().double() - want_y).abs() <= (u_of(dtype) + 104 * U32) * want_y.abs()).all())
+    dy = randn(g, x.shape, dtype)
+    kept = se().NormCheckpoint(shifted(kept.q.view(torch.uint8), by).view(torch.float8_e4m3fn), kept.scale, kept.rstd)
+    dx, dgamma, y2 = se().residual_norm_backward(shifted(dy, 4), kept, shifted(gamma, 3), ds=shifted(r, by), recompute=True)
+    w = ref.norm_backward(dy, r, kept.q.cpu(), kept.scale.cpu(), kept.rstd.cpu(), gamma)
+    assert bool(((dx.cpu().double() - w[0]).abs() <= u_of(dtype) * w[0].abs() + 100 * U32 * w[1]).all())
+    assert bool(((dgamma.cpu().double() - w[2]).abs() <= 40 * U32 * w[3]).all())
+    assert bool(((y2.cpu().double() - w[4]).abs() <= (u_of(dtype) + 4 * U32) * w[4].abs()).all())
+    assert torch.equal(se().residual_norm_recompute(kept, shifted(gamma, 5)), y2)
+
+    ids = zipf(g, 30, 17)
+    out = shifted(torch.zeros(17, dim, dtype=dtype), by)
+    check_grad(se().embed_grad(shifted(ids, 1), shifted(dy, 3), 17, out=out), ids, dy, 17, 1.0)
+    check_grad(se().embed_grad(ids.cuda(), shifted(dy, 6), 17, out=out, accumulate=True), ids, dy, 17, 1.0,
+               before=ref.embed_grad(ids, dy, 17, 1.0)[0].to(dtype))
+    table = randn(g, (17, dim), dtype)
+    out = shifted(torch.zeros(30, dim, dtype=BF), 7)
+    got = se().embed_lookup(shifted(table, by), ids.cuda(), scale=3.0, out=out)
+    assert torch.equal(got.cpu(), (table[ids].float() * 3).to(BF))
+
+
+@pytest.mark.parametrize("dim", [64, 72, 33])
+def test_head_with_unaligned_hidden_states_and_gradient(dim):
+    h, w, target = head_inputs(90, 700, dim, seed=9)
+    dw = shifted(torch.zeros(700, dim), 1)
+    loss, row_loss, dh, dw = se().head_loss_grad(shifted(h, 3), w.cuda(), shifted(target, 1), dw=dw)
+    want = ref.head(h, w, target)
+    check_loss(loss, row_loss, want, dim)
+    check_grads(dh, dw, want, h, w)
+
+
 # ---------------------------------------------------------------- head
 
 HEADS = [(1, 3, 8), (1, 1000, 64), (5, 257, 72), (130, 300, 64), (128, 256, 128), (300, 1111, 200), (257, 5000, 136),
