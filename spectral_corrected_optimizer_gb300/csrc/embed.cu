@@ -11,7 +11,7 @@
 // its row, one that crosses chunks leaves fp32 partial sums that a last kernel
 // adds in chunk order.  So a frequent token costs as much as rare ones and the
 // result does not depend on timing.  Rows without a token are zero-filled by
-// further blocks of the same launch.
+// further blocks of the last launch.
 #include <algorithm>
 #include <string>
 
@@ -77,7 +77,7 @@ void launch_lookup(const void *table, const void *ids, int64_t tokens, int64_t v
     const int64_t resident = (int64_t)num_sms() * 8;
     // few tokens: one per block, so that every row has an SM of its own
     const bool few = tokens <= resident;
-    const int grid = (int)(few ? tokens : std::min<int64_t>(ceil_div(tokens, 4), resident * 4));
+    const int grid = (int)(few ? tokens : std::min<int64_t>(ceil_div(tokens, 4), resident));
     auto *k = few ? (vec ? &lookup_kernel<TI, TO, ID, true, 1> : &lookup_kernel<TI, TO, ID, false, 1>)
                   : (vec ? &lookup_kernel<TI, TO, ID, true, 4> : &lookup_kernel<TI, TO, ID, false, 4>);
     k<<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
@@ -106,12 +106,77 @@ __device__ __forceinline__ uint32_t key_of(const ID *ids, int64_t t, int64_t voc
     return (uint32_t)vocab;
 }
 
-// digits of one tile of kTile keys, counted into hist[block][bin]
-template <typename ID, bool FIRST>
+// ---- zero rows ----------------------------------------------------------------------
+
+// zeros to the bytes [from, to) of p
+__device__ __forceinline__ void zero_bytes(char *p, int64_t from, int64_t to) {
+    const int64_t lead = (16 - (reinterpret_cast<uintptr_t>(p + from) & 15)) & 15;
+    const int64_t a = min(from + lead, to), b = a + (to - a) / 16 * 16;
+    for (int64_t i = a + (int64_t)threadIdx.x * 16; i < b; i += (int64_t)blockDim.x * 16)
+        *reinterpret_cast<uint4 *>(p + i) = make_uint4(0, 0, 0, 0);
+    // up to 15 bytes on either side; values have 2 or 4 bytes
+    const int64_t end = threadIdx.x < 8 ? from + 2 * threadIdx.x : b + 2 * ((int64_t)threadIdx.x - 8);
+    if (threadIdx.x < 16 && end < (threadIdx.x < 8 ? a : to)) *reinterpret_cast<uint16_t *>(p + end) = 0;
+}
+
+// Zero-filling the rows without a token is most of the gradient's traffic and
+// needs nothing but to know those rows, so it runs beside the sort and the joins
+// (latency), a share of it in each of their launches: blocks behind a launch's
+// own, kZeroRows rows each.
+constexpr int kZeroRows = 64;
+struct Fill {
+    char *grad;
+    int64_t row_bytes, vocab;
+    int64_t first;  // this launch's first group of kZeroRows rows
+};
+
+__device__ __forceinline__ void fill_rows(const Fill &f, int64_t group, const bool *present) {
+    const int64_t row0 = (f.first + group) * kZeroRows;
+    const int rows = (int)min((int64_t)kZeroRows, f.vocab - row0);
+    for (int i = 0; i < rows; ++i) {
+        if (present[i]) continue;
+        const int from = i;
+        while (i + 1 < rows && !present[i + 1]) ++i;
+        zero_bytes(f.grad, (row0 + from) * f.row_bytes, (row0 + i + 1) * f.row_bytes);
+    }
+}
+
+// the rows that have a token by the map of them
+__device__ __forceinline__ void fill_by_map(const Fill &f, int64_t group, const uint32_t *__restrict__ map) {
+    __shared__ bool present[kZeroRows];
+    const int64_t row0 = (f.first + group) * kZeroRows;
+    for (int i = threadIdx.x; i < kZeroRows; i += blockDim.x)
+        present[i] = row0 + i < f.vocab && (map[(row0 + i) >> 5] >> ((row0 + i) & 31)) & 1u;
+    __syncthreads();
+    fill_rows(f, group, present);
+}
+
+// the same from the ids themselves, where they are few
+template <typename ID>
+__device__ __forceinline__ void fill_by_ids(const Fill &f, int64_t group, const ID *__restrict__ ids, int64_t n,
+                                            int64_t padding) {
+    __shared__ bool present[kZeroRows];
+    const int64_t row0 = (f.first + group) * kZeroRows;
+    for (int i = threadIdx.x; i < kZeroRows; i += blockDim.x) present[i] = false;
+    __syncthreads();
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < n; t += blockDim.x) {
+        const int64_t id = (int64_t)ids[t];
+        if (id >= row0 && id < row0 + kZeroRows && id != padding) present[id - row0] = true;
+    }
+    __syncthreads();
+    fill_rows(f, group, present);
+}
+
+// Digits of one tile of kTile ids, counted into hist[block][bin], and the ids
+// into the map of rows that have a token; the next pass's table is cleared on
+// the way.
+template <typename ID>
 __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const ID *__restrict__ ids, int64_t vocab,
-                                                                 int64_t padding, const uint32_t *__restrict__ keys,
-                                                                 int64_t n, int shift, uint32_t *__restrict__ hist,
-                                                                 unsigned *flag) {
+                                                                 int64_t padding, int64_t n,
+                                                                 uint32_t *__restrict__ hist,
+                                                                 uint32_t *__restrict__ next_hist,
+                                                                 uint32_t *__restrict__ map, unsigned *flag) {
     __shared__ uint32_t cnt[kBins];
     for (int b = threadIdx.x; b < kBins; b += kSortThreads) cnt[b] = 0;
     __syncthreads();
@@ -119,53 +184,56 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const ID *__res
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
         const int64_t t = base + i * kSortThreads + threadIdx.x;
-        if (t < n) {
-            const uint32_t k = FIRST ? key_of(ids, t, vocab, padding, flag) : keys[t];
-            atomicAdd(&cnt[(k >> shift) & (kBins - 1)], 1u);
-        }
+        if (t >= n) break;
+        const uint32_t k = key_of(ids, t, vocab, padding, flag);
+        atomicAdd(&cnt[k & (kBins - 1)], 1u);
+        if ((int64_t)k < vocab) atomicOr(&map[k >> 5], 1u << (k & 31));
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < kBins; b += kSortThreads) hist[(int64_t)blockIdx.x * kBins + b] = cnt[b];
+    for (int b = threadIdx.x; b < kBins; b += kSortThreads) {
+        hist[(int64_t)blockIdx.x * kBins + b] = cnt[b];
+        next_hist[(int64_t)blockIdx.x * kBins + b] = 0;
+    }
 }
 
-// Moves one tile to its place in the order of this digit.  Each block adds up
-// the table of counts itself (a scan kernel of its own would cost a launch):
-// its bins' totals give where a bin starts, the blocks before it where its own
-// share starts.  Within the tile each warp owns consecutive keys and ranks 32
-// of them at a time by matching digits, so equal digits keep their order.
-template <typename ID, bool FIRST>
-__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(
-    const ID *__restrict__ ids, int64_t vocab, int64_t padding, const uint32_t *__restrict__ keys,
-    const uint32_t *__restrict__ vals, int64_t n, int shift, const uint32_t *__restrict__ hist, int blocks,
-    uint32_t *__restrict__ keys_out, uint32_t *__restrict__ vals_out) {
-    __shared__ uint32_t where[kSortWarps][kBins];
-    __shared__ uint32_t warp_total[kSortWarps];
+struct SortShared {
+    uint32_t where[kSortWarps][kBins];
+    uint32_t warp_total[kSortWarps];
+};
+
+// Moves one tile to its place in the order of this digit (bits shift ..
+// shift + 8).  total and before are the counts of this thread's two bins over
+// all tiles and over the tiles in front (ALONE: there is only this tile and
+// they are counted here).  Within the tile each warp owns consecutive keys and
+// ranks 32 of them at a time by matching digits, so equal digits keep their
+// order.  next_hist (may be null) collects the next digit's counts by the tile
+// that a key moves to; integer counts, so their order does not matter.
+template <typename ID, bool FIRST, bool ALONE>
+__device__ __forceinline__ void sort_tile(SortShared &sh, const ID *ids, int64_t vocab, int64_t padding,
+                                          const uint32_t *keys, const uint32_t *vals, int64_t n, int64_t tile,
+                                          int shift, uint32_t (&total)[2], const uint32_t (&before)[2],
+                                          uint32_t *keys_out, uint32_t *vals_out, uint32_t *next_hist,
+                                          unsigned *flag) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    for (int b = tid; b < kSortWarps * kBins; b += kSortThreads) (&where[0][0])[b] = 0;
-    // two neighbouring bins per thread
-    uint32_t total[2] = {0, 0}, before[2] = {0, 0};
-    const uint2 *h2 = reinterpret_cast<const uint2 *>(hist);
-#pragma unroll 8
-    for (int b = 0; b < blocks; ++b) {
-        const uint2 c = h2[(int64_t)b * (kBins / 2) + tid];
-        total[0] += c.x;
-        total[1] += c.y;
-        if (b < (int)blockIdx.x) {
-            before[0] += c.x;
-            before[1] += c.y;
-        }
-    }
+    for (int b = tid; b < kSortWarps * kBins; b += kSortThreads) (&sh.where[0][0])[b] = 0;
     __syncthreads();
-    // per-warp counts of the tile's digits
-    const int64_t base = (int64_t)blockIdx.x * kTile + w * kWarpItems;
+    const int64_t base = tile * kTile + w * kWarpItems;
     uint32_t key[kWarpItems / 32];
 #pragma unroll
     for (int i = 0; i < kWarpItems / 32; ++i) {
         const int64_t t = base + i * 32 + lane;
-        key[i] = t < n ? (FIRST ? key_of(ids, t, vocab, padding, (unsigned *)nullptr) : keys[t]) : 0u;
-        if (t < n) atomicAdd(&where[w][(key[i] >> shift) & (kBins - 1)], 1u);
+        key[i] = t < n ? (FIRST ? key_of(ids, t, vocab, padding, flag) : keys[t]) : 0u;
+        if (t < n) atomicAdd(&sh.where[w][(key[i] >> shift) & (kBins - 1)], 1u);
     }
-    // exclusive sum of the bins' totals over the block
+    __syncthreads();
+    if (ALONE) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            total[j] = 0;
+            for (int i = 0; i < kSortWarps; ++i) total[j] += sh.where[i][2 * tid + j];
+        }
+    }
+    // exclusive sum of the bins' totals over the block: where each bin starts
     const uint32_t mine = total[0] + total[1];
     uint32_t incl = mine;
 #pragma unroll
@@ -173,18 +241,18 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(
         const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) warp_total[w] = incl;
+    if (lane == 31) sh.warp_total[w] = incl;
     __syncthreads();
     uint32_t start = incl - mine;
-    for (int i = 0; i < w; ++i) start += warp_total[i];
+    for (int i = 0; i < w; ++i) start += sh.warp_total[i];
     // where[w][bin] = first position of this warp's keys of the bin
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int b = 2 * tid + j;
         uint32_t at = start + (j ? total[0] : 0u) + before[j];
         for (int i = 0; i < kSortWarps; ++i) {
-            const uint32_t c = where[i][b];
-            where[i][b] = at;
+            const uint32_t c = sh.where[i][b];
+            sh.where[i][b] = at;
             at += c;
         }
     }
@@ -196,14 +264,67 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(
         const uint32_t d = in ? (key[i] >> shift) & (kBins - 1) : kBins;  // kBins: no key
         const uint32_t peers = __match_any_sync(0xffffffffu, d);
         if (in) {
-            const uint32_t rank = __popc(peers & ((1u << lane) - 1u));
-            const uint32_t to = where[w][d] + rank;
+            const uint32_t to = sh.where[w][d] + __popc(peers & ((1u << lane) - 1u));
             keys_out[to] = key[i];
             vals_out[to] = FIRST ? (uint32_t)t : vals[t];
+            if (next_hist)
+                atomicAdd(&next_hist[(int64_t)(to / kTile) * kBins + ((key[i] >> (shift + kBits)) & (kBins - 1))], 1u);
         }
         __syncwarp();
-        if (in && (peers >> lane) == 1u) where[w][d] += __popc(peers);  // the last of the peers
+        if (in && (peers >> lane) == 1u) sh.where[w][d] += __popc(peers);  // the last of the peers
         __syncwarp();
+    }
+}
+
+// One pass over all tiles.  Each block adds up the table of counts itself (a
+// scan kernel of its own would cost a launch).
+template <typename ID, bool FIRST>
+__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(
+    const ID *__restrict__ ids, int64_t vocab, int64_t padding, const uint32_t *__restrict__ keys,
+    const uint32_t *__restrict__ vals, int64_t n, int shift, const uint32_t *__restrict__ hist, int blocks,
+    uint32_t *__restrict__ keys_out, uint32_t *__restrict__ vals_out, uint32_t *__restrict__ next_hist,
+    uint32_t *__restrict__ clear_hist, const Fill fill, const uint32_t *__restrict__ map) {
+    if ((int)blockIdx.x >= blocks) {
+        fill_by_map(fill, (int)blockIdx.x - blocks, map);
+        return;
+    }
+    __shared__ SortShared sh;
+    uint32_t total[2] = {0, 0}, before[2] = {0, 0};  // of two neighbouring bins per thread
+    const uint2 *h2 = reinterpret_cast<const uint2 *>(hist);
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b) {
+        const uint2 c = h2[(int64_t)b * (kBins / 2) + threadIdx.x];
+        total[0] += c.x;
+        total[1] += c.y;
+        if (b < (int)blockIdx.x) {
+            before[0] += c.x;
+            before[1] += c.y;
+        }
+    }
+    if (clear_hist) reinterpret_cast<uint2 *>(clear_hist)[(int64_t)blockIdx.x * (kBins / 2) + threadIdx.x] = make_uint2(0, 0);
+    sort_tile<ID, FIRST, false>(sh, ids, vocab, padding, keys, vals, n, blockIdx.x, shift, total, before, keys_out,
+                                vals_out, next_hist, nullptr);
+}
+
+// All passes of a list that fits one tile, in one block; zero rows in the others.
+template <typename ID>
+__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const ID *__restrict__ ids, int64_t vocab,
+                                                                  int64_t padding, int64_t n, int passes, uint32_t *k0,
+                                                                  uint32_t *v0, uint32_t *k1, uint32_t *v1,
+                                                                  const Fill fill, unsigned *flag) {
+    if (blockIdx.x > 0) {
+        fill_by_ids(fill, (int)blockIdx.x - 1, ids, n, padding);
+        return;
+    }
+    __shared__ SortShared sh;
+    uint32_t total[2];
+    const uint32_t before[2] = {0, 0};
+    sort_tile<ID, true, true>(sh, ids, vocab, padding, nullptr, nullptr, n, 0, 0, total, before, k0, v0, nullptr, flag);
+    for (int pass = 1; pass < passes; ++pass) {
+        __syncthreads();  // the block's own writes of the last pass
+        const bool odd = pass & 1;
+        sort_tile<ID, false, true>(sh, nullptr, vocab, padding, odd ? k0 : k1, odd ? v0 : v1, n, 0, pass * kBits, total,
+                                   before, odd ? k1 : k0, odd ? v1 : v0, nullptr, nullptr);
     }
 }
 
@@ -214,6 +335,21 @@ struct Sorted {
     int64_t n;
     int chunk;
     int64_t chunks;
+};
+
+// What is left to do of the zero rows, and the map of the others.
+struct Filling {
+    Fill next;
+    int64_t left;  // groups of rows
+    const uint32_t *map;
+
+    // the next share of them: this launch's blocks
+    Fill take(int64_t groups) {
+        const Fill f = next;
+        next.first += groups;
+        left -= groups;
+        return f;
+    }
 };
 
 // First column of a thread's 8 in row `row` of the gradient: rows that are not
@@ -239,45 +375,27 @@ __device__ __forceinline__ void put_row(const Span<TG> &grad, int64_t row, int d
     else store_any(grad, at, from, from + dim, a);
 }
 
-constexpr int kMaxChunk = 64, kBatch = 8, kZeroRows = 64;
+constexpr int kMaxChunk = 64, kBatch = 8;
 
-// Blocks [0, chunks * col_blocks): one chunk of the sorted list, 8 columns per
-// thread.  Blocks after them: kZeroRows rows each, zero-filled where the list
-// has no such id.  partial: [chunks][2][pitch], slot 0 for a run that began
-// before the chunk, slot 1 for one that begins in it and goes on; its columns
-// are shifted as the run's row is.
+// One chunk of the sorted list per block and column block, 8 columns per
+// thread.  partial: [chunks][2][pitch], slot 0 for a run that began before the
+// chunk, slot 1 for one that begins in it and goes on; its columns are shifted
+// as the run's row is.
 template <typename TD, typename TG, bool VEC>
 __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const Span<const TD> dy, int64_t vocab,
                                                           int dim, int col_blocks, float scale, bool accumulate,
-                                                          const Span<TG> grad, float *__restrict__ partial, int pitch) {
+                                                          const Span<TG> grad, float *__restrict__ partial, int pitch,
+                                                          const Fill fill, const uint32_t *__restrict__ map) {
     __shared__ uint32_t sk[kMaxChunk + 2], sv[kMaxChunk];
     const int tid = threadIdx.x;
-    const int64_t work = s.chunks * col_blocks;
-    if ((int64_t)blockIdx.x >= work) {
-        __shared__ uint8_t present[kZeroRows];
-        const int64_t row0 = ((int64_t)blockIdx.x - work) * kZeroRows;
-        for (int i = tid; i < kZeroRows; i += blockDim.x) {
-            const int64_t row = row0 + i;
-            int64_t lo = 0, hi = s.n;  // first position with key >= row
-            while (lo < hi) {
-                const int64_t mid = (lo + hi) >> 1;
-                if ((int64_t)s.keys[mid] < row) lo = mid + 1;
-                else hi = mid;
-            }
-            present[i] = row >= vocab || (lo < s.n && (int64_t)s.keys[lo] == row);
-        }
-        __syncthreads();
-        for (int i = 0; i < kZeroRows; ++i) {
-            if (present[i]) continue;
-            for (int j = tid; j * 8 < dim + (VEC ? 0 : 7); j += blockDim.x) {
-                float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                put_row<TG, VEC>(grad, row0 + i, dim, j, 0.f, false, zero);
-            }
-        }
+    // sums and zero rows are spread evenly over the blocks, so that both are under way at any time
+    const int64_t sums = s.chunks * col_blocks, block = (int64_t)blockIdx.x * sums / gridDim.x;
+    if (((int64_t)blockIdx.x + 1) * sums / gridDim.x == block) {
+        fill_by_map(fill, (int64_t)blockIdx.x - block, map);
         return;
     }
-    const int64_t c = (int64_t)blockIdx.x / col_blocks;
-    const int j = (int)((int64_t)blockIdx.x % col_blocks) * (int)blockDim.x + tid;
+    const int64_t c = block / col_blocks;
+    const int j = (int)(block % col_blocks) * (int)blockDim.x + tid;
     const int64_t p0 = c * s.chunk;
     const int len = (int)(s.n - p0 < s.chunk ? s.n - p0 : s.chunk);
     // keys of the chunk and of its two neighbours (~0: none)
@@ -319,33 +437,42 @@ __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const 
     }
 }
 
-// One block per chunk and column block: if a run begins in the chunk and goes
-// on, its partial sums are added in chunk order and written to its row.
+// Blocks [0, chunks * col_blocks): if a run begins in the block's chunk and goes
+// on, its partial sums are added in chunk order and written to its row.  Blocks
+// after them: zero rows.
 template <typename TG, bool VEC>
-__global__ void __launch_bounds__(256) segment_join_kernel(const Sorted s, int64_t vocab, int dim, float scale,
-                                                           bool accumulate, const Span<TG> grad,
-                                                           const float *__restrict__ partial, int pitch) {
-    const int64_t c = blockIdx.x;
+__global__ void __launch_bounds__(256) segment_join_kernel(const Sorted s, int64_t vocab, int dim, int col_blocks,
+                                                           float scale, bool accumulate, const Span<TG> grad,
+                                                           const float *__restrict__ partial, int pitch,
+                                                           const Fill fill, const uint32_t *__restrict__ map) {
+    const int64_t joins = s.chunks * col_blocks;
+    if ((int64_t)blockIdx.x >= joins) {
+        fill_by_map(fill, (int64_t)blockIdx.x - joins, map);
+        return;
+    }
+    const int64_t c = (int64_t)blockIdx.x / col_blocks;
     const int64_t p0 = c * s.chunk, p1 = p0 + s.chunk;
     if (p1 >= s.n) return;
-    const uint32_t k = s.keys[p1 - 1];
-    if ((int64_t)k >= vocab || s.keys[p1] != k) return;
-    if (s.keys[p0] == k && p0 > 0 && s.keys[p0 - 1] == k) return;  // the run began earlier
-    const int j = (int)blockIdx.y * (int)blockDim.x + threadIdx.x;
-    if (j * 8 >= pitch) return;
-    int64_t lo = p1, hi = s.n;  // first position behind the run
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (s.keys[mid] <= k) lo = mid + 1;
-        else hi = mid;
+    const uint32_t k = s.keys[p1 - 1], next = s.keys[p1], head = s.keys[p0], prev = p0 > 0 ? s.keys[p0 - 1] : ~0u;
+    if ((int64_t)k >= vocab || next != k) return;
+    if (head == k && prev == k) return;  // the run began earlier
+    // the chunks behind this one that begin with the run: all threads look at once
+    int64_t more = 0;
+    for (;;) {
+        const int64_t q = (c + 1 + more + threadIdx.x) * s.chunk;
+        const int here = __syncthreads_count(q < s.n && s.keys[q] == k);
+        more += here;
+        if (here < (int)blockDim.x) break;
     }
-    const int64_t last = (lo - 1) / s.chunk;  // chunk of the run's last token
+    const int j = (int)((int64_t)blockIdx.x % col_blocks) * (int)blockDim.x + threadIdx.x;
+    if (j * 8 >= pitch) return;
     float acc[8];
     load8(partial + (c * 2 + 1) * pitch + j * 8, acc);
-#pragma unroll 4
-    for (int64_t i = c + 1; i <= last; ++i) {
+    const float *part = partial + (c + 1) * 2 * pitch + j * 8;
+#pragma unroll 16
+    for (int64_t i = 0; i < more; ++i) {
         float x[8];
-        load8(partial + i * 2 * pitch + j * 8, x);
+        load8(part + i * 2 * pitch, x);
 #pragma unroll
         for (int l = 0; l < 8; ++l) acc[l] += x[l];
     }
@@ -364,7 +491,7 @@ int chunk_len(int64_t tokens, int col_blocks) {
 struct GradPlan {
     int threads, col_blocks, chunk, passes, pitch;
     int64_t chunks, sort_blocks;
-    int64_t off_hist, off_k0, off_v0, off_k1, off_v1, off_partial, bytes;
+    int64_t off_map, off_hist[3], off_k0, off_v0, off_k1, off_v1, off_partial, bytes;
 };
 
 GradPlan plan_grad(int64_t tokens, int64_t vocab, int32_t dim, bool vec) {
@@ -384,7 +511,8 @@ GradPlan plan_grad(int64_t tokens, int64_t vocab, int32_t dim, bool vec) {
         at += round_up(bytes, 256);
         return here;
     };
-    p.off_hist = take(p.sort_blocks * kBins * 4);
+    p.off_map = take((vocab + 31) / 32 * 4);
+    for (int64_t &off : p.off_hist) off = take(p.sort_blocks * kBins * 4);
     p.off_k0 = take(tokens * 4);
     p.off_v0 = take(tokens * 4);
     p.off_k1 = take(tokens * 4);
@@ -396,51 +524,66 @@ GradPlan plan_grad(int64_t tokens, int64_t vocab, int32_t dim, bool vec) {
 
 template <typename ID>
 int sort_tokens(const GradPlan &p, const ID *ids, int64_t tokens, int64_t vocab, int64_t padding, char *ws,
-                cudaStream_t st, Sorted *out) {
-    uint32_t *hist = reinterpret_cast<uint32_t *>(ws + p.off_hist);
+                Filling *fill, cudaStream_t st, Sorted *out) {
+    uint32_t *hist[3], *map = reinterpret_cast<uint32_t *>(ws + p.off_map);
+    fill->map = map;
+    for (int i = 0; i < 3; ++i) hist[i] = reinterpret_cast<uint32_t *>(ws + p.off_hist[i]);
     uint32_t *k[2] = {reinterpret_cast<uint32_t *>(ws + p.off_k0), reinterpret_cast<uint32_t *>(ws + p.off_k1)};
     uint32_t *v[2] = {reinterpret_cast<uint32_t *>(ws + p.off_v0), reinterpret_cast<uint32_t *>(ws + p.off_v1)};
-    const int blocks = (int)p.sort_blocks;
-    for (int pass = 0; pass < p.passes; ++pass) {
-        const int shift = pass * kBits, to = pass & 1, from = to ^ 1;
-        if (pass == 0) {
-            SPCO_LAUNCH("embed_sort_hist", st, sort_hist_kernel<ID, true><<<blocks, kSortThreads, 0, st>>>(
-                                                   ids, vocab, padding, nullptr, tokens, shift, hist, device_flag_ptr()));
-            SPCO_LAUNCH("embed_sort_scatter", st,
-                        sort_scatter_kernel<ID, true><<<blocks, kSortThreads, 0, st>>>(
-                            ids, vocab, padding, nullptr, nullptr, tokens, shift, hist, blocks, k[to], v[to]));
-        } else {
-            SPCO_LAUNCH("embed_sort_hist", st, sort_hist_kernel<ID, false><<<blocks, kSortThreads, 0, st>>>(
-                                                   nullptr, vocab, padding, k[from], tokens, shift, hist, nullptr));
-            SPCO_LAUNCH("embed_sort_scatter", st,
-                        sort_scatter_kernel<ID, false><<<blocks, kSortThreads, 0, st>>>(
-                            nullptr, vocab, padding, k[from], v[from], tokens, shift, hist, blocks, k[to], v[to]));
+    const int blocks = (int)p.sort_blocks, last = (p.passes - 1) & 1;
+    if (blocks == 1) {
+        const int64_t share = fill->left;
+        const Fill f = fill->take(share);
+        SPCO_LAUNCH("embed_sort_small", st,
+                    sort_small_kernel<ID><<<(unsigned)(1 + share), kSortThreads, 0, st>>>(
+                        ids, vocab, padding, tokens, p.passes, k[0], v[0], k[1], v[1], f, device_flag_ptr()));
+    } else {
+        SPECOPTIM_CUDA(cudaMemsetAsync(map, 0, (size_t)((vocab + 31) / 32 * 4), st));
+        SPCO_LAUNCH("embed_sort_hist", st, sort_hist_kernel<ID><<<blocks, kSortThreads, 0, st>>>(
+                                               ids, vocab, padding, tokens, hist[0], hist[1], map, device_flag_ptr()));
+        const int64_t fills = fill->left;
+        for (int pass = 0; pass < p.passes; ++pass) {
+            // three tables in turn: pass i reads table i, counts for pass i + 1
+            // into the next one and clears the one behind it
+            const int to = pass & 1, from = to ^ 1;
+            const uint32_t *counts = hist[pass % 3];
+            uint32_t *next = pass + 1 < p.passes ? hist[(pass + 1) % 3] : nullptr;
+            uint32_t *clear = pass + 2 < p.passes ? hist[(pass + 2) % 3] : nullptr;
+            const int64_t share = std::min(fill->left, fills / 8);
+            const Fill f = fill->take(share);
+            const unsigned grid = (unsigned)(blocks + share);
+            if (pass == 0)
+                SPCO_LAUNCH("embed_sort_scatter", st,
+                            sort_scatter_kernel<ID, true><<<grid, kSortThreads, 0, st>>>(
+                                ids, vocab, padding, nullptr, nullptr, tokens, 0, counts, blocks, k[to], v[to], next, clear, f, map));
+            else
+                SPCO_LAUNCH("embed_sort_scatter", st,
+                            sort_scatter_kernel<ID, false><<<grid, kSortThreads, 0, st>>>(
+                                nullptr, vocab, padding, k[from], v[from], tokens, pass * kBits, counts, blocks, k[to],
+                                v[to], next, clear, f, map));
         }
-        out->keys = k[to];
-        out->vals = v[to];
     }
+    out->keys = k[last];
+    out->vals = v[last];
     SPECOPTIM_LAUNCHED("embed_grad sort");
-    out->n = tokens;
-    out->chunk = p.chunk;
-    out->chunks = p.chunks;
     return SPECOPTIM_OK;
 }
 
 template <typename TD, typename TG, bool VEC>
-int sum_segments(const GradPlan &p, const Sorted &s, const void *dy, int64_t vocab, int dim, float scale,
+int sum_segments(const GradPlan &p, const Sorted &s, Filling fill, const void *dy, int64_t vocab, int dim, float scale,
                  bool accumulate, void *grad, float *partial, cudaStream_t st) {
     const Span<const TD> in(static_cast<const TD *>(dy), s.n * dim);
     const Span<TG> out(static_cast<TG *>(grad), vocab * dim);
-    const int64_t work = s.chunks * p.col_blocks + (accumulate ? 0 : ceil_div(vocab, kZeroRows));
-    if (work > INT32_MAX) return fail(SPECOPTIM_ERR_NOT_IMPLEMENTED, "embed_grad: tokens x dim too large for one launch");
-    if (work > 0)
-        SPCO_LAUNCH("embed_segment_sum", st,
-                    segment_sum_kernel<TD, TG, VEC><<<(unsigned)work, p.threads, 0, st>>>(
-                        s, in, vocab, dim, p.col_blocks, scale, accumulate, out, partial, p.pitch));
-    if (s.chunks > 1)
+    const int64_t sums = s.chunks * p.col_blocks;
+    const int64_t beside = fill.left - fill.left / 2;  // the rest beside the joins
+    const Fill f = fill.take(beside);
+    SPCO_LAUNCH("embed_segment_sum", st,
+                segment_sum_kernel<TD, TG, VEC><<<(unsigned)(sums + beside), p.threads, 0, st>>>(
+                    s, in, vocab, dim, p.col_blocks, scale, accumulate, out, partial, p.pitch, f, fill.map));
+    if (s.chunks > 1 || fill.left > 0)
         SPCO_LAUNCH("embed_segment_join", st,
-                    segment_join_kernel<TG, VEC><<<dim3((unsigned)s.chunks, p.col_blocks), p.threads, 0, st>>>(
-                        s, vocab, dim, scale, accumulate, out, partial, p.pitch));
+                    segment_join_kernel<TG, VEC><<<(unsigned)(sums + fill.left), p.threads, 0, st>>>(
+                        s, vocab, dim, p.col_blocks, scale, accumulate, out, partial, p.pitch, fill.next, fill.map));
     SPECOPTIM_LAUNCHED("embed_grad sums");
     return SPECOPTIM_OK;
 }
@@ -520,22 +663,30 @@ extern "C" int embed_grad(const void *ids, int32_t id_bytes, const void *dy, int
         const GradPlan p = plan_grad(tokens, vocab, dim, vec);
         if (tokens > 0 && (!workspace || workspace_bytes < p.bytes))
             return fail(SPECOPTIM_ERR_INVALID_ARG, "embed_grad: the workspace is smaller than embed_grad_workspace() says");
+        const int64_t fills = accumulate ? 0 : ceil_div(vocab, kZeroRows);
+        if (p.chunks * p.col_blocks + p.sort_blocks + fills > INT32_MAX)
+            return fail(SPECOPTIM_ERR_NOT_IMPLEMENTED, "embed_grad: tokens x dim too large for one launch");
         if (int rc = bind_device()) return rc;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
-        char *ws = static_cast<char *>(workspace);
-        Sorted s{nullptr, nullptr, 0, p.chunk, 0};
-        if (tokens > 0) {
-            const int rc = id_bytes == 8 ? sort_tokens(p, static_cast<const int64_t *>(ids), tokens, vocab, padding_idx, ws, st, &s)
-                                         : sort_tokens(p, static_cast<const int32_t *>(ids), tokens, vocab, padding_idx, ws, st, &s);
-            if (rc) return rc;
+        const int64_t row_bytes = dim * (int64_t)type_bytes(grad_type);
+        if (tokens == 0) {
+            if (!accumulate) SPECOPTIM_CUDA(cudaMemsetAsync(grad, 0, (size_t)(vocab * row_bytes), st));
+            return SPECOPTIM_OK;
         }
+        char *ws = static_cast<char *>(workspace);
+        Sorted s{nullptr, nullptr, tokens, p.chunk, p.chunks};
+        Filling fill{{static_cast<char *>(grad), row_bytes, vocab, 0}, fills, nullptr};
+        const int rc = id_bytes == 8
+                           ? sort_tokens(p, static_cast<const int64_t *>(ids), tokens, vocab, padding_idx, ws, &fill, st, &s)
+                           : sort_tokens(p, static_cast<const int32_t *>(ids), tokens, vocab, padding_idx, ws, &fill, st, &s);
+        if (rc) return rc;
         float *partial = reinterpret_cast<float *>(ws + p.off_partial);
         const bool acc = accumulate != 0;
         auto go = [&](auto td, auto tg) -> int {
             using TD = decltype(td);
             using TG = decltype(tg);
-            return vec ? sum_segments<TD, TG, true>(p, s, dy, vocab, dim, scale, acc, grad, partial, st)
-                       : sum_segments<TD, TG, false>(p, s, dy, vocab, dim, scale, acc, grad, partial, st);
+            return vec ? sum_segments<TD, TG, true>(p, s, fill, dy, vocab, dim, scale, acc, grad, partial, st)
+                       : sum_segments<TD, TG, false>(p, s, fill, dy, vocab, dim, scale, acc, grad, partial, st);
         };
         if (dy_type == STAGE_BF16) return grad_type == STAGE_BF16 ? go(bf16{}, bf16{}) : go(bf16{}, float{});
         return grad_type == STAGE_BF16 ? go(float{}, bf16{}) : go(float{}, float{});

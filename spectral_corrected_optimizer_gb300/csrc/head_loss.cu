@@ -29,62 +29,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ---- the rows that have a target ---------------------------------------------------------
 
-// One block: lists the tokens with a target in token order.  row_of[r] = token
-// of row r, at[t] = row of token t (-1: none), target[r].  A thread takes 8
-// neighbouring tokens at a time, so 8192 tokens cost one round.
-constexpr int kRowItems = 8;
-template <typename ID>
-__global__ void __launch_bounds__(1024) head_rows_kernel(const ID *__restrict__ targets, int64_t ignore, int tokens,
-                                                         int vocab, int mean, HeadState *state, int *__restrict__ row_of,
-                                                         int *__restrict__ at, int *__restrict__ target,
-                                                         float *__restrict__ row_loss, unsigned *flag) {
-    __shared__ int warp_count[2][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int rows = 0, parity = 0;
-    for (int64_t t0 = 0; t0 < tokens; t0 += 1024 * kRowItems, parity ^= 1) {
-        const int64_t t = t0 + (int64_t)threadIdx.x * kRowItems;
-        int y[kRowItems], count = 0;
-#pragma unroll
-        for (int i = 0; i < kRowItems; ++i) {
-            const int64_t id = t + i < tokens ? (int64_t)targets[t + i] : ignore;
-            const bool inside = id >= 0 && id < vocab;
-            if (id != ignore && !inside) atomicExch(flag, kSiteTarget);
-            y[i] = id != ignore && inside ? (int)id : -1;
-            count += y[i] >= 0;
-        }
-        int incl = count;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) warp_count[parity][w] = incl;
-        __syncthreads();
-        int r = rows + incl - count;
-        for (int i = 0; i < 32; ++i) {
-            const int c = warp_count[parity][i];
-            if (i < w) r += c;
-            rows += c;
-        }
-#pragma unroll
-        for (int i = 0; i < kRowItems; ++i) {
-            if (t + i >= tokens) break;
-            at[t + i] = y[i] >= 0 ? r : -1;
-            if (y[i] >= 0) {
-                row_of[r] = (int)(t + i);
-                target[r++] = y[i];
-            } else {
-                row_loss[t + i] = 0.f;
-            }
-        }
-    }
-    if (threadIdx.x == 0) {
-        state->rows = rows;
-        state->blocks_done = 0;
-        state->inv_count = mean ? 1.f / (float)max(rows, 1) : 1.f;
-    }
-}
-
 // 8 bf16 values of a row from column 8 v, zero behind dim
 __device__ __forceinline__ uint4 row_vec(const uint16_t *row, int v, int dim, bool vec) {
     if (vec) return __ldg(reinterpret_cast<const uint4 *>(row) + v);
@@ -98,25 +42,83 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float s) {
     return fmaf(hi_f(a), hi_f(b), fmaf(lo_f(a), lo_f(b), s));
 }
 
-// Copies the listed rows of h together, in column blocks of 64 (zero behind
-// dim), with zero rows up to the next multiple of the tile height.  On the way
-// the logit of each row's target is formed as an fp32 dot product: the loss is the difference between it and the log-sum-exp, and the tensor cores'
-// long accumulation (dim / 16 steps, each cut off rather than rounded) leaves a
-// large logit 2^-24 dim / 32 of itself short.
-__global__ void __launch_bounds__(256) head_gather_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ w,
-                                                          const int *__restrict__ row_of, const int *__restrict__ target,
-                                                          const HeadState *__restrict__ state, int dim, int row_cap,
-                                                          int h_vec, int w_vec, uint16_t *__restrict__ out,
-                                                          float *__restrict__ target_logit) {
-    __shared__ float red[2][8];
-    const int rows = state->rows, end = (rows + kHeadTileM - 1) / kHeadTileM * kHeadTileM;
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+
+// Lists the tokens with a target in token order (row_of[r] = token of row r,
+// at[t] = row of token t or -1, target[r]) and copies their rows of h together,
+// in column blocks of 64 (zero behind dim).  Each block takes `share`
+// neighbouring tokens (at most one per thread), counts the targets in front of
+// them itself -- the ids come from L2, a kernel of its own for the list would
+// cost more -- and then copies its rows, a warp per row.  The last block appends the
+// zero rows up to the next multiple of the tile height.
+//
+// On the way the logit of each row's target is formed as an fp32 dot product:
+// the loss is the difference between it and the log-sum-exp, and the tensor
+// cores' long accumulation (dim / 16 steps, each cut off rather than rounded)
+// leaves a large logit 2^-24 dim / 32 of itself short.
+constexpr int kPadBlocks = 8;
+template <typename ID>
+__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__restrict__ targets, int64_t ignore, int tokens,
+                                                        int vocab, int mean, int share, int own_blocks,
+                                                        const uint16_t *__restrict__ h,
+                                                        const uint16_t *__restrict__ w, int dim, int row_cap, int h_vec,
+                                                        int w_vec, HeadState *state, int *__restrict__ row_of,
+                                                        int *__restrict__ at, int *__restrict__ target,
+                                                        uint16_t *__restrict__ out, float *__restrict__ target_logit,
+                                                        float *__restrict__ row_loss, unsigned *flag) {
+    __shared__ int red[2][kRowWarps], own_token[kRowThreads], own_target[kRowThreads];
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int pad = (int)blockIdx.x - own_blocks;  // >= 0: a block of zero rows, which counts all targets
+    const int t0 = pad >= 0 ? tokens : (int)blockIdx.x * share, t1 = min(t0 + share, tokens);
+    auto usable = [&](int64_t id) { return id != ignore && id >= 0 && id < vocab; };
+    int before = 0;
+#pragma unroll 4
+    for (int t = threadIdx.x; t < t0; t += kRowThreads) before += usable((int64_t)targets[t]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    const int t = t0 + threadIdx.x;
+    const int64_t id = t < t1 ? (int64_t)targets[t] : ignore;
+    const bool has = usable(id);
+    if (id != ignore && !has) atomicExch(flag, kSiteTarget);
+    const unsigned ballot = __ballot_sync(0xffffffffu, has);
+    if (lane == 0) {
+        red[0][wp] = before;
+        red[1][wp] = __popc(ballot);
+    }
+    __syncthreads();
+    before = 0;
+    int count = 0, k = __popc(ballot & ((1u << lane) - 1u));
+#pragma unroll
+    for (int i = 0; i < kRowWarps; ++i) {
+        before += red[0][i];
+        if (i < wp) k += red[1][i];
+        count += red[1][i];
+    }
+    if (t < t1) at[t] = has ? before + k : -1;
+    if (has) {
+        row_of[before + k] = t;
+        target[before + k] = (int)id;
+        own_token[k] = t;
+        own_target[k] = (int)id;
+    } else if (t < t1) {
+        row_loss[t] = 0.f;
+    }
+    __syncthreads();
     const int vecs = (dim + 63) / 64 * 8;
-    int parity = 0;
-    for (int r = blockIdx.x; r < end; r += gridDim.x, parity ^= 1) {
-        const uint16_t *hr = r < rows ? h + (int64_t)row_of[r] * dim : nullptr;
-        const uint16_t *wr = r < rows ? w + (int64_t)target[r] * dim : nullptr;
+    const int copy = pad >= 0 ? (before + 63) / 64 * 64 - before : count;
+    if (pad == -1 && threadIdx.x == 0) {
+        const int rows = before + count;
+        state->rows = rows;
+        state->blocks_done = 0;
+        state->inv_count = mean ? 1.f / (float)max(rows, 1) : 1.f;
+    }
+    for (int i = max(pad, 0) * kRowWarps + wp; i < copy; i += (pad >= 0 ? kPadBlocks : 1) * kRowWarps) {
+        const int r = before + i;
+        const uint16_t *hr = i < count ? h + (int64_t)own_token[i] * dim : nullptr;
+        const uint16_t *wr = i < count ? w + (int64_t)own_target[i] * dim : nullptr;
         float s = 0.f;
-        for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+#pragma unroll 4
+        for (int v = lane; v < vecs; v += 32) {
             uint4 a = make_uint4(0, 0, 0, 0);
             if (hr && v * 8 < dim) {
                 a = row_vec(hr, v, dim, h_vec);
@@ -127,12 +129,7 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const uint16_t *__rest
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if ((threadIdx.x & 31) == 0) red[parity][threadIdx.x >> 5] = s;
-        __syncthreads();
-        if (threadIdx.x == 0 && r < rows) {
-            for (int i = 1; i < (int)blockDim.x / 32; ++i) s += red[parity][i];
-            target_logit[r] = s;
-        }
+        if (lane == 0 && i < count) target_logit[r] = s;
     }
 }
 
@@ -329,7 +326,7 @@ int check_call(const HeadCall &c, const HeadPlan &p, const std::string &what) {
 }
 
 // Steps 1 and 2: afterwards loss, row_loss and the rows' norms exist.
-int run_loss(const HeadCall &c, const HeadPlan &p, HeadGemm *g) {
+int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     std::memset(g, 0, sizeof(*g));
     HeadState *state = reinterpret_cast<HeadState *>(c.ws + p.off_state);
     int *row_of = reinterpret_cast<int *>(c.ws + p.off_row_of), *at = reinterpret_cast<int *>(c.ws + p.off_at);
@@ -339,29 +336,29 @@ int run_loss(const HeadCall &c, const HeadPlan &p, HeadGemm *g) {
     uint16_t *hc = reinterpret_cast<uint16_t *>(c.ws + p.off_h);
     const uint16_t *w = static_cast<const uint16_t *>(c.w);
     const int tokens = (int)c.tokens, vocab = (int)c.vocab;
-    if (c.id_bytes == 8)
+    // tokens per block: one each while there are SMs for them, at most one per thread
+    const int share = std::max(1, std::min(kRowThreads, tokens / (num_sms() * 4)));
+    const int blocks = (int)std::max<int64_t>(1, ceil_div(tokens, share));
+    const bool w_vec = c.dim % 8 == 0, h_vec = w_vec && aligned16(c.h);
+    auto rows = [&](auto id) {
+        using ID = decltype(id);
         SPCO_LAUNCH("head_rows", c.st,
-                    head_rows_kernel<<<1, 1024, 0, c.st>>>(static_cast<const int64_t *>(c.targets), c.ignore, tokens,
-                                                           vocab, c.mean, state, row_of, at, target, c.row_loss,
-                                                           device_flag_ptr()));
-    else
-        SPCO_LAUNCH("head_rows", c.st,
-                    head_rows_kernel<<<1, 1024, 0, c.st>>>(static_cast<const int32_t *>(c.targets), c.ignore, tokens,
-                                                           vocab, c.mean, state, row_of, at, target, c.row_loss,
-                                                           device_flag_ptr()));
-    const int copy_threads = (int)std::min<int64_t>(256, round_up(p.ld / 8, 32));
-    SPCO_LAUNCH("head_gather", c.st,
-                head_gather_kernel<<<std::min(p.row_cap, num_sms() * 16), copy_threads, 0, c.st>>>(
-                    static_cast<const uint16_t *>(c.h), w, row_of, target, state, c.dim, p.row_cap,
-                    c.dim % 8 == 0 && aligned16(c.h), c.dim % 8 == 0, hc, tlogit));
+                    head_rows_kernel<ID><<<blocks + (grad ? kPadBlocks : 0), kRowThreads, 0, c.st>>>(
+                        static_cast<const ID *>(c.targets), c.ignore, tokens, vocab, c.mean, share, blocks,
+                        static_cast<const uint16_t *>(c.h), w, c.dim, p.row_cap, h_vec, w_vec, state, row_of, at, target,
+                        hc, tlogit, c.row_loss, device_flag_ptr()));
+    };
+    if (c.id_bytes == 8) rows(int64_t{});
+    else rows(int32_t{});
     if (p.ld != c.dim) {
         uint16_t *wc = reinterpret_cast<uint16_t *>(c.ws + p.off_w);
         SPCO_LAUNCH("head_pad", c.st,
-                    head_pad_kernel<<<(unsigned)std::min<int64_t>(c.vocab, num_sms() * 16), copy_threads, 0, c.st>>>(
+                    head_pad_kernel<<<(unsigned)std::min<int64_t>(c.vocab, num_sms() * 16),
+                                  (unsigned)std::min<int64_t>(256, round_up(p.ld / 8, 32)), 0, c.st>>>(
                         w, c.vocab, c.dim, p.ld, wc));
         w = wc;
     }
-    SPECOPTIM_LAUNCHED("head_gather_kernel");
+    SPECOPTIM_LAUNCHED("head_rows_kernel");
     const int64_t h_lines = ceil_div(c.dim, 64) * p.row_cap;
     if (int rc = make_tmap_2d_bf16(&g->tm_h_k, hc, h_lines, 64, 64, 128)) return rc;
     if (int rc = make_tmap_2d_bf16(&g->tm_w_k, w, c.vocab, p.ld, p.ld, 128)) return rc;
@@ -422,7 +419,7 @@ extern "C" int head_loss(const void *h, const void *w, const void *targets, int3
         if (int rc = check_call(c, p, "head_loss")) return rc;
         if (int rc = bind_device()) return rc;
         HeadGemm g;
-        return run_loss(c, p, &g);
+        return run_loss(c, p, false, &g);
     });
 }
 
@@ -443,9 +440,9 @@ extern "C" int head_loss_grad(const void *h, const void *w, const void *targets,
             return fail(SPECOPTIM_ERR_MISALIGNED, "head_loss_grad: dh and dw must be aligned to their elements");
         if (int rc = bind_device()) return rc;
         HeadGemm g;
-        if (int rc = run_loss(c, p, &g)) return rc;
+        if (int rc = run_loss(c, p, true, &g)) return rc;
         const int64_t p_lines = (int64_t)(p.piece / 64) * p.row_cap;
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < std::min(p.pieces, 2); ++b) {
             char *piece = c.ws + (b ? p.off_p1 : p.off_p0);
             if (int rc = make_tmap_2d_bf16(&g.tm_p_k[b], piece, p_lines, 64, 64, 128)) return rc;
             if (int rc = make_tmap_2d_bf16(&g.tm_p[b], piece, p_lines, 64, 64, 64)) return rc;
