@@ -9,10 +9,16 @@
 // All of it is one pass over the data: a block holds a row in registers (8
 // values per thread and step), so the row is read once, its mean square and
 // its groups' maxima are reduced by shuffles, and everything derived from it is
-// written from the same registers.  What bounds both directions is the DRAM
-// traffic.  Where rows are multiples of 16 bytes a group of 128 values lies in 16
-// neighbouring lanes; otherwise (rowvec.cuh) a thread's 8 values may belong to
-// two groups, and the groups' maxima meet in shared memory.
+// written from the same registers.  The backward pass reads the next row while
+// it works on one.  What bounds both directions is the DRAM traffic.
+//
+// Rows that are not multiples of 16 bytes (rowvec.cuh) are cut where memory is,
+// not where the row is: a thread's 8 values are one 16-byte piece of the
+// tensors (32 bytes in fp32), whose first `ph` values may belong to the row in
+// front.  A block's rows lie a multiple of 8 rows apart, so ph is the same for
+// all of them.  16 neighbouring threads then hold a group of 128 values, except
+// that its last ph values are the first ph of the next 16 threads' first piece:
+// those two maxima meet in shared memory.
 //
 // The norm statistics and every sum are fp32.  The checkpoint is the only
 // tensor below 16 bits: e4m3 with a scale per 128 values keeps each value to
@@ -33,19 +39,34 @@ constexpr float kFp8Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
 
 // Sum over the block of one value per thread, to all threads, in a fixed order.
-// `red` is one buffer of 32 floats per call site and parity of the loop, so one
-// barrier is enough.
-__device__ __forceinline__ float block_sum(float v, float *red) {
+// `red` holds one value per warp and zeros behind them (at most 16 warps), a
+// buffer per parity of the loop, so one barrier is enough.
+constexpr int kMaxWarps = kMaxThreads / 32;
+struct BlockSum {
+    float (*red)[kMaxWarps];
+    int warps;
+
+    __device__ __forceinline__ void init() const {
+        for (int i = threadIdx.x; i < 2 * kMaxWarps; i += blockDim.x) (&red[0][0])[i] = 0.f;
+        __syncthreads();
+    }
+    __device__ __forceinline__ float operator()(float v, int parity) const {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int i = 0; i < warps; ++i) v += red[i];
-    return v;
-}
+        for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (warps == 1) return v;
+        if ((threadIdx.x & 31) == 0) red[parity][threadIdx.x >> 5] = v;
+        __syncthreads();
+        const float4 *r = reinterpret_cast<const float4 *>(red[parity]);
+        float4 a = r[0];
+#pragma unroll
+        for (int i = 1; i < kMaxWarps / 4; ++i) {
+            if (warps <= 4 * i) break;
+            const float4 b = r[i];
+            a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        }
+        return (a.x + a.y) + (a.z + a.w);
+    }
+};
 
 __device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -63,50 +84,148 @@ __device__ __forceinline__ void from_fp8x4(uint32_t u, float *v) {
     }
 }
 
-// Columns col .. col + 7 of the row that begins at `row`, as far as they lie in
-// [0, dim): a vector where the piece lies in the row and on a boundary.
-template <typename T>
-__device__ __forceinline__ void store_span(const Span<T> &s, int64_t row, int col, int dim, const float (&v)[8]) {
-    if (((row + col) & 7) == 0) {
-        store_any(s, row + col, row, row + dim, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (col + i >= 0 && col + i < dim) s.p[row + col + i] = from_f<T>(v[i]);
-}
-__device__ __forceinline__ void store_q8(const Span<uint8_t> &s, int64_t row, int col, int dim, uint2 v) {
-    if (col >= 0 && col + 8 <= dim && ((row + col) & 7) == 0) {
-        *reinterpret_cast<uint2 *>(s.p + row + col) = v;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (col + i >= 0 && col + i < dim) s.p[row + col + i] = (uint8_t)((i < 4 ? v.x : v.y) >> (8 * (i & 3)));
-}
-
-// largest magnitude of v[from..to), infinite where one of them is a NaN (fmaxf
-// drops it): the group's scale then marks the group
-__device__ __forceinline__ float magnitude(const float (&v)[8], int from, int to) {
-    float m = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (i < from || i >= to) continue;
-        m = fmaxf(m, fabsf(v[i]));
-        bad |= v[i] != v[i];
-    }
-    return bad ? __int_as_float(0x7f800000) : m;
-}
-__device__ __forceinline__ float scale_of(float m) { return fmaxf(m / kFp8Max, kTinyScale); }
-
 __device__ __forceinline__ void unpack_q8(uint2 u, float (&v)[8]) {
     from_fp8x4(u.x, v);
     from_fp8x4(u.y, v + 4);
 }
 
-// The tensors of one call as spans, and their width.  All of a type that are 16
-// byte aligned begin each row at the same place between two boundaries.
+// How the rows lie: multiples of 16 bytes from a 16-byte boundary; not multiples,
+// but all tensors from a 16-byte boundary; anything else.
+enum Rows : int { ROWS_VEC = 0, ROWS_ODD = 1, ROWS_ANY = 2 };
+
+template <typename T> struct Raw8 {
+    uint4 a[sizeof(T) / 2];
+};
+__device__ __forceinline__ void values(const Raw8<bf16> &r, float (&v)[8]) {
+    const uint4 u = r.a[0];
+    v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
+    v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
+}
+__device__ __forceinline__ void values(const Raw8<float> &r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[4 * i] = __uint_as_float(r.a[i].x);
+        v[4 * i + 1] = __uint_as_float(r.a[i].y);
+        v[4 * i + 2] = __uint_as_float(r.a[i].z);
+        v[4 * i + 3] = __uint_as_float(r.a[i].w);
+    }
+}
+__device__ __forceinline__ void raw_of(const float (&v)[8], Raw8<bf16> &r) {
+    r.a[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void raw_of(const float (&v)[8], Raw8<float> &r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        r.a[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                            __float_as_uint(v[4 * i + 3]));
+}
+
+// values i .. i + 7 counted from the tensor's first one
+template <int ROWS, typename T> __device__ __forceinline__ Raw8<T> load_raw(const Span<const T> &s, int64_t i) {
+    Raw8<T> r;
+    if (ROWS == ROWS_VEC || (ROWS == ROWS_ODD && i + 8 <= s.hi)) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(s.p + i);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.a[k] = __ldg(q + k);
+    } else {
+        float v[8];
+        if (ROWS == ROWS_ANY) {
+            load_any(s, s.lo + i, v);
+        } else {  // the tensor's last piece is cut short
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = i + k < s.hi ? to_f(s.p[i + k]) : 0.f;
+        }
+        raw_of(v, r);  // exact: the values are the tensor's own
+    }
+    return r;
+}
+template <int ROWS> __device__ __forceinline__ uint2 load_q(const Span<const uint8_t> &s, int64_t i) {
+    if (ROWS == ROWS_VEC || (ROWS == ROWS_ODD && i + 8 <= s.hi)) return __ldg(reinterpret_cast<const uint2 *>(s.p + s.lo + i));
+    if (ROWS == ROWS_ANY) return load_any8(s, s.lo + i);
+    uint32_t u[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (i + k < s.hi) u[k / 4] |= (uint32_t)s.p[i + k] << (8 * (k & 3));
+    return make_uint2(u[0], u[1]);
+}
+
+template <typename T> __device__ __forceinline__ bool aligned_piece(const T *p) {
+    return (reinterpret_cast<uintptr_t>(p) & (sizeof(T) == 1 ? 7 : 15)) == 0;
+}
+// v to columns col .. col + 7 of the row that begins at value `row`, as far as they exist
+template <int ROWS, typename T>
+__device__ __forceinline__ void store_row(const Span<T> &s, int64_t row, int col, int dim, const float (&v)[8]) {
+    T *p = s.p + s.lo + row + col;
+    if (ROWS == ROWS_VEC || (col >= 0 && col + 8 <= dim && (ROWS == ROWS_ODD || aligned_piece(p)))) {
+        store8(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i >= 0 && col + i < dim) p[i] = from_f<T>(v[i]);
+    }
+}
+// the same for values that are packed already
+template <int ROWS, typename T>
+__device__ __forceinline__ void store_raw(const Span<T> &s, int64_t row, int col, int dim, const Raw8<T> &r) {
+    T *p = s.p + s.lo + row + col;
+    if (ROWS == ROWS_VEC || (col >= 0 && col + 8 <= dim && (ROWS == ROWS_ODD || aligned_piece(p)))) {
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) reinterpret_cast<uint4 *>(p)[k] = r.a[k];
+    } else {
+        float v[8];
+        values(r, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i >= 0 && col + i < dim) p[i] = from_f<T>(v[i]);
+    }
+}
+template <int ROWS>
+__device__ __forceinline__ void store_q(const Span<uint8_t> &s, int64_t row, int col, int dim, uint2 v) {
+    uint8_t *p = s.p + s.lo + row + col;
+    if (ROWS == ROWS_VEC || (col >= 0 && col + 8 <= dim && (ROWS == ROWS_ODD || aligned_piece(p)))) {
+        *reinterpret_cast<uint2 *>(p) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i >= 0 && col + i < dim) p[i] = (uint8_t)((i < 4 ? v.x : v.y) >> (8 * (i & 3)));
+    }
+}
+
+// zeros for the values that belong to the rows in front and behind
+template <int ROWS> __device__ __forceinline__ void mask_row(float (&v)[8], int col, int dim) {
+    if (ROWS != ROWS_VEC && (col < 0 || col + 8 > dim)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < 0 || col + i >= dim) v[i] = 0.f;
+    }
+}
+
+template <int ROWS, typename T>
+__device__ __forceinline__ void load_gamma(const Span<const T> &gamma, int col, float (&g)[8]) {
+    if (ROWS == ROWS_VEC) load8(gamma.p + col, g);
+    else load_any(gamma, gamma.lo + col, g);
+}
+
+// largest of a and |b|, NaN if one of them is (fmaxf would drop it)
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
+    return m;
+}
+// A group's scale from its largest magnitude: infinite where that is a NaN, which
+// marks the group like an infinity does.
+__device__ __forceinline__ float scale_of(float m) {
+    return m == m ? fmaxf(m / kFp8Max, kTinyScale) : __int_as_float(0x7f800000);
+}
+
+// q of 8 values; the first ph of them are divided by another scale
+__device__ __forceinline__ uint2 quantise8(const float (&s)[8], float inv_lo, float inv_hi, int ph) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = s[i] * (i < ph ? inv_lo : inv_hi);
+    return make_uint2(to_fp8x4(t[0], t[1], t[2], t[3]), to_fp8x4(t[4], t[5], t[6], t[7]));
+}
+
 template <typename T> struct Forward {
     Span<const T> x, r, gamma;
     Span<T> s, y;
@@ -114,127 +233,127 @@ template <typename T> struct Forward {
     float *scale, *rstd;
     int64_t rows;
     int dim;
-    float eps;
+    float inv_dim, eps;
 };
 
-// q of the 8 values and their group's (or two groups') scales
-__device__ __forceinline__ uint2 quantise8(const float (&s)[8], float inv_lo, float inv_hi, int cut) {
-    float t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = s[i] * (i < cut ? inv_lo : inv_hi);
-    return make_uint2(to_fp8x4(t[0], t[1], t[2], t[3]), to_fp8x4(t[4], t[5], t[6], t[7]));
-}
-
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(512) resnorm_forward_kernel(const Forward<T> a) {
-    __shared__ float red[2][32];
-    __shared__ int group_max[VEC ? 1 : 3][VEC ? 1 : kMaxGroups + 1];
+template <typename T, int ROWS, int NV>
+__global__ void __launch_bounds__(kMaxThreads, NV * sizeof(T) <= 4 ? 2 : 1) resnorm_forward_kernel(const Forward<T> a) {
+    __shared__ __align__(16) float red[2][kMaxWarps];
+    // of each 16 threads' pieces: the maximum of their own group, and of the ph values in front of it
+    __shared__ float group_max[2][ROWS == ROWS_VEC ? 1 : kMaxGroups + 2], head_max[2][ROWS == ROWS_VEC ? 1 : kMaxGroups + 2];
     const int dim = a.dim, groups = (dim + kGroup - 1) / kGroup;
-    if (!VEC) {
-        for (int i = threadIdx.x; i < 3 * (kMaxGroups + 1); i += blockDim.x) (&group_max[0][0])[i] = 0;
-        __syncthreads();
+    const int ph = ROWS == ROWS_VEC ? 0 : (int)((a.y.lo + (int64_t)blockIdx.x * dim) & 7);
+    const int col0 = (int)threadIdx.x * 8 - ph, step = (int)blockDim.x * 8;
+    const int hl = threadIdx.x & 15;
+    if (ROWS != ROWS_VEC)
+        for (int i = threadIdx.x; i < kMaxGroups + 2; i += blockDim.x) head_max[0][i] = head_max[1][i] = 0.f;
+    const BlockSum block_sum{red, (int)blockDim.x >> 5};
+    block_sum.init();
+    float gm[NV <= 2 ? NV : 1][8];
+    if (NV <= 2) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (col0 + k * step < dim) load_gamma<ROWS>(a.gamma, col0 + k * step, gm[k]);
     }
-    int parity = 0, turn = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1, turn = turn == 2 ? 0 : turn + 1) {
+    int parity = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
         const int64_t base = row * dim;
-        const int first = VEC ? 0 : -(int)((a.y.lo + base) & 7);  // column where the row's first piece begins
         float s[NV][8];
+        {
+            Raw8<T> x[NV], r[NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+            for (int k = 0; k < NV; ++k)
+                if (col0 + k * step < dim) x[k] = load_raw<ROWS>(a.x, base + col0 + k * step);
+            if (a.r.p) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[k][i] = 0.f;
-            if (col >= dim) continue;
-            if (VEC) load8(a.x.p + base + col, s[k]);
-            else load_any(a.x, a.x.lo + base + col, s[k]);
-        }
-        if (a.r.p) {
-            float b[NV][8];
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) b[k][i] = 0.f;
-                if (col >= dim) continue;
-                if (VEC) load8(a.r.p + base + col, b[k]);
-                else load_any(a.r, a.r.lo + base + col, b[k]);
+                for (int k = 0; k < NV; ++k)
+                    if (col0 + k * step < dim) r[k] = load_raw<ROWS>(a.r, base + col0 + k * step);
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
-                // the stream is held in T: norm and checkpoint are those of the rounded sum
+                const int col = col0 + k * step;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[k][i] = to_f(from_f<T>(s[k][i] + b[k][i]));
+                for (int i = 0; i < 8; ++i) s[k][i] = 0.f;
                 if (col >= dim) continue;
-                if (VEC) store8(a.s.p + base + col, s[k]);
-                else store_span(a.s, a.s.lo + base, col, dim, s[k]);
+                values(x[k], s[k]);
+                if (a.r.p) {
+                    float b[8];
+                    values(r[k], b);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[k][i] += b[i];
+                    // the stream is held in T: norm and checkpoint are those of the rounded sum
+                    raw_of(s[k], x[k]);
+                    values(x[k], s[k]);
+                    store_raw<ROWS>(a.s, base, col, dim, x[k]);
+                }
+                mask_row<ROWS>(s[k], col, dim);
             }
         }
         float ss = 0.f;
 #pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(s[k][i], s[k][i], ss);
+#pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+            const int col = col0 + k * step;
+            float m = 0.f, head = 0.f;  // head: of the first ph values, which may belong to the group in front
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (!VEC && (col + i < 0 || col + i >= dim)) s[k][i] = 0.f;  // the neighbouring rows' values
-                ss = fmaf(s[k][i], s[k][i], ss);
+                if (ROWS != ROWS_VEC && i < ph) head = max_nan(head, s[k][i]);
+                else m = max_nan(m, s[k][i]);
             }
-        }
-        if (VEC) {
-            // the checkpoint needs no row sum: it is written while the sum is under way
+            if (ROWS != ROWS_VEC && hl != 0) m = max_nan(m, head);
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = (k * blockDim.x + threadIdx.x) * 8;
-                float m = magnitude(s[k], 0, 8);
-#pragma unroll
-                for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int o = 8; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (ROWS == ROWS_VEC) {
+                // the checkpoint needs no row sum: it is written while the sum is under way
                 const float sc = scale_of(m), inv = 1.f / sc;
                 if (col >= dim) continue;
-                *reinterpret_cast<uint2 *>(a.q.p + a.q.lo + base + col) = quantise8(s[k], inv, inv, 8);
-                if ((threadIdx.x & 15) == 0) a.scale[row * groups + col / kGroup] = sc;
+                store_q<ROWS>(a.q, base, col, dim, quantise8(s[k], inv, inv, 0));
+                if (hl == 0) a.scale[row * groups + col / kGroup] = sc;
+            } else if (hl == 0) {
+                const int h = (k * (int)blockDim.x + (int)threadIdx.x) / 16;
+                if (h <= kMaxGroups) {
+                    group_max[parity][h] = m;
+                    head_max[parity][h] = head;
+                }
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
-                if (col >= dim) continue;
-                const int g = max(col, 0) / kGroup, cut = min(8, (g + 1) * kGroup - col);
-                atomicMax(&group_max[turn][g], __float_as_int(magnitude(s[k], 0, cut)));
-                if (cut < 8) atomicMax(&group_max[turn][g + 1], __float_as_int(magnitude(s[k], cut, 8)));
-            }
-            __syncwarp();  // one warp: block_sum has no barrier
         }
-        ss = block_sum(ss, red[parity]);
-        const float rs = 1.f / sqrtf(ss / (float)dim + a.eps);
+        if (ROWS != ROWS_VEC) __syncwarp();  // one warp: block_sum has no barrier
+        const float rs = rsqrtf(fmaf(block_sum(ss, parity), a.inv_dim, a.eps));
         if (threadIdx.x == 0) a.rstd[row] = rs;
-        if (!VEC) {
-            // the previous row's maxima have been read by all; they are used again the row after next
-            int *stale = group_max[turn == 0 ? 2 : turn - 1];
-            for (int i = threadIdx.x; i < groups; i += blockDim.x) {
-                stale[i] = 0;
-                a.scale[row * groups + i] = scale_of(__int_as_float(group_max[turn][i]));
-            }
+        if (ROWS != ROWS_VEC) {
+            // a warp's pieces lie in two groups and end the one in front of them: lanes 0 to 2
+            // form the three scales, the others repeat the last
+            const int lane = threadIdx.x & 31;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
-                if (col >= dim) continue;
-                const int g = max(col, 0) / kGroup, cut = min(8, (g + 1) * kGroup - col);
-                const float lo = 1.f / scale_of(__int_as_float(group_max[turn][g]));
-                const float hi = cut < 8 ? 1.f / scale_of(__int_as_float(group_max[turn][g + 1])) : lo;
-                store_q8(a.q, a.q.lo + base, col, dim, quantise8(s[k], lo, hi, cut));
+                const int col = col0 + k * step;
+                const int g = (k * (int)blockDim.x + (int)threadIdx.x - lane) / 16 + min(lane, 2) - 1;
+                const float sc = scale_of(g >= 0 ? max_nan(group_max[parity][g], head_max[parity][g + 1]) : 0.f);
+                const float inv = 1.f / sc;
+                const float hi = __shfl_sync(0xffffffffu, inv, 1 + (lane >> 4));
+                float lo = __shfl_sync(0xffffffffu, inv, lane >> 4);
+                if (hl != 0) lo = hi;
+                if ((lane == 1 || lane == 2) && g < groups) a.scale[row * groups + g] = sc;
+                if (col < dim) store_q<ROWS>(a.q, base, col, dim, quantise8(s[k], lo, hi, ph));
             }
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+            const int col = col0 + k * step;
             if (col >= dim) continue;
-            float g[8];
-            if (VEC) load8(a.gamma.p + col, g);
-            else load_any(a.gamma, a.gamma.lo + col, g);
+            if (NV <= 2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[k][i] = s[k][i] * rs * g[i];
-            if (VEC) store8(a.y.p + base + col, s[k]);
-            else store_span(a.y, a.y.lo + base, col, dim, s[k]);
+                for (int i = 0; i < 8; ++i) s[k][i] = s[k][i] * rs * gm[k < 2 ? k : 0][i];
+            } else {
+                float g[8];
+                load_gamma<ROWS>(a.gamma, col, g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[k][i] = s[k][i] * rs * g[i];
+            }
+            store_row<ROWS>(a.y, base, col, dim, s[k]);
         }
     }
 }
@@ -247,87 +366,191 @@ template <typename T> struct Backward {
     float *partial;
     int64_t rows;
     int dim, pitch;
+    float inv_dim;
 };
 
-// n of 8 values: q times the scale of their group (or two groups) times rstd, 0
-// outside the row
-template <bool VEC>
-__device__ __forceinline__ void load_n(const Span<const uint8_t> &q, const float *scale, int64_t row, int groups,
-                                       int col, int dim, float rs, float (&n)[8]) {
-    const int64_t at = q.lo + row * dim + col;
-    unpack_q8(VEC ? __ldg(reinterpret_cast<const uint2 *>(q.p + at)) : load_any8(q, at), n);
-    const int g = VEC ? col / kGroup : max(col, 0) / kGroup, cut = VEC ? 8 : min(8, (g + 1) * kGroup - col);
-    const float lo = __ldg(scale + row * groups + g);
-    const float hi = !VEC && cut < 8 && g + 1 < groups ? __ldg(scale + row * groups + g + 1) : lo;
+// The scales of the first ph values of a row's piece and of the others (piece
+// h * 16 + 0 .. 15 of the row, the thread's place among 16 being hl).
+struct Scales {
+    float lo, hi;
+};
+template <int ROWS>
+__device__ __forceinline__ Scales load_scales(const float *scale, int64_t row, int groups, int h, int hl) {
+    const float *sc = scale + row * groups;
+    Scales s;
+    s.hi = __ldg(sc + (ROWS == ROWS_VEC ? h : min(h, groups - 1)));
+    s.lo = ROWS != ROWS_VEC && hl == 0 && h > 0 ? __ldg(sc + h - 1) : s.hi;
+    return s;
+}
+// n = q * scale * rstd, 0 outside the row
+template <int ROWS>
+__device__ __forceinline__ void normed(uint2 q, const Scales &s, float rs, int ph, int col, int dim, float (&n)[8]) {
+    unpack_q8(q, n);
+    const float lo = s.lo * rs, hi = s.hi * rs;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        n[i] = n[i] * (i < cut ? lo : hi) * rs;
-        if (!VEC && (col + i < 0 || col + i >= dim)) n[i] = 0.f;
-    }
+    for (int i = 0; i < 8; ++i) n[i] *= ROWS != ROWS_VEC && i < ph ? lo : hi;
+    mask_row<ROWS>(n, col, dim);
 }
 
-template <typename T, bool VEC>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(256) resnorm_recompute_kernel(const Backward<T> a) {
     const int dim = a.dim, groups = (dim + kGroup - 1) / kGroup;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const float rs = a.rstd[row];
-        const int first = VEC ? 0 : -(int)((a.y.lo + row * dim) & 7);
-        for (int col = first + (int)threadIdx.x * 8; col < dim; col += blockDim.x * 8) {
+        const int ph = ROWS == ROWS_VEC ? 0 : (int)((a.y.lo + row * dim) & 7);
+        for (int j = threadIdx.x; j * 8 - ph < dim; j += blockDim.x) {
+            const int col = j * 8 - ph;
             float n[8], g[8];
-            load_n<VEC>(a.q, a.scale, row, groups, col, dim, rs, n);
-            if (VEC) load8(a.gamma.p + col, g);
-            else load_any(a.gamma, a.gamma.lo + col, g);
+            normed<ROWS>(load_q<ROWS>(a.q, row * dim + col), load_scales<ROWS>(a.scale, row, groups, j / 16, j & 15), rs,
+                         ph, col, dim, n);
+            load_gamma<ROWS>(a.gamma, col, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) n[i] *= g[i];
-            if (VEC) store8(a.y.p + row * dim + col, n);
-            else store_span(a.y, a.y.lo + row * dim, col, dim, n);
+            store_row<ROWS>(a.y, row * dim, col, dim, n);
         }
     }
 }
 
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Each block keeps its columns' share of dgamma in registers over all its rows
-// and writes it once, to partial[block][pitch].  Where rows begin at different
-// places, a block's rows lie a multiple of 8 rows apart and so begin alike.
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(512) resnorm_backward_kernel(const Backward<T> a) {
-    __shared__ float red[2][32];
-    const int dim = a.dim, groups = (dim + kGroup - 1) / kGroup;
-    const int first = VEC ? 0 : -(int)((a.dx.lo + (int64_t)blockIdx.x * dim) & 7);
-    float dg[NV][8];
+// and writes it once, to partial[block][pitch].
+//
+// RING > 0 (up to 16 values per thread and tensor): the rows ahead are copied to
+// shared memory asynchronously, RING - 1 of them at a time, each piece by the
+// thread that will use it, so no barrier is needed for them and the bytes in
+// flight do not depend on registers.  In registers the same width held 40 KB per
+// SM in flight, a third of what the DRAM's latency asks for at full rate.
+template <typename T, int ROWS, int NV, int RING>
+__global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) resnorm_backward_kernel(const Backward<T> a) {
+    __shared__ __align__(16) float red[2][kMaxWarps];
+    extern __shared__ __align__(16) unsigned char ring[];
+    constexpr int PIECES = (int)sizeof(T) / 2;  // 16-byte pieces of 8 values
+    constexpr int STAGES = RING > 0 ? RING : 1;
+    const int dim = a.dim, groups = (dim + kGroup - 1) / kGroup, threads = blockDim.x, tid = threadIdx.x;
+    const int ph = ROWS == ROWS_VEC ? 0 : (int)((a.dx.lo + (int64_t)blockIdx.x * dim) & 7);
+    const int col0 = tid * 8 - ph, step = threads * 8, hl = tid & 15;
+    const BlockSum block_sum{red, threads >> 5};
+    block_sum.init();
+    float dg[NV][8], gm[RING ? NV : 1][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dg[k][i] = 0.f;
-    int parity = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
-        const int64_t base = row * dim;
-        const float rs = a.rstd[row];
-        float n[NV][8], d[NV][8];
+    if (RING) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
-            if (col < dim) {
-                if (VEC) load8(a.dy.p + base + col, d[k]);
-                else load_any(a.dy, a.dy.lo + base + col, d[k]);
-                load_n<VEC>(a.q, a.scale, row, groups, col, dim, rs, n[k]);
-                if (!VEC) {
+        for (int k = 0; k < NV; ++k)
+            if (col0 + k * step < dim) load_gamma<ROWS>(a.gamma, col0 + k * step, gm[k]);
+    }
+    // ring: [stage][k][dy, ds][piece][thread] 16 bytes, then [stage][k][thread] 8 bytes of q
+    uint4 *ring16 = reinterpret_cast<uint4 *>(ring);
+    uint2 *ring8 = reinterpret_cast<uint2 *>(ring16 + STAGES * NV * 2 * PIECES * threads);
+    auto slot16 = [&](int stage, int k, int which, int piece) {
+        return ring16 + (((stage * NV + k) * 2 + which) * PIECES + piece) * threads + tid;
+    };
+    auto slot8 = [&](int stage, int k) { return ring8 + (stage * NV + k) * threads + tid; };
+    auto copy_row = [&](int64_t row, int stage) {
+        if (row < a.rows) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (col + i < 0 || col + i >= dim) d[k][i] = 0.f;
+            for (int k = 0; k < NV; ++k) {
+                const int col = col0 + k * step;
+                if (col >= dim) continue;
+                const int64_t at = row * dim + col;
+                if (ROWS == ROWS_VEC || (ROWS == ROWS_ODD && at + 8 <= a.dy.hi)) {
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) {
+                        copy_async16(slot16(stage, k, 0, p), reinterpret_cast<const uint4 *>(a.dy.p + at) + p);
+                        if (a.ds.p) copy_async16(slot16(stage, k, 1, p), reinterpret_cast<const uint4 *>(a.ds.p + at) + p);
+                    }
+                    copy_async8(slot8(stage, k), a.q.p + a.q.lo + at);
+                } else {
+                    const Raw8<T> x = load_raw<ROWS>(a.dy, at);
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) *slot16(stage, k, 0, p) = x.a[p];
+                    if (a.ds.p) {
+                        const Raw8<T> y = load_raw<ROWS>(a.ds, at);
+#pragma unroll
+                        for (int p = 0; p < PIECES; ++p) *slot16(stage, k, 1, p) = y.a[p];
+                    }
+                    *slot8(stage, k) = load_q<ROWS>(a.q, at);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[k][i] = n[k][i] = 0.f;
             }
         }
-        float t = 0.f;
+        copy_async_commit();  // a group per row, empty ones too
+    };
+    Scales sc[NV];
+    float rs = 0.f;
+    auto fetch_scales = [&](int64_t row) {
+        if (row >= a.rows) return;
+        rs = __ldg(a.rstd + row);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (col0 + k * step < dim) sc[k] = load_scales<ROWS>(a.scale, row, groups, (k * threads + tid) / 16, hl);
+    };
+    const int64_t stride = gridDim.x;
+    if (RING) {
+#pragma unroll
+        for (int i = 0; i < RING - 1; ++i) copy_row(blockIdx.x + i * stride, i);
+        fetch_scales(blockIdx.x);
+    }
+    int parity = 0, stage = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += stride, parity ^= 1) {
+        const int64_t base = row * dim;
+        float n[NV][8], d[NV][8], t = 0.f;
+        Raw8<T> add[NV];
+        if (RING) {
+            copy_async_wait<RING >= 2 ? RING - 2 : 0>();
+        } else {
+            fetch_scales(row);
+        }
+        const float r = rs;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+            const int col = col0 + k * step;
+            if (col >= dim) continue;
+            Raw8<T> x;
+            uint2 q;
+            if (RING) {
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) {
+                    x.a[p] = *slot16(stage, k, 0, p);
+                    if (a.ds.p) add[k].a[p] = *slot16(stage, k, 1, p);
+                }
+                q = *slot8(stage, k);
+            } else {
+                x = load_raw<ROWS>(a.dy, base + col);
+                q = load_q<ROWS>(a.q, base + col);
+                if (a.ds.p) add[k] = load_raw<ROWS>(a.ds, base + col);
+            }
+            values(x, d[k]);
+            mask_row<ROWS>(d[k], col, dim);
+            normed<ROWS>(q, sc[k], r, ph, col, dim, n[k]);
+        }
+        if (RING) {  // into the slots that were read a row ago
+            copy_row(row + (RING - 1) * stride, (stage + RING - 1) % STAGES);
+            fetch_scales(row + stride);
+            stage = (stage + 1) % STAGES;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int col = col0 + k * step;
             if (col >= dim) continue;
             float g[8];
-            if (VEC) load8(a.gamma.p + col, g);  // stays in L1 over the rows
-            else load_any(a.gamma, a.gamma.lo + col, g);
+            if (RING) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] = gm[RING ? k : 0][i];
+            } else {
+                load_gamma<ROWS>(a.gamma, col, g);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dg[k][i] = fmaf(d[k][i], n[k][i], dg[k][i]);
@@ -335,32 +558,27 @@ __global__ void __launch_bounds__(512) resnorm_backward_kernel(const Backward<T>
                 t = fmaf(d[k][i], n[k][i], t);
                 g[i] *= n[k][i];
             }
-            if (!a.y.p) continue;
-            if (VEC) store8(a.y.p + base + col, g);
-            else store_span(a.y, a.y.lo + base, col, dim, g);
+            if (a.y.p) store_row<ROWS>(a.y, base, col, dim, g);
         }
-        t = block_sum(t, red[parity]) / (float)dim;
+        const float rt = r * (block_sum(t, parity) * a.inv_dim);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+            const int col = col0 + k * step;
             if (col >= dim) continue;
             float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (a.ds.p) {
-                if (VEC) load8(a.ds.p + base + col, b);
-                else load_any(a.ds, a.ds.lo + base + col, b);
-            }
+            if (a.ds.p) values(add[k], b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = fmaf(rs, d[k][i] - n[k][i] * t, b[i]);
-            if (VEC) store8(a.dx.p + base + col, b);
-            else store_span(a.dx, a.dx.lo + base, col, dim, b);
+            for (int i = 0; i < 8; ++i) b[i] = fmaf(-rt, n[k][i], fmaf(r, d[k][i], b[i]));
+            store_row<ROWS>(a.dx, base, col, dim, b);
         }
     }
+    if (RING) copy_async_wait<0>();
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int col = first + (int)(k * blockDim.x + threadIdx.x) * 8;
+        const int col = col0 + k * step;
         if (col >= dim) continue;
         float *out = a.partial + (int64_t)blockIdx.x * a.pitch;
-        if (VEC) {
+        if (ROWS == ROWS_VEC) {
             store8(out + col, dg[k]);
         } else {
 #pragma unroll
@@ -370,35 +588,53 @@ __global__ void __launch_bounds__(512) resnorm_backward_kernel(const Backward<T>
     }
 }
 
-// dgamma[j] = sum over blocks of partial[block][j]: 32 columns per block, 8
+// dgamma[j] = sum over blocks of partial[block][j]: 32 columns per block, 32
 // threads per column, joined in a fixed order.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float *__restrict__ partial, int blocks, int dim,
-                                                     int pitch, float *__restrict__ dgamma) {
-    __shared__ float red[8][33];
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float *__restrict__ partial, int blocks, int dim,
+                                                      int pitch, float *__restrict__ dgamma) {
+    __shared__ float red[32][33];
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
     float a = 0.f;
     if (col < dim) {
 #pragma unroll 8
-        for (int b = w; b < blocks; b += 8) a += partial[(int64_t)b * pitch + col];
+        for (int b = w; b < blocks; b += 32) a += partial[(int64_t)b * pitch + col];
     }
     red[w][c] = a;
     __syncthreads();
-    if (w == 0 && col < dim) {
-        for (int i = 1; i < 8; ++i) a += red[i][c];
-        dgamma[col] = a;
-    }
+    a = red[c][w];  // warp w adds up column w of the block's 32
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (c == 0 && blockIdx.x * 32 + w < dim) dgamma[blockIdx.x * 32 + w] = a;
 }
 
-// Values per thread: 16 (NV = 2) up to a width of 8192, so that a row of 2048
-// takes 4 warps and many rows are in flight on an SM; then 32 and 64.
+// Values per thread of the forward pass: 16 (NV = 2) up to a width of 8192, so
+// that a row of 2048 takes 4 warps and many rows are in flight on an SM; then 32
+// and 64.  The backward pass keeps four times as much per value and takes 8 (NV
+// = 1) up to 4096.
 struct Shape {
     int nv, threads;
 };
-Shape shape_of(int dim, bool vec) {
+Shape shape_of(int dim, bool vec, bool one) {
     const int64_t vecs = vec ? dim / 8 : (dim + 14) / 8;  // 8-value pieces that a row can touch
     int nv = 1;
-    while (nv < 8 && (vecs > kMaxThreads * nv || (nv < 2 && vecs > 32))) nv *= 2;
+    while (nv < 8 && (vecs > kMaxThreads * nv || (!one && nv < 2 && vecs > 32))) nv *= 2;
     return {nv, (int)round_up(ceil_div(vecs, nv), 32)};
+}
+
+// Rows in the ring of the backward pass: four (three on their way while one is
+// worked on), two where four do not fit, none for wide rows.
+constexpr int ring_of(int nv, int value_bytes) { return nv == 1 ? 4 : nv == 2 ? (value_bytes == 2 ? 4 : 2) : 0; }
+constexpr int ring_bytes(const Shape &sh, int value_bytes) {
+    return sh.threads * sh.nv * ring_of(sh.nv, value_bytes) * (2 * 8 * value_bytes + 8);
+}
+
+// Resident blocks: what registers and shared memory allow.  A multiple of 8
+// where there are that many rows: a block's rows then begin alike.
+int backward_blocks(int64_t rows, const Shape &sh, int value_bytes) {
+    const int by_threads = (sh.nv == 1 ? 1024 : 512) / sh.threads;
+    const int by_smem = 220 * 1024 / std::max(1, ring_bytes(sh, value_bytes) + 1024);
+    const int per_sm = std::max(1, std::min({8, by_threads, by_smem}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms() * per_sm / 8 * 8));
 }
 
 template <typename F> int with_nv(int nv, F &&f) {
@@ -410,14 +646,6 @@ template <typename F> int with_nv(int nv, F &&f) {
     }
 }
 
-constexpr int kBackwardBlocksPerSm = 8;
-
-// A multiple of 8 where there are that many rows (see resnorm_backward_kernel)
-int backward_blocks(int64_t rows, const Shape &sh) {
-    const int per_sm = std::max(1, std::min(kBackwardBlocksPerSm, 1024 / sh.threads));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(rows, (int64_t)num_sms() * per_sm / 8 * 8));
-}
-
 int check_sizes(int64_t rows, int32_t dim, int32_t type, const char *what) {
     if (rows < 0 || rows > INT32_MAX)
         return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": rows outside [0, 2^31)");
@@ -427,11 +655,13 @@ int check_sizes(int64_t rows, int32_t dim, int32_t type, const char *what) {
     return SPECOPTIM_OK;
 }
 
-template <typename T> int run_forward(const Shape &sh, bool vec, const Forward<T> &a, cudaStream_t st) {
+template <typename T> int run_forward(const Shape &sh, int rows, const Forward<T> &a, cudaStream_t st) {
     return with_nv(sh.nv, [&](auto nv) -> int {
         constexpr int NV = decltype(nv)::value;
         const int grid = (int)std::min<int64_t>(a.rows, (int64_t)num_sms() * 64);
-        auto *k = vec ? &resnorm_forward_kernel<T, true, NV> : &resnorm_forward_kernel<T, false, NV>;
+        auto *k = rows == ROWS_VEC   ? &resnorm_forward_kernel<T, ROWS_VEC, NV>
+                  : rows == ROWS_ODD ? &resnorm_forward_kernel<T, ROWS_ODD, NV>
+                                     : &resnorm_forward_kernel<T, ROWS_ANY, NV>;
         SPCO_LAUNCH("resnorm_forward", st, k<<<grid, sh.threads, 0, st>>>(a));
         SPECOPTIM_LAUNCHED("resnorm_forward_kernel");
         return SPECOPTIM_OK;
@@ -439,17 +669,30 @@ template <typename T> int run_forward(const Shape &sh, bool vec, const Forward<T
 }
 
 template <typename T>
-int run_backward(const Shape &sh, bool vec, int blocks, const Backward<T> &a, float *dgamma, cudaStream_t st) {
+int run_backward(const Shape &sh, int rows, int blocks, const Backward<T> &a, float *dgamma, cudaStream_t st) {
     return with_nv(sh.nv, [&](auto nv) -> int {
         constexpr int NV = decltype(nv)::value;
-        auto *k = vec ? &resnorm_backward_kernel<T, true, NV> : &resnorm_backward_kernel<T, false, NV>;
-        SPCO_LAUNCH("resnorm_backward", st, k<<<blocks, sh.threads, 0, st>>>(a));
+        constexpr int RING = ring_of(NV, sizeof(T));
+        auto *k = rows == ROWS_VEC   ? &resnorm_backward_kernel<T, ROWS_VEC, NV, RING>
+                  : rows == ROWS_ODD ? &resnorm_backward_kernel<T, ROWS_ODD, NV, RING>
+                                     : &resnorm_backward_kernel<T, ROWS_ANY, NV, RING>;
+        const int smem = ring_bytes(sh, sizeof(T));
+        if (smem > 48 * 1024)
+            if (int rc = set_smem_limit(reinterpret_cast<const void *>(k), smem)) return rc;
+        SPCO_LAUNCH("resnorm_backward", st, k<<<blocks, sh.threads, smem, st>>>(a));
         SPECOPTIM_LAUNCHED("resnorm_backward_kernel");
         SPCO_LAUNCH("resnorm_dgamma", st,
-                    dgamma_kernel<<<(unsigned)ceil_div(a.dim, 32), 256, 0, st>>>(a.partial, blocks, a.dim, a.pitch, dgamma));
+                    dgamma_kernel<<<(unsigned)ceil_div(a.dim, 32), 1024, 0, st>>>(a.partial, blocks, a.dim, a.pitch, dgamma));
         SPECOPTIM_LAUNCHED("dgamma_kernel");
         return SPECOPTIM_OK;
     });
+}
+
+// how the rows of the given tensors lie
+int rows_of(int dim, std::initializer_list<const void *> tensors) {
+    for (const void *p : tensors)
+        if (!aligned16(p)) return ROWS_ANY;
+    return dim % 8 == 0 ? ROWS_VEC : ROWS_ODD;
 }
 
 // f(T{}) for the tensors' type
@@ -473,9 +716,8 @@ extern "C" int resnorm_forward(const void *x, const void *r, const void *gamma, 
             !aligned_to(scale, 4) || !aligned_to(rstd, 4))
             return fail(SPECOPTIM_ERR_MISALIGNED, "resnorm_forward: pointers must be aligned to their elements");
         if (int rc = bind_device()) return rc;
-        const bool vec = dim % 8 == 0 && aligned16(x) && aligned16(r) && aligned16(gamma) && aligned16(y) &&
-                         (!r || aligned16(s)) && aligned_to(q, 8);
-        const Shape sh = shape_of(dim, vec);
+        const int layout = rows_of(dim, {x, r, gamma, y, r ? s : nullptr, q});
+        const Shape sh = shape_of(dim, layout == ROWS_VEC, layout != ROWS_VEC || type != STAGE_BF16);
         const int64_t n = rows * dim;
         return with_type(type, [&](auto t) -> int {
             using T = decltype(t);
@@ -489,8 +731,9 @@ extern "C" int resnorm_forward(const void *x, const void *r, const void *gamma, 
                                rstd,
                                rows,
                                dim,
+                               1.f / (float)dim,
                                eps};
-            return run_forward<T>(sh, vec, a, static_cast<cudaStream_t>(stream));
+            return run_forward<T>(sh, layout, a, static_cast<cudaStream_t>(stream));
         });
     });
 }
@@ -506,7 +749,7 @@ extern "C" int resnorm_recompute(const void *q, const float *scale, const float 
         if (!aligned_to(gamma, b) || !aligned_to(y, b) || !aligned_to(scale, 4) || !aligned_to(rstd, 4))
             return fail(SPECOPTIM_ERR_MISALIGNED, "resnorm_recompute: pointers must be aligned to their elements");
         if (int rc = bind_device()) return rc;
-        const bool vec = dim % 8 == 0 && aligned16(gamma) && aligned16(y) && aligned_to(q, 8);
+        const int layout = rows_of(dim, {gamma, y, q});
         const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim + 7, 8), 32));
         const int grid = (int)std::min<int64_t>(rows, (int64_t)num_sms() * 64);
         const int64_t n = rows * dim;
@@ -524,8 +767,11 @@ extern "C" int resnorm_recompute(const void *q, const float *scale, const float 
                                 nullptr,
                                 rows,
                                 dim,
-                                dim};
-            auto *k = vec ? &resnorm_recompute_kernel<T, true> : &resnorm_recompute_kernel<T, false>;
+                                dim,
+                                0.f};
+            auto *k = layout == ROWS_VEC   ? &resnorm_recompute_kernel<T, ROWS_VEC>
+                      : layout == ROWS_ODD ? &resnorm_recompute_kernel<T, ROWS_ODD>
+                                           : &resnorm_recompute_kernel<T, ROWS_ANY>;
             SPCO_LAUNCH("resnorm_recompute", st, k<<<grid, threads, 0, st>>>(a));
             SPECOPTIM_LAUNCHED("resnorm_recompute_kernel");
             return SPECOPTIM_OK;
@@ -537,9 +783,12 @@ extern "C" int64_t resnorm_backward_workspace(int64_t rows, int32_t dim) {
     int64_t bytes = -1;
     entry([&]() -> int {
         if (int rc = check_sizes(rows, dim, STAGE_BF16, "resnorm_backward")) return rc;
-        // of the two shapes the one with more blocks: the pointers' alignment is not known yet
-        bytes = (int64_t)std::max(backward_blocks(rows, shape_of(dim, true)), backward_blocks(rows, shape_of(dim, false))) *
-                round_up(dim, 8) * 4;
+        // the most blocks of any type and layout: the call's are not known yet
+        int blocks = 0;
+        for (const bool vec : {true, false})
+            for (const int value_bytes : {2, 4})
+                blocks = std::max(blocks, backward_blocks(rows, shape_of(dim, vec, true), value_bytes));
+        bytes = (int64_t)blocks * round_up(dim, 8) * 4;
         return SPECOPTIM_OK;
     });
     return bytes;
@@ -557,10 +806,9 @@ extern "C" int resnorm_backward(const void *dy, const void *ds, const void *q, c
             !aligned_to(y, b) || !aligned_to(scale, 4) || !aligned_to(rstd, 4) || !aligned_to(dgamma, 4) ||
             !aligned16(workspace))
             return fail(SPECOPTIM_ERR_MISALIGNED, "resnorm_backward: pointers must be aligned to their elements, the workspace to 16 bytes");
-        const bool vec = dim % 8 == 0 && aligned16(dy) && aligned16(ds) && aligned16(gamma) && aligned16(dx) &&
-                         aligned16(y) && aligned_to(q, 8);
-        const Shape sh = shape_of(dim, vec);
-        const int blocks = backward_blocks(rows, sh), pitch = (int)round_up(dim, 8);
+        const int layout = rows_of(dim, {dy, ds, gamma, dx, y, q});
+        const Shape sh = shape_of(dim, layout == ROWS_VEC, true);
+        const int blocks = backward_blocks(rows, sh, (int)type_bytes(type)), pitch = (int)round_up(dim, 8);
         if (workspace_bytes < (int64_t)blocks * pitch * 4)
             return fail(SPECOPTIM_ERR_INVALID_ARG, "resnorm_backward: the workspace is smaller than resnorm_backward_workspace() says");
         if (int rc = bind_device()) return rc;
@@ -578,8 +826,9 @@ extern "C" int resnorm_backward(const void *dy, const void *ds, const void *q, c
                                 static_cast<float *>(workspace),
                                 rows,
                                 dim,
-                                pitch};
-            return run_backward<T>(sh, vec, blocks, a, dgamma, static_cast<cudaStream_t>(stream));
+                                pitch,
+                                1.f / (float)dim};
+            return run_backward<T>(sh, layout, blocks, a, dgamma, static_cast<cudaStream_t>(stream));
         });
     });
 }
