@@ -191,28 +191,50 @@ __device__ __forceinline__ Tile tile_at(const HeadGemm &g, const Walk &w, int i,
 
 // ---- epilogues: thread = one row of the tile, 32 columns at a time -------------------
 
+// f(c, v) for the 32-column blocks c = 0 .. blocks - 1 of this warp's rows and
+// columns; the next block is on its way from TMEM while f works on one.
+template <typename F> __device__ __forceinline__ void for_columns(uint32_t taddr, int blocks, F &&f) {
+    uint32_t next[32];
+    __syncwarp();
+    if (blocks > 0) tmem_ld32_begin(taddr, next);
+    for (int c = 0; c < blocks; ++c) {
+        float v[32];
+        tmem_ld32_end(next);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(next[i]);
+        __syncwarp();
+        if (c + 1 < blocks) tmem_ld32_begin(taddr + (c + 1) * 32, next);
+        f(c, v);
+        __syncwarp();
+    }
+}
+
+// how many of a warp's four 32-column blocks begin in front of `end`
+__device__ __forceinline__ int blocks_before(int first, int end) { return min(4, max(0, (end - first + 31) / 32)); }
+
+// The part's sum is taken relative to 2^r, r the largest logit times log2(e)
+// rounded to a whole number: the exponent of each term is then one fused
+// multiply-add, and parts are joined by exact powers of two.
 __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Walk &w, const Tile &x, uint32_t acc, int q,
                                                int lane, int half) {
     const int row = x.m + x.rank * CM + q * 32 + lane;
     const int target = row < w.rows ? g.target[row] : -1;
-    float m = -INFINITY, s = 0.f;
-    for (int c = 0; c < BN / 2 / 32; ++c) {
-        const int col0 = half * (BN / 2) + c * 32, v0 = x.n + col0;
-        if (v0 >= g.vocab) break;
-        float v[32];
-        __syncwarp();
-        tmem_ld32(acc + col0 + ((uint32_t)(q * 32) << 16), v);
+    const int first = x.n + half * (BN / 2);
+    float r = -INFINITY, s = 0.f;
+    for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), blocks_before(first, g.vocab), [&](int c, float (&v)[32]) {
+        const int v0 = first + c * 32;
         if (v0 + 32 > g.vocab) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (v0 + i >= g.vocab) v[i] = -INFINITY;
         }
-        float top = v[0];
+        float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-        if (top > m) {
-            s *= ex2((m - top) * kLog2e);
-            m = top;
+        for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+        const float most = rintf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e);
+        if (most > r) {
+            s *= ex2(r - most);
+            r = most;
         }
         if ((unsigned)(target - v0) < 32u) {  // the target's own term is added when the parts are joined
 #pragma unroll
@@ -220,13 +242,13 @@ __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Walk &w,
                 if (v0 + i == target) v[i] = -INFINITY;
         }
         // all -inf so far: any finite reference gives exp = 0 (and keeps a NaN visible)
-        const float ref = m == -INFINITY ? 0.f : m;
+        const float ref = r == -INFINITY ? 0.f : r;
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) part[i & 3] += ex2((v[i] - ref) * kLog2e);
+        for (int i = 0; i < 32; ++i) part[i & 3] += ex2(fmaf(v[i], kLog2e, -ref));
         s += (part[0] + part[1]) + (part[2] + part[3]);
-    }
-    if (row < w.rows) g.stats[(int64_t)(x.n / (BN / 2) + half) * g.row_cap + row] = make_float2(m, s);
+    });
+    if (row < w.rows) g.stats[(int64_t)(x.n / (BN / 2) + half) * g.row_cap + row] = make_float2(r, s);
 }
 
 // A warp's way out: 32 rows of 128 bytes (64 bf16 or 32 fp32 columns) are laid
@@ -272,33 +294,32 @@ __device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Walk &w, 
     const int row0 = x.m + x.rank * CM + q * 32, row = row0 + out.lane;
     const bool in = row < w.rows;
     const int target = in ? g.target[row] - x.v0 : -1;  // column within the piece
-    const float4 norm = in ? g.norm[row] : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < BN / 2 / 32; ++c) {
-        const int col0 = half * (BN / 2) + c * 32, p0 = x.n + col0;
-        float v[32];
-        __syncwarp();
-        tmem_ld32(acc + col0 + ((uint32_t)(q * 32) << 16), v);
+    const float2 norm = in ? g.norm[row] : make_float2(0.f, 0.f);
+    const int first = x.n + half * (BN / 2);
+    for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), 4, [&](int c, float (&v)[32]) {
+        const int p0 = first + c * 32;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            float p = ex2((v[i] - norm.x) * kLog2e) * norm.y;
-            if (p0 + i == target) p = norm.z;
-            v[i] = in && p0 + i < x.width ? p : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], kLog2e, -norm.x));
+        if ((unsigned)(target - p0) < 32u) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (p0 + i == target) v[i] = norm.y;
+        }
+        if (!in || p0 + 32 > x.width) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (!in || p0 + i >= x.width) v[i] = 0.f;
         }
         if ((c & 1) == 0) out.ready();
         out.put_bf16((c & 1) * 4, v);
         if (c & 1) out.send(&g.tm_p_st[x.piece], 0, (p0 / 64) * g.row_cap + row0, false);
-    }
+    });
 }
 
 __device__ __forceinline__ void epilogue_dh(const HeadGemm &g, const Walk &w, const Tile &x, uint32_t acc, int q,
                                             int half, const WayOut &out) {
-    const int row0 = x.m + x.rank * CM + q * 32;
-    for (int c = 0; c < BN / 2 / 32; ++c) {
-        const int col0 = half * (BN / 2) + c * 32;
-        if (x.n + col0 >= g.dim) break;
-        float v[32];
-        __syncwarp();
-        tmem_ld32(acc + col0 + ((uint32_t)(q * 32) << 16), v);
+    const int row0 = x.m + x.rank * CM + q * 32, first = x.n + half * (BN / 2);
+    for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), blocks_before(first, g.dim), [&](int c, float (&v)[32]) {
         if (x.kb == 0) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -306,8 +327,8 @@ __device__ __forceinline__ void epilogue_dh(const HeadGemm &g, const Walk &w, co
         out.ready();
         out.put_fp32(v);
         // one addend per value and launch: the order of the sum is the order of the launches
-        out.send(&g.tm_dh, x.n + col0, x.split * g.row_cap + row0, x.add != 0);
-    }
+        out.send(&g.tm_dh, first + c * 32, x.split * g.row_cap + row0, x.add != 0);
+    });
 }
 
 // dw through shared memory and a tensor copy where its rows are multiples of 16
@@ -317,12 +338,9 @@ __device__ __forceinline__ void epilogue_dw(const HeadGemm &g, const Tile &x, ui
                                             float factor, const WayOut &out) {
     const int local0 = x.m + x.rank * CM + q * 32, local = local0 + out.lane;
     const int64_t row = (int64_t)x.v0 + local;
-    for (int c = 0; c < BN / 2 / 32; ++c) {
-        const int col0 = half * (BN / 2) + c * 32, col = x.n + col0;
-        if (col >= g.dim || local0 >= x.width) break;
-        float v[32];
-        __syncwarp();
-        tmem_ld32(acc + col0 + ((uint32_t)(q * 32) << 16), v);
+    const int first = x.n + half * (BN / 2), blocks = local0 < x.width ? blocks_before(first, g.dim) : 0;
+    for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), blocks, [&](int c, float (&v)[32]) {
+        const int col = first + c * 32;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = x.kb == 0 ? 0.f : v[i] * factor;
         if (g.dw_tma && g.dw_bf16) {
@@ -348,7 +366,7 @@ __device__ __forceinline__ void epilogue_dw(const HeadGemm &g, const Tile &x, ui
                 }
             }
         }
-    }
+    });
 }
 
 // ---- the kernel ------------------------------------------------------------------------
@@ -383,6 +401,8 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
     cluster_sync();  // the other CTA's barriers exist and its TMEM is allocated
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    grid_dependency_launch();
+    grid_dependency_wait();  // up to here nothing of an earlier launch was touched
     const Walk walk = make_walk(g, blockIdx.x / 2, gridDim.x / 2);
     const int tiles = tile_count(walk);
 
@@ -487,8 +507,9 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
 int head_gemm(const HeadGemm &g, int max_tiles, const char *name, cudaStream_t st) {
     if (int rc = set_smem_limit(reinterpret_cast<const void *>(&head_gemm_kernel), SMEM_BYTES)) return rc;
     const int pairs = std::max(1, std::min(max_tiles, num_sms() / 2));
-    SPCO_LAUNCH(name, st, head_gemm_kernel<<<2 * pairs, THREADS, SMEM_BYTES, st>>>(g, device_flag_ptr()));
-    SPECOPTIM_LAUNCHED("head_gemm_kernel");
+    cudaError_t e = cudaSuccess;
+    SPCO_LAUNCH(name, st, e = launch_dependent(head_gemm_kernel, dim3(2 * pairs), dim3(THREADS), SMEM_BYTES, st, g, device_flag_ptr()));
+    SPECOPTIM_CUDA(e);
     return SPECOPTIM_OK;
 }
 

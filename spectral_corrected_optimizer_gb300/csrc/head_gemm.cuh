@@ -15,7 +15,7 @@ struct HeadState {
 };
 
 enum HeadJobKind : int {
-    HEAD_STATS = 0,  // logits tile -> each row's maximum and its sum of exponentials without the target's
+    HEAD_STATS = 0,  // logits tile -> each row's scale and sum of exponentials without the target's
     HEAD_PROB = 1,   // logits tile -> softmax - onehot, bf16, into a piece's buffer
     HEAD_DH = 2,     // dh partial sums (+)= piece . W
     HEAD_DW = 3,     // dw = factor * piece^T . H
@@ -46,8 +46,8 @@ struct HeadGemm {
     int row_cap;               // rows of the compact buffers (a multiple of the tile height)
     const HeadState *state;
     const int *target;         // [row_cap]
-    float2 *stats;             // [2 * ceil(vocab / 256)][row_cap]
-    const float4 *norm;        // [row_cap]: largest logit, 1 / sum, softmax - 1 at the target
+    float2 *stats;             // [2 * ceil(vocab / 256)][row_cap]: r and the part's sum relative to 2^r
+    const float2 *norm;        // [row_cap]: log2 of the sum of exponentials, softmax - 1 at the target
     void *dw;                  // [vocab][dim]
     int dw_bf16, dw_add;
     int dw_tma;                // dw is stored through tm_dw

@@ -25,7 +25,9 @@
 namespace spco {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+// log2(e) and what its fp32 value lacks
+constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = (float)(1.4426950408889634074 - (double)kLog2e);
+constexpr float kLn2 = 0.6931471805599453f;
 
 // ---- the rows that have a target ---------------------------------------------------------
 
@@ -67,6 +69,7 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
                                                         uint16_t *__restrict__ out, float *__restrict__ target_logit,
                                                         float *__restrict__ row_loss, unsigned *flag) {
     __shared__ int red[2][kRowWarps], own_token[kRowThreads], own_target[kRowThreads];
+    grid_dependency_launch();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int pad = (int)blockIdx.x - own_blocks;  // >= 0: a block of zero rows, which counts all targets
     const int t0 = pad >= 0 ? tokens : (int)blockIdx.x * share, t1 = min(t0 + share, tokens);
@@ -143,48 +146,52 @@ __global__ void __launch_bounds__(256) head_pad_kernel(const uint16_t *__restric
 
 // ---- joining the row statistics ------------------------------------------------------------
 
+// (m, s) <- (m, s) joined with a part: sums relative to 2^m, m whole numbers, so
+// the factors are exact powers of two
+__device__ __forceinline__ void join(float &m, float &s, float2 x) {
+    const float top = fmaxf(m, x.x), ref = top == -INFINITY ? 0.f : top;
+    s = s * exp2f(m - ref) + x.y * exp2f(x.x - ref);
+    m = top;
+}
+
 // 32 rows per block, 32 threads per row: each joins every 32nd part, then the
-// 32 are joined in order.  The parts' sums leave the target out: S of them
-// gives softmax - 1 = -S / (S + e_target) and the loss log(1 + S / e_target)
-// without the cancellation that a well-predicted token (S small) would meet in
-// 1 - p and in lse - l.  The last block to finish adds up the blocks' loss
-// sums, in block order.
+// 32 are joined in order.  The parts' sums leave the target out: S of them,
+// relative to 2^r, and e = 2^(target's logit in log2 - r) give softmax - 1 = -S /
+// (S + e) and the loss log(1 + S / e) without the cancellation that a
+// well-predicted token (S small) would meet in 1 - p and in lse - l.  The last
+// block to finish adds up the blocks' loss sums, in block order.
 __global__ void __launch_bounds__(1024) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
                                                        const float *__restrict__ target_logit,
                                                        const int *__restrict__ row_of, HeadState *state,
-                                                       float4 *__restrict__ norm, float *__restrict__ row_loss,
+                                                       float2 *__restrict__ norm, float *__restrict__ row_loss,
                                                        float *__restrict__ block_loss, float *__restrict__ loss) {
     __shared__ float sm[32][33], ss[32][33];
     __shared__ bool last;
+    grid_dependency_launch();
+    grid_dependency_wait();
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int rows = state->rows, row = blockIdx.x * 32 + c;
     float m = -INFINITY, s = 0.f;
     if (row < rows) {
 #pragma unroll 8
-        for (int p = w; p < parts; p += 32) {
-            const float2 x = stats[(int64_t)p * row_cap + row];
-            const float top = fmaxf(m, x.x), ref = top == -INFINITY ? 0.f : top;
-            s = s * exp2f((m - ref) * kLog2e) + x.y * exp2f((x.x - ref) * kLog2e);
-            m = top;
-        }
+        for (int p = w; p < parts; p += 32) join(m, s, stats[(int64_t)p * row_cap + row]);
     }
     sm[w][c] = m;
     ss[w][c] = s;
     __syncthreads();
     if (w == 0) {
 #pragma unroll 4
-        for (int i = 1; i < 32; ++i) {
-            const float top = fmaxf(m, sm[i][c]), ref = top == -INFINITY ? 0.f : top;
-            s = s * exp2f((m - ref) * kLog2e) + ss[i][c] * exp2f((sm[i][c] - ref) * kLog2e);
-            m = top;
-        }
+        for (int i = 1; i < 32; ++i) join(m, s, make_float2(sm[i][c], ss[i][c]));
         float l = 0.f;
         if (row < rows) {
-            const float lt = target_logit[row], above = m - lt;
-            const float total = s + expf(-above);
-            norm[row] = make_float4(m, 1.f / total, -s / total, 0.f);
-            // exp(20) S stays far from overflow; beyond it log(total) is no longer a small correction
-            l = above < 20.f ? log1pf(s * expf(above)) : above + logf(total);
+            // the target's logit in log2, to twice fp32's digits: hi + lo
+            const float lt = target_logit[row], hi = lt * kLog2e;
+            const float lo = fmaf(lt, kLog2e, -hi) + lt * kLog2eRest;
+            const float above = (m - hi) - lo;  // log2 of 2^r / e^target
+            const float total = s + exp2f(-above);
+            norm[row] = make_float2(m + log2f(total), -s / total);
+            // 2^30 S stays far from overflow; beyond it log(total) is no longer a small correction
+            l = above < 30.f ? log1pf(s * exp2f(above)) : (above + log2f(total)) * kLn2;
             row_loss[row_of[row]] = l;
         }
 #pragma unroll
@@ -211,6 +218,7 @@ template <bool VEC>
 __global__ void __launch_bounds__(256) head_dh_kernel(const Span<const float> sums, int parts, int row_cap, int ld,
                                                       const int *__restrict__ at, const HeadState *__restrict__ state,
                                                       float grad_scale, int tokens, int dim, const Span<bf16> dh) {
+    grid_dependency_wait();
     const float factor = grad_scale * state->inv_count;
     for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
         const int r = at[t];
@@ -268,7 +276,7 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
     p.off_at = take(cap * 4);
     p.off_target = take(cap * 4);
     p.off_tlogit = take(cap * 4);
-    p.off_norm = take(cap * 16);
+    p.off_norm = take(cap * 8);
     p.off_block_loss = take(ceil_div(cap, 32) * 4);
     p.off_stats = take((int64_t)p.parts * cap * 8);
     p.off_h = take(cap * round_up(dim, 64) * 2);
@@ -332,7 +340,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     int *row_of = reinterpret_cast<int *>(c.ws + p.off_row_of), *at = reinterpret_cast<int *>(c.ws + p.off_at);
     int *target = reinterpret_cast<int *>(c.ws + p.off_target);
     float *tlogit = reinterpret_cast<float *>(c.ws + p.off_tlogit);
-    float4 *norm = reinterpret_cast<float4 *>(c.ws + p.off_norm);
+    float2 *norm = reinterpret_cast<float2 *>(c.ws + p.off_norm);
     uint16_t *hc = reinterpret_cast<uint16_t *>(c.ws + p.off_h);
     const uint16_t *w = static_cast<const uint16_t *>(c.w);
     const int tokens = (int)c.tokens, vocab = (int)c.vocab;
@@ -375,11 +383,12 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     g->job[0] = HeadJob{HEAD_STATS, 0, 0, vocab, 1, 0};
     const int64_t tiles = (int64_t)(p.row_cap / kHeadTileM) * (p.parts / 2);
     if (int rc = head_gemm(*g, (int)std::min<int64_t>(tiles, INT32_MAX), "head_stats", c.st)) return rc;
+    cudaError_t e = cudaSuccess;
     SPCO_LAUNCH("head_lse", c.st,
-                head_lse_kernel<<<p.row_cap / 32, 1024, 0, c.st>>>(
-                    g->stats, p.parts, p.row_cap, tlogit, row_of, state, norm, c.row_loss,
-                    reinterpret_cast<float *>(c.ws + p.off_block_loss), c.loss));
-    SPECOPTIM_LAUNCHED("head_lse_kernel");
+                e = launch_dependent(head_lse_kernel, dim3(p.row_cap / 32), dim3(1024), 0, c.st, g->stats, p.parts,
+                                     p.row_cap, tlogit, row_of, state, norm, c.row_loss,
+                                     reinterpret_cast<float *>(c.ws + p.off_block_loss), c.loss));
+    SPECOPTIM_CUDA(e);
     return SPECOPTIM_OK;
 }
 
@@ -482,13 +491,14 @@ extern "C" int head_loss_grad(const void *h, const void *w, const void *targets,
             const int grid = (int)std::min<int64_t>(tokens, num_sms() * 16);
             const bool vec = dim % 8 == 0 && aligned16(dh);
             auto *k = vec ? &head_dh_kernel<true> : &head_dh_kernel<false>;
+            cudaError_t e = cudaSuccess;
             SPCO_LAUNCH("head_dh", c.st,
-                        k<<<grid, threads, 0, c.st>>>(Span<const float>(dh_sums, (int64_t)p.splits * p.row_cap * p.dh_ld),
-                                                      p.splits, p.row_cap, p.dh_ld,
-                                                      reinterpret_cast<const int *>(c.ws + p.off_at), g.state,
-                                                      grad_scale, (int)tokens, dim,
-                                                      Span<bf16>(static_cast<bf16 *>(dh), tokens * dim)));
-            SPECOPTIM_LAUNCHED("head_dh_kernel");
+                        e = launch_dependent(k, dim3(grid), dim3(threads), 0, c.st,
+                                             Span<const float>(dh_sums, (int64_t)p.splits * p.row_cap * p.dh_ld),
+                                             p.splits, p.row_cap, p.dh_ld, reinterpret_cast<const int *>(c.ws + p.off_at),
+                                             g.state, grad_scale, (int)tokens, dim,
+                                             Span<bf16>(static_cast<bf16 *>(dh), tokens * dim)));
+            SPECOPTIM_CUDA(e);
         }
         return SPECOPTIM_OK;
     });
