@@ -73,4 +73,4 @@ def head(h, w, target, ignore=-100, mean=True, grad_scale=1.0):
     d = torch.where(valid[:, None], d, torch.zeros_like(d))
     g = f * grad_scale
     return {"loss": row.sum() * f, "row_loss": row, "lse": lse, "dh": d @ w * g, "dw": d.T @ h * g, "d": d,
-            "factor": g, "valid": valid, "logit_mag": (h.abs() @ w.abs().T).amax(1)}
+            "factor": g, "loss_factor": f, "valid": valid, "logit_mag": (h.abs() @ w.abs().T).amax(1)}
