@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const ID *__res
                                                                  uint32_t *__restrict__ hist,
                                                                  uint32_t *__restrict__ next_hist,
                                                                  uint32_t *__restrict__ map, unsigned *flag) {
+    grid_dependency_launch();
     __shared__ uint32_t cnt[kBins];
     for (int b = threadIdx.x; b < kBins; b += kSortThreads) cnt[b] = 0;
     __syncthreads();
@@ -284,6 +285,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(
     const uint32_t *__restrict__ vals, int64_t n, int shift, const uint32_t *__restrict__ hist, int blocks,
     uint32_t *__restrict__ keys_out, uint32_t *__restrict__ vals_out, uint32_t *__restrict__ next_hist,
     uint32_t *__restrict__ clear_hist, const Fill fill, const uint32_t *__restrict__ map) {
+    // beside a fill the successor's blocks would wait in slots that the fill can use (+6 us on 65536 x 2048)
+    if ((int)gridDim.x == blocks) grid_dependency_launch();
+    grid_dependency_wait();
     if ((int)blockIdx.x >= blocks) {
         fill_by_map(fill, (int)blockIdx.x - blocks, map);
         return;
@@ -312,6 +316,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const ID *__re
                                                                   int64_t padding, int64_t n, int passes, uint32_t *k0,
                                                                   uint32_t *v0, uint32_t *k1, uint32_t *v1,
                                                                   const Fill fill, unsigned *flag) {
+    grid_dependency_launch();
     if (blockIdx.x > 0) {
         fill_by_ids(fill, (int)blockIdx.x - 1, ids, n, padding);
         return;
@@ -387,6 +392,8 @@ __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const 
                                                           const Span<TG> grad, float *__restrict__ partial, int pitch,
                                                           const Fill fill, const uint32_t *__restrict__ map) {
     __shared__ uint32_t sk[kMaxChunk + 2], sv[kMaxChunk];
+    if (s.chunks * col_blocks == (int64_t)gridDim.x) grid_dependency_launch();
+    grid_dependency_wait();
     const int tid = threadIdx.x;
     // sums and zero rows are spread evenly over the blocks, so that both are under way at any time
     const int64_t sums = s.chunks * col_blocks, block = (int64_t)blockIdx.x * sums / gridDim.x;
@@ -438,13 +445,16 @@ __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const 
 }
 
 // Blocks [0, chunks * col_blocks): if a run begins in the block's chunk and goes
-// on, its partial sums are added in chunk order and written to its row.  Blocks
-// after them: zero rows.
+// on, its partial sums are added in chunk order and written to its row.  Where
+// rows are narrow, groups of `threads` threads add up one stretch of chunks each
+// and their sums are added in order.  Blocks after them: zero rows.
 template <typename TG, bool VEC>
 __global__ void __launch_bounds__(256) segment_join_kernel(const Sorted s, int64_t vocab, int dim, int col_blocks,
+                                                           int threads,
                                                            float scale, bool accumulate, const Span<TG> grad,
                                                            const float *__restrict__ partial, int pitch,
                                                            const Fill fill, const uint32_t *__restrict__ map) {
+    grid_dependency_wait();
     const int64_t joins = s.chunks * col_blocks;
     if ((int64_t)blockIdx.x >= joins) {
         fill_by_map(fill, (int64_t)blockIdx.x - joins, map);
@@ -464,25 +474,39 @@ __global__ void __launch_bounds__(256) segment_join_kernel(const Sorted s, int64
         more += here;
         if (here < (int)blockDim.x) break;
     }
-    const int j = (int)((int64_t)blockIdx.x % col_blocks) * (int)blockDim.x + threadIdx.x;
-    if (j * 8 >= pitch) return;
-    float acc[8];
-    load8(partial + (c * 2 + 1) * pitch + j * 8, acc);
-    const float *part = partial + (c + 1) * 2 * pitch + j * 8;
+    const int groups = blockDim.x / threads, group = threadIdx.x / threads, at = threadIdx.x % threads;
+    const int j = (int)((int64_t)blockIdx.x % col_blocks) * threads + at;
+    const bool in = j * 8 < pitch;
+    // partial 0 is the chunk's own (its second slot), partial i the first slot of the chunk i behind it
+    const int64_t from = (more + 1) * group / groups, to = (more + 1) * (group + 1) / groups;
+    const float *first = partial + (c * 2 + 1) * pitch + j * 8, *rest = partial + (c * 2) * pitch + j * 8;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in) {
 #pragma unroll 16
-    for (int64_t i = 0; i < more; ++i) {
-        float x[8];
-        load8(part + i * 2 * pitch, x);
+        for (int64_t i = from; i < to; ++i) {
+            float x[8];
+            load8(i == 0 ? first : rest + i * 2 * pitch, x);
 #pragma unroll
-        for (int l = 0; l < 8; ++l) acc[l] += x[l];
+            for (int l = 0; l < 8; ++l) acc[l] += x[l];
+        }
     }
-    put_row<TG, VEC>(grad, k, dim, j, scale, accumulate, acc);
+    if (groups > 1) {
+        __shared__ float sums[8][256];  // [value][thread]
+#pragma unroll
+        for (int l = 0; l < 8; ++l) sums[l][threadIdx.x] = acc[l];
+        __syncthreads();
+        if (group > 0) return;
+        for (int g = 1; g < groups; ++g)
+#pragma unroll
+            for (int l = 0; l < 8; ++l) acc[l] += sums[l][g * threads + at];
+    }
+    if (in) put_row<TG, VEC>(grad, k, dim, j, scale, accumulate, acc);
 }
 
-// Tokens per chunk: as many blocks as fill the GPU four times over, between 8
+// Tokens per chunk: as many blocks as give every SM 1024 threads, between 8
 // tokens (a shorter chunk would leave more partial sums than it saves) and 64.
-int chunk_len(int64_t tokens, int col_blocks) {
-    const int64_t want = tokens * col_blocks / ((int64_t)num_sms() * 4);
+int chunk_len(int64_t tokens, int col_blocks, int threads) {
+    const int64_t want = tokens * col_blocks / ((int64_t)num_sms() * (1024 / threads));
     int len = 8;
     while (len < kMaxChunk && len < want) len *= 2;
     return len;
@@ -499,7 +523,7 @@ GradPlan plan_grad(int64_t tokens, int64_t vocab, int32_t dim, bool vec) {
     p.pitch = vec ? dim : (int)round_up(dim + 7, 8);  // with the start of the piece it begins in
     p.threads = (int)std::min<int64_t>(256, round_up(p.pitch / 8, 32));
     p.col_blocks = (int)ceil_div(p.pitch, (int64_t)p.threads * 8);
-    p.chunk = chunk_len(tokens, p.col_blocks);
+    p.chunk = chunk_len(tokens, p.col_blocks, p.threads);
     p.chunks = ceil_div(tokens, p.chunk);
     p.sort_blocks = ceil_div(tokens, kTile);
     int bits = 1;
@@ -552,15 +576,13 @@ int sort_tokens(const GradPlan &p, const ID *ids, int64_t tokens, int64_t vocab,
             const int64_t share = std::min(fill->left, fills / 8);
             const Fill f = fill->take(share);
             const unsigned grid = (unsigned)(blocks + share);
-            if (pass == 0)
-                SPCO_LAUNCH("embed_sort_scatter", st,
-                            sort_scatter_kernel<ID, true><<<grid, kSortThreads, 0, st>>>(
-                                ids, vocab, padding, nullptr, nullptr, tokens, 0, counts, blocks, k[to], v[to], next, clear, f, map));
-            else
-                SPCO_LAUNCH("embed_sort_scatter", st,
-                            sort_scatter_kernel<ID, false><<<grid, kSortThreads, 0, st>>>(
-                                nullptr, vocab, padding, k[from], v[from], tokens, pass * kBits, counts, blocks, k[to],
-                                v[to], next, clear, f, map));
+            auto *kernel = pass == 0 ? &sort_scatter_kernel<ID, true> : &sort_scatter_kernel<ID, false>;
+            cudaError_t e = cudaSuccess;
+            SPCO_LAUNCH("embed_sort_scatter", st,
+                        e = launch_dependent(kernel, dim3(grid), dim3(kSortThreads), 0, st, ids, vocab, padding, k[from],
+                                             v[from], tokens, pass * kBits, counts, blocks, k[to], v[to], next, clear, f,
+                                             map));
+            SPECOPTIM_CUDA(e);
         }
     }
     out->keys = k[last];
@@ -577,14 +599,18 @@ int sum_segments(const GradPlan &p, const Sorted &s, Filling fill, const void *d
     const int64_t sums = s.chunks * p.col_blocks;
     const int64_t beside = fill.left - fill.left / 2;  // the rest beside the joins
     const Fill f = fill.take(beside);
+    cudaError_t e = cudaSuccess;
     SPCO_LAUNCH("embed_segment_sum", st,
-                segment_sum_kernel<TD, TG, VEC><<<(unsigned)(sums + beside), p.threads, 0, st>>>(
-                    s, in, vocab, dim, p.col_blocks, scale, accumulate, out, partial, p.pitch, f, fill.map));
+                e = launch_dependent(segment_sum_kernel<TD, TG, VEC>, dim3((unsigned)(sums + beside)), dim3(p.threads), 0,
+                                     st, s, in, vocab, dim, p.col_blocks, scale, accumulate, out, partial, p.pitch, f,
+                                     fill.map));
+    SPECOPTIM_CUDA(e);
     if (s.chunks > 1 || fill.left > 0)
         SPCO_LAUNCH("embed_segment_join", st,
-                    segment_join_kernel<TG, VEC><<<(unsigned)(sums + fill.left), p.threads, 0, st>>>(
-                        s, vocab, dim, p.col_blocks, scale, accumulate, out, partial, p.pitch, fill.next, fill.map));
-    SPECOPTIM_LAUNCHED("embed_grad sums");
+                    e = launch_dependent(segment_join_kernel<TG, VEC>, dim3((unsigned)(sums + fill.left)),
+                                         dim3(256 / p.threads * p.threads), 0, st, s, vocab, dim, p.col_blocks, p.threads,
+                                         scale, accumulate, out, partial, p.pitch, fill.next, fill.map));
+    SPECOPTIM_CUDA(e);
     return SPECOPTIM_OK;
 }
 

@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) resnorm_backward
     const int ph = ROWS == ROWS_VEC ? 0 : (int)((a.dx.lo + (int64_t)blockIdx.x * dim) & 7);
     const int col0 = tid * 8 - ph, step = threads * 8, hl = tid & 15;
     const BlockSum block_sum{red, threads >> 5};
+    grid_dependency_launch();
     block_sum.init();
     float dg[NV][8], gm[RING ? NV : 1][8];
 #pragma unroll
@@ -593,6 +594,7 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) resnorm_backward
 __global__ void __launch_bounds__(1024) dgamma_kernel(const float *__restrict__ partial, int blocks, int dim,
                                                       int pitch, float *__restrict__ dgamma) {
     __shared__ float red[32][33];
+    grid_dependency_wait();
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
     float a = 0.f;
     if (col < dim) {
@@ -681,9 +683,11 @@ int run_backward(const Shape &sh, int rows, int blocks, const Backward<T> &a, fl
             if (int rc = set_smem_limit(reinterpret_cast<const void *>(k), smem)) return rc;
         SPCO_LAUNCH("resnorm_backward", st, k<<<blocks, sh.threads, smem, st>>>(a));
         SPECOPTIM_LAUNCHED("resnorm_backward_kernel");
+        cudaError_t e = cudaSuccess;
         SPCO_LAUNCH("resnorm_dgamma", st,
-                    dgamma_kernel<<<(unsigned)ceil_div(a.dim, 32), 1024, 0, st>>>(a.partial, blocks, a.dim, a.pitch, dgamma));
-        SPECOPTIM_LAUNCHED("dgamma_kernel");
+                    e = launch_dependent(dgamma_kernel, dim3((unsigned)ceil_div(a.dim, 32)), dim3(1024), 0, st, a.partial,
+                                         blocks, a.dim, a.pitch, dgamma));
+        SPECOPTIM_CUDA(e);
         return SPECOPTIM_OK;
     });
 }
