@@ -51,7 +51,7 @@ __device__ __forceinline__ float ex2(float x) {
 // One tile of a job: where its operands start and how far k runs.
 struct Tile {
     int kind, piece;
-    int m, n;        // first row (M) and column (N) of the tile
+    int m, n, bn;    // first row (M) and column (N) of the tile, its columns (256, or 128 at the end of dim)
     int k0, kb;      // first k, number of 64-k blocks
     int v0, width;   // vocabulary rows of the job's piece
     int split, add;
@@ -166,6 +166,7 @@ __device__ __forceinline__ Tile tile_at(const HeadGemm &g, const Walk &w, int i,
     x.split = 0;
     x.add = q.add;
     x.k0 = 0;
+    x.bn = BN;
     if (q.kind <= HEAD_PROB) {         // M = rows (fastest: a W tile is read from DRAM once), N = vocabulary, K = dim
         x.m = (t % w.m_tiles) * BM;
         x.n = (t / w.m_tiles) * BN;
@@ -186,6 +187,7 @@ __device__ __forceinline__ Tile tile_at(const HeadGemm &g, const Walk &w, int i,
         x.m = (t / w.d_tiles) * BM;
         x.kb = (w.rows + BK - 1) / BK;
     }
+    if (q.kind >= HEAD_DH && g.dim - x.n <= BN / 2) x.bn = BN / 2;
     return x;
 }
 
@@ -212,15 +214,45 @@ template <typename F> __device__ __forceinline__ void for_columns(uint32_t taddr
 // how many of a warp's four 32-column blocks begin in front of `end`
 __device__ __forceinline__ int blocks_before(int first, int end) { return min(4, max(0, (end - first + 31) / 32)); }
 
-// The part's sum is taken relative to 2^r, r the largest logit times log2(e)
-// rounded to a whole number: the exponent of each term is then one fused
-// multiply-add, and parts are joined by exact powers of two.
-__device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Walk &w, const Tile &x, uint32_t acc, int q,
-                                               int lane, int half) {
-    const int row = x.m + x.rank * CM + q * 32 + lane;
-    const int target = row < w.rows ? g.target[row] : -1;
-    const int first = x.n + half * (BN / 2);
-    float r = -INFINITY, s = 0.f;
+// What an epilogue needs of its row; loaded while the tile is still being formed.
+struct RowOf {
+    int row, target;
+    bool in;
+    float2 norm;  // HEAD_STATS: x the target's logit; HEAD_PROB: HeadGemm::norm
+};
+__device__ __forceinline__ RowOf row_of(const HeadGemm &g, const Walk &w, const Tile &x, int q, int lane) {
+    RowOf o;
+    o.row = x.m + x.rank * CM + q * 32 + lane;
+    o.in = x.kind <= HEAD_PROB && o.row < w.rows;
+    o.target = o.in ? g.target[o.row] : -1;
+    o.norm = make_float2(0.f, 0.f);
+    if (o.in) {
+        if (x.kind == HEAD_STATS) o.norm.x = g.target_logit[o.row];
+        else o.norm = g.norm[o.row];
+    }
+    return o;
+}
+
+// The part's sum is taken relative to 2^r, r a whole number: the exponent of each
+// term is then one fused multiply-add, and parts are joined by exact powers of
+// two.  r starts as the target's logit (in log2), which serves every row whose
+// other logits are less than 2^100 / 128 times as likely -- so no pass for the
+// maximum is needed; where a block of 32 terms reaches 2^100, r moves up to the
+// block's maximum.
+constexpr float kMuch = 1.2676506e30f;  // 2^100
+
+__device__ __forceinline__ float sum_exp2(const float (&v)[32], float r) {
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) part[i & 3] += ex2(fmaf(v[i], kLog2e, -r));
+    return (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+__device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Tile &x, const RowOf &of, uint32_t acc, int q,
+                                               int half) {
+    const int target = of.target, first = x.n + half * (BN / 2);
+    float r = rintf(of.norm.x * kLog2e), s = 0.f;
+    if (!(fabsf(r) < kMuch)) r = 0.f;  // not finite: the row's loss will say so
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), blocks_before(first, g.vocab), [&](int c, float (&v)[32]) {
         const int v0 = first + c * 32;
         if (v0 + 32 > g.vocab) {
@@ -228,27 +260,26 @@ __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Walk &w,
             for (int i = 0; i < 32; ++i)
                 if (v0 + i >= g.vocab) v[i] = -INFINITY;
         }
-        float top[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
-        const float most = rintf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e);
-        if (most > r) {
-            s *= ex2(r - most);
-            r = most;
-        }
         if ((unsigned)(target - v0) < 32u) {  // the target's own term is added when the parts are joined
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (v0 + i == target) v[i] = -INFINITY;
         }
-        // all -inf so far: any finite reference gives exp = 0 (and keeps a NaN visible)
-        const float ref = r == -INFINITY ? 0.f : r;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        float t = sum_exp2(v, r);
+        if (!(t < kMuch)) {
+            float top = v[0];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) part[i & 3] += ex2(fmaf(v[i], kLog2e, -ref));
-        s += (part[0] + part[1]) + (part[2] + part[3]);
+            for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
+            const float most = rintf(top * kLog2e);
+            if (most > r) {  // false where only NaN brought us here: it stays in the sum
+                s *= ex2(r - most);
+                r = most;
+                t = sum_exp2(v, r);
+            }
+        }
+        s += t;
     });
-    if (row < w.rows) g.stats[(int64_t)(x.n / (BN / 2) + half) * g.row_cap + row] = make_float2(r, s);
+    if (of.in) g.stats[(int64_t)(x.n / (BN / 2) + half) * g.row_cap + of.row] = make_float2(r, s);
 }
 
 // A warp's way out: 32 rows of 128 bytes (64 bf16 or 32 fp32 columns) are laid
@@ -289,12 +320,12 @@ struct WayOut {
     }
 };
 
-__device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Walk &w, const Tile &x, uint32_t acc, int q,
+__device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Tile &x, const RowOf &of, uint32_t acc, int q,
                                               int half, const WayOut &out) {
-    const int row0 = x.m + x.rank * CM + q * 32, row = row0 + out.lane;
-    const bool in = row < w.rows;
-    const int target = in ? g.target[row] - x.v0 : -1;  // column within the piece
-    const float2 norm = in ? g.norm[row] : make_float2(0.f, 0.f);
+    const int row0 = of.row - out.lane;
+    const bool in = of.in;
+    const int target = in ? of.target - x.v0 : -1;  // column within the piece
+    const float2 norm = of.norm;
     const int first = x.n + half * (BN / 2);
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), 4, [&](int c, float (&v)[32]) {
         const int p0 = first + c * 32;
@@ -316,7 +347,7 @@ __device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Walk &w, 
     });
 }
 
-__device__ __forceinline__ void epilogue_dh(const HeadGemm &g, const Walk &w, const Tile &x, uint32_t acc, int q,
+__device__ __forceinline__ void epilogue_dh(const HeadGemm &g, const Tile &x, uint32_t acc, int q,
                                             int half, const WayOut &out) {
     const int row0 = x.m + x.rank * CM + q * 32, first = x.n + half * (BN / 2);
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), blocks_before(first, g.dim), [&](int c, float (&v)[32]) {
@@ -414,26 +445,27 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
             const Tile x = tile_at(g, walk, t, rank);
             const CUtensorMap *ma = x.kind <= HEAD_PROB ? &g.tm_h_k : x.kind == HEAD_DH ? &g.tm_p_k[x.piece] : &g.tm_p[x.piece];
             const CUtensorMap *mb = x.kind <= HEAD_PROB ? &g.tm_w_k : x.kind == HEAD_DH ? &g.tm_w : &g.tm_h;
-            const int m = x.m + rank * CM, n = x.n + rank * CN;
+            const int m = x.m + rank * CM, n = x.n + rank * (x.bn / 2);
+            const uint32_t bytes = 2 * (A_BYTES + (uint32_t)x.bn / 2 * BK * 2);
             for (int kb = 0; kb < x.kb; ++kb, ++it) {
                 const int s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
-                if (!mbar_wait_cluster(&empty[s], ph ^ 1u, flag, 0x601u)) { ok = false; break; }
+                if (!mbar_wait_bounded(&empty[s], ph ^ 1u, flag, 0x601u)) { ok = false; break; }
                 unsigned char *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
                 const int k = x.k0 + kb * BK;
                 const uint32_t bar = cluster_addr(&full[s], 0);
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                 // k, m, n are multiples of 64: a column block of h and of the pieces
                 if (x.kind == HEAD_DW) {
                     tma_load_2d_pair(sa, ma, 0, m / 64 * g.row_cap + k, bar);
                     tma_load_2d_pair(sa + BOX_BYTES, ma, 0, (m / 64 + 1) * g.row_cap + k, bar);
                     tma_load_2d_pair(sb, mb, 0, n / 64 * g.row_cap + k, bar);
-                    tma_load_2d_pair(sb + BOX_BYTES, mb, 0, (n / 64 + 1) * g.row_cap + k, bar);
+                    if (x.bn == BN) tma_load_2d_pair(sb + BOX_BYTES, mb, 0, (n / 64 + 1) * g.row_cap + k, bar);
                 } else {
                     tma_load_2d_pair(sa, ma, 0, k / 64 * g.row_cap + m, bar);
                     if (x.kind == HEAD_DH) {
                         tma_load_2d_pair(sb, mb, n, x.v0 + k, bar);
-                        tma_load_2d_pair(sb + BOX_BYTES, mb, n + 64, x.v0 + k, bar);
+                        if (x.bn == BN) tma_load_2d_pair(sb + BOX_BYTES, mb, n + 64, x.v0 + k, bar);
                     } else {
                         tma_load_2d_pair(sb, mb, k, x.v0 + n, bar);
                     }
@@ -447,15 +479,15 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
         for (int t = 0; t < tiles && ok; ++t, ++local) {
             const Tile x = tile_at(g, walk, t, rank);
             const bool a_mn = x.kind == HEAD_DW, b_mn = x.kind >= HEAD_DH;
-            const uint32_t idesc = bf16_idesc(BM, BN, a_mn, b_mn);
+            const uint32_t idesc = bf16_idesc(BM, x.bn, a_mn, b_mn);
             const uint32_t acc = local & 1u, aph = (local >> 1) & 1u;
-            if (!mbar_wait_cluster(&tempty[acc], aph ^ 1u, flag, 0x602u)) break;
+            if (!mbar_wait_bounded(&tempty[acc], aph ^ 1u, flag, 0x602u)) break;
             tc_fence_after();
             const uint32_t d = tmem_base + acc * BN;
             for (int kb = 0; kb < x.kb; ++kb, ++it) {
                 const int s = it % STAGES;
                 const uint32_t ph = (it / STAGES) & 1u;
-                if (!mbar_wait_cluster(&full[s], ph, flag, 0x603u)) { ok = false; break; }
+                if (!mbar_wait_bounded(&full[s], ph, flag, 0x603u)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BYTES;
 #pragma unroll
@@ -478,13 +510,14 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
         uint32_t local = 0;
         for (int t = 0; t < tiles; ++t, ++local) {
             const Tile x = tile_at(g, walk, t, rank);
+            const RowOf of = row_of(g, walk, x, q, lane);
             const uint32_t a = local & 1u, aph = (local >> 1) & 1u;
-            if (!mbar_wait_cluster(&tfull[a], aph, flag, 0x604u)) break;
+            if (!mbar_wait_bounded(&tfull[a], aph, flag, 0x604u)) break;
             tc_fence_after();
             const uint32_t acc = tmem_base + a * BN;
-            if (x.kind == HEAD_STATS) epilogue_stats(g, walk, x, acc, q, lane, half);
-            else if (x.kind == HEAD_PROB) epilogue_prob(g, walk, x, acc, q, half, out);
-            else if (x.kind == HEAD_DH) epilogue_dh(g, walk, x, acc, q, half, out);
+            if (x.kind == HEAD_STATS) epilogue_stats(g, x, of, acc, q, half);
+            else if (x.kind == HEAD_PROB) epilogue_prob(g, x, of, acc, q, half, out);
+            else if (x.kind == HEAD_DH) epilogue_dh(g, x, acc, q, half, out);
             else epilogue_dw(g, x, acc, q, half, factor, out);
             tc_fence_before();
             __syncwarp();

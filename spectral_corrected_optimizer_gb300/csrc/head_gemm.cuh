@@ -46,6 +46,7 @@ struct HeadGemm {
     int row_cap;               // rows of the compact buffers (a multiple of the tile height)
     const HeadState *state;
     const int *target;         // [row_cap]
+    const float *target_logit; // [row_cap]
     float2 *stats;             // [2 * ceil(vocab / 256)][row_cap]: r and the part's sum relative to 2^r
     const float2 *norm;        // [row_cap]: log2 of the sum of exponentials, softmax - 1 at the target
     void *dw;                  // [vocab][dim]

@@ -377,6 +377,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     g->row_cap = p.row_cap;
     g->state = state;
     g->target = target;
+    g->target_logit = tlogit;
     g->stats = reinterpret_cast<float2 *>(c.ws + p.off_stats);
     g->norm = norm;
     g->jobs = 1;

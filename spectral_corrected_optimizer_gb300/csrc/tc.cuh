@@ -128,26 +128,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     return a;
 }
 
+// Arrival on a barrier of either CTA.  The release is of this CTA's scope: what is
+// handed over is TMEM, ordered by the tcgen05 fence in front; a release of the
+// cluster's scope would wait for the thread's global stores to be acknowledged.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-// bounded wait whose acquire covers the other CTA's arrivals
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, unsigned *flag, unsigned code) {
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if (i > 64) __nanosleep(32);
-    }
-    if (flag) atomicExch(flag, code);
-    return false;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // load into this CTA's shared memory, completion counted on a barrier of either CTA
