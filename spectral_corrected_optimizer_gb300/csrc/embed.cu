@@ -13,11 +13,37 @@
 // result does not depend on timing.  Rows without a token are zero-filled by
 // further blocks of the last launch.
 #include <algorithm>
+#include <mutex>
 #include <string>
 
 #include "rowvec.cuh"
 
 namespace spco {
+
+static __device__ unsigned g_stage_flag;
+
+unsigned *stage_flag_ptr() {
+    static unsigned *ptr = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_stage_flag) == cudaSuccess) ptr = static_cast<unsigned *>(p);
+    });
+    return ptr;
+}
+
+int check_stage_flag(cudaStream_t st) {
+    unsigned *p = stage_flag_ptr(), v = 0;
+    if (!p) return SPECOPTIM_OK;
+    SPECOPTIM_CUDA(cudaMemcpyAsync(&v, p, sizeof(v), cudaMemcpyDeviceToHost, st));
+    SPECOPTIM_CUDA(cudaStreamSynchronize(st));
+    if (!v) return SPECOPTIM_OK;
+    SPECOPTIM_CUDA(cudaMemsetAsync(p, 0, sizeof(v), st));
+    SPECOPTIM_CUDA(cudaStreamSynchronize(st));
+    return fail(SPECOPTIM_ERR_BOUNDS, v == kSiteTokenId ? "a token id lies outside the vocabulary"
+                                                        : "a target lies outside the vocabulary");
+}
+
 namespace {
 
 // ---- lookup ----------------------------------------------------------------------
@@ -80,7 +106,7 @@ void launch_lookup(const void *table, const void *ids, int64_t tokens, int64_t v
     const int grid = (int)(few ? tokens : std::min<int64_t>(ceil_div(tokens, 4), resident));
     auto *k = few ? (vec ? &lookup_kernel<TI, TO, ID, true, 1> : &lookup_kernel<TI, TO, ID, false, 1>)
                   : (vec ? &lookup_kernel<TI, TO, ID, true, 4> : &lookup_kernel<TI, TO, ID, false, 4>);
-    k<<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, device_flag_ptr());
+    k<<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, stage_flag_ptr());
 }
 
 template <typename TI, typename TO>
@@ -560,11 +586,11 @@ int sort_tokens(const GradPlan &p, const ID *ids, int64_t tokens, int64_t vocab,
         const Fill f = fill->take(share);
         SPCO_LAUNCH("embed_sort_small", st,
                     sort_small_kernel<ID><<<(unsigned)(1 + share), kSortThreads, 0, st>>>(
-                        ids, vocab, padding, tokens, p.passes, k[0], v[0], k[1], v[1], f, device_flag_ptr()));
+                        ids, vocab, padding, tokens, p.passes, k[0], v[0], k[1], v[1], f, stage_flag_ptr()));
     } else {
         SPECOPTIM_CUDA(cudaMemsetAsync(map, 0, (size_t)((vocab + 31) / 32 * 4), st));
         SPCO_LAUNCH("embed_sort_hist", st, sort_hist_kernel<ID><<<blocks, kSortThreads, 0, st>>>(
-                                               ids, vocab, padding, tokens, hist[0], hist[1], map, device_flag_ptr()));
+                                               ids, vocab, padding, tokens, hist[0], hist[1], map, stage_flag_ptr()));
         const int64_t fills = fill->left;
         for (int pass = 0; pass < p.passes; ++pass) {
             // three tables in turn: pass i reads table i, counts for pass i + 1

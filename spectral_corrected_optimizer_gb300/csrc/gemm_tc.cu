@@ -390,21 +390,6 @@ int make_tmap_2d_ex(CUtensorMap *map, const float *ptr, int64_t rows, int64_t co
     return SPECOPTIM_OK;
 }
 
-int make_tmap_2d_bf16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return fail(SPECOPTIM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {64, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        return fail(SPECOPTIM_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")");
-    return SPECOPTIM_OK;
-}
-
 int gemm_tc(int64_t M, int64_t N, int64_t K, Operand A, Operand B, const Epilogue &epi,
             cudaStream_t stream) {
     GemmProblem q{M, N, K, A, B, epi};

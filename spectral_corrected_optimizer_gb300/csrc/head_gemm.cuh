@@ -3,7 +3,7 @@
 #pragma once
 
 #include "rowvec.cuh"
-#include "tc.cuh"
+#include "tc_pair.cuh"
 
 namespace spco {
 

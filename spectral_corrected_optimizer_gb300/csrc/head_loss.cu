@@ -354,7 +354,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
                     head_rows_kernel<ID><<<blocks + (grad ? kPadBlocks : 0), kRowThreads, 0, c.st>>>(
                         static_cast<const ID *>(c.targets), c.ignore, tokens, vocab, c.mean, share, blocks,
                         static_cast<const uint16_t *>(c.h), w, c.dim, p.row_cap, h_vec, w_vec, state, row_of, at, target,
-                        hc, tlogit, c.row_loss, device_flag_ptr()));
+                        hc, tlogit, c.row_loss, stage_flag_ptr()));
     };
     if (c.id_bytes == 8) rows(int64_t{});
     else rows(int32_t{});

@@ -21,8 +21,10 @@ namespace spco {
 
 using bf16 = __nv_bfloat16;
 
-// bit 31 marks a failed index check; these sites are ids outside the vocabulary
-constexpr unsigned kSiteTokenId = 0x80000040u, kSiteTarget = 0x80000041u;
+// What a kernel writes to the stage-end operators' device flag when it skips an
+// id outside the vocabulary; check_stage_flag() (embed.cu) reads and clears it.
+constexpr unsigned kSiteTokenId = 1, kSiteTarget = 2;
+unsigned *stage_flag_ptr();
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }

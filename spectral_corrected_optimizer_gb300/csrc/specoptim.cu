@@ -83,10 +83,7 @@ int check_device_flag(cudaStream_t st) {
         unsigned zero = 0;
         cudaMemcpyAsync(p, &zero, sizeof(zero), cudaMemcpyHostToDevice, st);
         cudaStreamSynchronize(st);
-        if (v == 0x80000040u || v == 0x80000041u)  // stage_ends.h: the access was skipped
-            return fail(SPECOPTIM_ERR_BOUNDS, v == 0x80000040u ? "a token id lies outside the vocabulary"
-                                                               : "a target lies outside the vocabulary");
-        if (v & 0x80000000u)  // the other sites exist in the checked build (-DSPECOPTIM_CHECK) only
+        if (v & 0x80000000u)  // only the checked build (-DSPECOPTIM_CHECK) sets bit 31
             return fail(SPECOPTIM_ERR_BOUNDS, "an index check of the checked build failed (site " +
                                                   std::to_string(v & 0x7FFFFFFFu) + ")");
         return fail(SPECOPTIM_ERR_TIMEOUT, "a bounded device-side wait gave up (code " +

@@ -45,6 +45,8 @@ void recycle_all() {
 
 }  // namespace
 
+int check_stage_flag(cudaStream_t st);  // embed.cu
+
 int trace_begin(const char *name, cudaStream_t st) {
     g_launches.fetch_add(1, std::memory_order_relaxed);
     if (!g_enabled.load(std::memory_order_relaxed)) return -1;
@@ -141,7 +143,9 @@ extern "C" int specoptim_selftest_wait_timeout(uint32_t spin_limit, void *stream
 
 extern "C" int specoptim_check_device(void *stream) {
     clear_error();
-    return check_device_flag(static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (int rc = check_device_flag(st)) return rc;
+    return check_stage_flag(st);
 }
 
 extern "C" int specoptim_trace_enable(int32_t enable) {
