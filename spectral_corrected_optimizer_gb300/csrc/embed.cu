@@ -101,11 +101,16 @@ void launch_lookup(const void *table, const void *ids, int64_t tokens, int64_t v
     const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim + 7, 8), 32));
     const bool vec = dim % 8 == 0 && aligned16(table) && aligned16(out);
     const int64_t resident = (int64_t)num_sms() * 8;
-    // few tokens: one per block, so that every row has an SM of its own
+    // Few tokens: one per block, so that every row has an SM of its own.  Many: four at a
+    // time in a grid that stays (65536 x 2048: 82 us; one at a time 117), but rows that are
+    // not multiples of 16 bytes one at a time in many blocks (50000 x 1234: 47 us against
+    // 69 with four: their shifts take the registers).
     const bool few = tokens <= resident;
-    const int grid = (int)(few ? tokens : std::min<int64_t>(ceil_div(tokens, 4), resident));
+    const int grid = (int)(few   ? tokens
+                           : vec ? std::min<int64_t>(ceil_div(tokens, 4), resident)
+                                 : std::min<int64_t>(tokens, resident * 8));
     auto *k = few ? (vec ? &lookup_kernel<TI, TO, ID, true, 1> : &lookup_kernel<TI, TO, ID, false, 1>)
-                  : (vec ? &lookup_kernel<TI, TO, ID, true, 4> : &lookup_kernel<TI, TO, ID, false, 4>);
+                  : (vec ? &lookup_kernel<TI, TO, ID, true, 4> : &lookup_kernel<TI, TO, ID, false, 1>);
     k<<<grid, threads, 0, st>>>(tb, id, tokens, vocab, dim, scale, o, stage_flag_ptr());
 }
 
@@ -406,7 +411,7 @@ __device__ __forceinline__ void put_row(const Span<TG> &grad, int64_t row, int d
     else store_any(grad, at, from, from + dim, a);
 }
 
-constexpr int kMaxChunk = 64, kBatch = 8;
+constexpr int kMaxChunk = 64;
 
 // One chunk of the sorted list per block and column block, 8 columns per
 // thread.  partial: [chunks][2][pitch], slot 0 for a run that began before the
@@ -439,6 +444,7 @@ __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const 
     for (int i = tid; i < len; i += blockDim.x) sv[i] = s.vals[p0 + i];
     __syncthreads();
     if (j * 8 >= pitch) return;
+    constexpr int kBatch = VEC ? 8 : 4;  // rows in flight per thread; shifting odd rows into place takes registers
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     bool began = sk[0] != sk[1];  // whether the current run begins in this chunk
     for (int i0 = 0; i0 < len; i0 += kBatch) {
