@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
                                                         uint16_t *__restrict__ out, float *__restrict__ target_logit,
                                                         float *__restrict__ row_loss, unsigned *flag) {
     __shared__ int red[2][kRowWarps], own_token[kRowThreads], own_target[kRowThreads];
+    __shared__ float dots[kRowWarps];
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int pad = (int)blockIdx.x - own_blocks;  // >= 0: a block of zero rows, which counts all targets
@@ -115,6 +116,30 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
         state->blocks_done = 0;
         state->inv_count = mean ? 1.f / (float)max(rows, 1) : 1.f;
     }
+    // one token per block: its row is shared by all warps
+    if (share == 1 && pad < 0) {
+        if (count == 0) return;
+        const uint16_t *hr = h + (int64_t)own_token[0] * dim, *wr = w + (int64_t)own_target[0] * dim;
+        float s = 0.f;
+        for (int v = threadIdx.x; v < vecs; v += kRowThreads) {
+            uint4 a = make_uint4(0, 0, 0, 0);
+            if (v * 8 < dim) {
+                a = row_vec(hr, v, dim, h_vec);
+                const uint4 b = row_vec(wr, v, dim, w_vec);
+                s += dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, 0.f))));
+            }
+            reinterpret_cast<uint4 *>(out + ((int64_t)(v / 8) * row_cap + before) * 64)[v % 8] = a;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) dots[wp] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 1; i < kRowWarps; ++i) s += dots[i];
+            target_logit[before] = s;
+        }
+        return;
+    }
     for (int i = max(pad, 0) * kRowWarps + wp; i < copy; i += (pad >= 0 ? kPadBlocks : 1) * kRowWarps) {
         const int r = before + i;
         const uint16_t *hr = i < count ? h + (int64_t)own_token[i] * dim : nullptr;
@@ -154,10 +179,10 @@ __device__ __forceinline__ void join(float &m, float &s, float2 x) {
     m = top;
 }
 
-// 32 rows per block, 32 threads per row: each joins every 32nd part, then the
-// 32 are joined in order.  The parts' sums leave the target out: S of them,
-// relative to 2^r, and e = 2^(target's logit in log2 - r) give softmax - 1 = -S /
-// (S + e) and the loss log(1 + S / e) without the cancellation that a
+// 32 rows per block, 32 threads per row: each joins every 32nd part, then a warp
+// per row joins the 32 by halves.  The parts' sums leave the target out: S of
+// them, relative to 2^r, and e = 2^(target's logit in log2 - r) give softmax - 1 =
+// -S / (S + e) and the loss log(1 + S / e) without the cancellation that a
 // well-predicted token (S small) would meet in 1 - p and in lse - l.  The last
 // block to finish adds up the blocks' loss sums, in block order.
 __global__ void __launch_bounds__(1024) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
@@ -165,23 +190,27 @@ __global__ void __launch_bounds__(1024) head_lse_kernel(const float2 *__restrict
                                                        const int *__restrict__ row_of, HeadState *state,
                                                        float2 *__restrict__ norm, float *__restrict__ row_loss,
                                                        float *__restrict__ block_loss, float *__restrict__ loss) {
-    __shared__ float sm[32][33], ss[32][33];
+    __shared__ float sm[32][33], ss[32][33], row_sum[32];
     __shared__ bool last;
     grid_dependency_launch();
     grid_dependency_wait();
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int rows = state->rows, row = blockIdx.x * 32 + c;
+    const int rows = state->rows;
     float m = -INFINITY, s = 0.f;
-    if (row < rows) {
+    if (blockIdx.x * 32 + c < rows) {
 #pragma unroll 8
-        for (int p = w; p < parts; p += 32) join(m, s, stats[(int64_t)p * row_cap + row]);
+        for (int p = w; p < parts; p += 32) join(m, s, stats[(int64_t)p * row_cap + blockIdx.x * 32 + c]);
     }
     sm[w][c] = m;
     ss[w][c] = s;
     __syncthreads();
-    if (w == 0) {
-#pragma unroll 4
-        for (int i = 1; i < 32; ++i) join(m, s, make_float2(sm[i][c], ss[i][c]));
+    m = sm[c][w];  // from here on warp w has row w of the block, a lane each 32nd of its parts
+    s = ss[c][w];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        join(m, s, make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
+    if (c == 0) {
+        const int row = blockIdx.x * 32 + w;
         float l = 0.f;
         if (row < rows) {
             // the target's logit in log2, to twice fp32's digits: hi + lo
@@ -194,18 +223,22 @@ __global__ void __launch_bounds__(1024) head_lse_kernel(const float2 *__restrict
             l = above < 30.f ? log1pf(s * exp2f(above)) : (above + log2f(total)) * kLn2;
             row_loss[row_of[row]] = l;
         }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (c == 0) {
-            block_loss[blockIdx.x] = l;
-            __threadfence();
-            last = atomicAdd(&state->blocks_done, 1u) == gridDim.x - 1;
-        }
+        row_sum[w] = l;
     }
     __syncthreads();
-    if (!last || w != 0) return;
+    if (w != 0) return;
+    float l = row_sum[c];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (c == 0) {
+        block_loss[blockIdx.x] = l;
+        __threadfence();
+        last = atomicAdd(&state->blocks_done, 1u) == gridDim.x - 1;
+    }
+    __syncwarp();
+    if (!last) return;
     __threadfence();
-    float l = 0.f;
+    l = 0.f;
     for (int b = c; b < (int)gridDim.x; b += 32) l += __ldcg(block_loss + b);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
