@@ -9,7 +9,8 @@
  *
  * Conventions: device pointers, row-major tensors without gaps between rows,
  * aligned to their element size (16-byte aligned tensors whose rows are
- * multiples of 16 bytes take the vectorised paths).  Calls are asynchronous on
+ * multiples of 16 bytes take the vectorised paths); the head's w is 16-byte
+ * aligned.  Calls are asynchronous on
  * `stream` (a cudaStream_t as void*), return the status codes of specoptim.h
  * (message in specoptim_last_error()) and allocate nothing: where a call takes
  * a workspace, the caller provides at least the bytes its *_workspace function

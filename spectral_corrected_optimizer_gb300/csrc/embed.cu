@@ -11,7 +11,17 @@
 // its row, one that crosses chunks leaves fp32 partial sums that a last kernel
 // adds in chunk order.  So a frequent token costs as much as rare ones and the
 // result does not depend on timing.  Rows without a token are zero-filled by
-// further blocks of the last launch.
+// further blocks of the same launches.
+//
+// Measured on a GB300 (copy bandwidth 6.78 TB/s), 65536 tokens whose frequencies
+// fall off as 1 / rank, vocabulary 128256, width 2048:
+//   lookup, fp32 table to bf16: 84 us, 5.2 TB/s of the bytes that have to move (64 us
+//     at the copy's rate).  The rows are read 3.3 times over from L2, 537 MB beside
+//     432 MB of DRAM traffic.
+//   gradient, bf16 to dense fp32: 247 us, 5.3 TB/s (195 us at the copy's rate).  Sums
+//     and zero rows run at 5.9 to 6.2 TB/s; the ids' count (6 us), the sort's two
+//     passes (8 us each, a third covered by zero rows) and five launches are the rest.
+// Small calls are launch and latency bound: 777 tokens 23 us in three launches.
 #include <algorithm>
 #include <mutex>
 #include <string>

@@ -19,6 +19,17 @@
 // per M or N index), 64 rows high where they run along M or N (one row per k),
 // so none of the products needs a transposed copy.
 //
+// What bounds it: the power limit.  Measured on a GB300 (library bf16 product 1.88
+// PFLOP/s, 1.66 to 1.76 once the card is at its power limit), H 2048 x 2048, W 128256 x
+// 2048: statistics 572 us, 1.88 PFLOP/s, tensor pipe 85 % busy, before the limit, 610 us
+// at it; a launch of gradients (a piece's probabilities beside the piece before's two
+// products) keeps the tensor pipe 81 % busy.  Steps that led there, training step of
+// 8192 tokens: one CTA per 128 x 256 tile 15.0 ms; pairs 12.3; one 128-row box per
+// operand instead of two of 64 rows 10.35; tiles dealt out by load 10.2; column blocks,
+// epilogues through tensor copies 9.8; two slabs handed over at a time 9.4.
+// The epilogue of a logits tile takes 2.2 us whatever the width, so below a width of
+// about 400 it, not the tensor core, sets the pace (3974 x 112636 x 200: 212 us).
+//
 // Every wait on an mbarrier is bounded, as in gemm_tc.cu.
 #include <algorithm>
 #include <cstring>

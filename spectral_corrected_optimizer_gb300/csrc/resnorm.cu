@@ -20,6 +20,14 @@
 // that its last ph values are the first ph of the next 16 threads' first piece:
 // those two maxima meet in shared memory.
 //
+// Measured on a GB300 (copy bandwidth 6.78 TB/s), bf16 [65536][2048] with a residual:
+//   forward 183 us, 6.63 TB/s of x, r, s, y and the checkpoint (1.21 GB): 98 % of a copy;
+//   backward with y 216 us, 5.6 TB/s (83 %): issue slots 55 % busy, 32 warps an SM; a
+//     row's chain of shuffles, barrier and stores is what is waited for.  Two rows at a
+//     time (112 registers, half the warps) took 231 us, registers instead of the ring 249.
+// Odd rows cost more instructions than bytes (440 per 256 values against 240): norm of
+// 9749 x 6030 109 us (44 at the copy's rate), backward of 30001 x 3001 271 us (120).
+//
 // The norm statistics and every sum are fp32.  The checkpoint is the only
 // tensor below 16 bits: e4m3 with a scale per 128 values keeps each value to
 // 2^-4 of itself, or 2^-10 of the group's scale where that is more.

@@ -242,7 +242,7 @@ def _head_args(h, w, targets, reduction):
 def head_loss(h, w, targets, ignore_index: int = -100, reduction: str = "mean", stream=None):
     """(loss, row_loss): softmax cross entropy of h @ w.T against targets, without the logits in memory.
 
-    h: [tokens, dim] bf16, w: [vocab, dim] bf16, targets: [tokens] int32 or int64.
+    h: [tokens, dim] bf16, w: [vocab, dim] bf16 (16-byte aligned), targets: [tokens] int32 or int64.
     Tokens with target ignore_index have row_loss 0 and do not count in the mean."""
     if stream is not None:
         return _on(stream, head_loss, h, w, targets, ignore_index=ignore_index, reduction=reduction)
