@@ -78,18 +78,24 @@ struct Tile {
 // tile of dw runs over all rows, one of dh over the whole piece): they come
 // first and are dealt out in turn.  The logits tiles are many and short; each
 // pair takes as many as bring its load up to the others' (a load is counted in
-// 64-k blocks and a tile's own cost as two of them).  Alone (HEAD_STATS) they
-// are dealt out in turn too, so that neighbouring pairs share W's rows in L2.
+// 64-k blocks and a tile's own cost as two of them).  With few rows dw's tiles are
+// short too, less than half of one of dh, and are dealt out by load in front of
+// the logits tiles.  Alone (HEAD_STATS) the logits tiles are dealt out in turn
+// too, so that neighbouring pairs share W's rows in L2.
 struct Walk {
     int rows, m_tiles, d_tiles;
-    int long_tiles, dw_tiles, dh_tiles;  // of the jobs HEAD_DW and HEAD_DH
-    int first_short, shorts, longs;      // this pair's logits tiles and long tiles
+    int long_dw, longs;                  // dw tiles dealt out in turn (in front of dh's); this pair's tiles in turn
+    int line_dw, first_short, shorts;    // dw tiles dealt out by load; this pair's tiles of those and the logits
     int pair, pairs;
     int dw_job, dh_job, short_job;       // -1: none
     bool in_turn;
 };
 
+// In 64-k blocks (0.35 us): what a tile costs beside its own, and what a tile of
+// dw costs at least, its 256 KB (fp32) being written (one token over 128256 x 2048:
+// 428 us with 4, 445 with 3; 333 over 50001 x 1000: 126 with 4, 129 with 6).
 constexpr int kTileCost = 2;
+constexpr int kDwCostFp32 = 4, kDwCostBf16 = 3;
 
 __device__ __forceinline__ Walk make_walk(const HeadGemm &g, int pair, int pairs) {
     Walk w;
@@ -99,8 +105,7 @@ __device__ __forceinline__ Walk make_walk(const HeadGemm &g, int pair, int pairs
     w.m_tiles = (w.rows + BM - 1) / BM;
     w.d_tiles = (g.dim + BN - 1) / BN;
     w.dw_job = w.dh_job = w.short_job = -1;
-    w.dw_tiles = w.dh_tiles = 0;
-    int n_short = 0, dw_cost = 0, dh_cost = 0;
+    int n_short = 0, dw_tiles = 0, dh_tiles = 0, dw_cost = 1, dh_cost = 0;
 #pragma unroll
     for (int j = 0; j < kHeadJobs; ++j) {
         if (j >= g.jobs) break;
@@ -110,48 +115,54 @@ __device__ __forceinline__ Walk make_walk(const HeadGemm &g, int pair, int pairs
             n_short = w.m_tiles * ((q.width + BN - 1) / BN);
         } else if (q.kind == HEAD_DH) {
             w.dh_job = j;
-            w.dh_tiles = w.m_tiles * w.d_tiles * q.splits;
+            dh_tiles = w.m_tiles * w.d_tiles * q.splits;
             dh_cost = (q.width + BK - 1) / BK / q.splits + kTileCost;
         } else {
             w.dw_job = j;
-            w.dw_tiles = ((q.width + BM - 1) / BM) * w.d_tiles;
-            dw_cost = (w.rows + BK - 1) / BK + kTileCost;
+            dw_tiles = ((q.width + BM - 1) / BM) * w.d_tiles;
+            dw_cost = max((w.rows + BK - 1) / BK, g.dw_bf16 ? kDwCostBf16 : kDwCostFp32) + kTileCost;
         }
     }
-    w.long_tiles = w.dw_tiles + w.dh_tiles;
-    w.longs = pair < w.long_tiles ? (w.long_tiles - pair + pairs - 1) / pairs : 0;
-    w.in_turn = w.long_tiles == 0;
+    w.line_dw = 2 * dw_cost < dh_cost ? dw_tiles : 0;
+    w.long_dw = dw_tiles - w.line_dw;
+    const int long_tiles = w.long_dw + dh_tiles, line = w.line_dw + n_short;
+    w.longs = pair < long_tiles ? (long_tiles - pair + pairs - 1) / pairs : 0;
+    w.in_turn = long_tiles == 0;
     w.first_short = pair;
-    w.shorts = pair < n_short ? (n_short - pair + pairs - 1) / pairs : 0;
+    w.shorts = pair < line ? (line - pair + pairs - 1) / pairs : 0;
     if (!w.in_turn) {
         // pairs below r1 have one dw tile more, pairs below r2 one long tile more:
         // three runs of pairs with equal loads
-        const int r1 = w.dw_tiles % pairs, r2 = w.long_tiles % pairs;
+        const int r1 = w.long_dw % pairs, r2 = long_tiles % pairs;
         const int cost = (g.dim + BK - 1) / BK + kTileCost;
-        const int64_t total = (int64_t)w.dw_tiles * dw_cost + (int64_t)w.dh_tiles * dh_cost + (int64_t)n_short * cost;
+        const int64_t line_dw_cost = (int64_t)w.line_dw * dw_cost, line_cost = line_dw_cost + (int64_t)n_short * cost;
+        const int64_t total = (int64_t)w.long_dw * dw_cost + (int64_t)dh_tiles * dh_cost + line_cost;
         const int edge[4] = {0, min(r1, r2), max(r1, r2), pairs};
         int64_t share[3], all = 0;  // `pairs` times what a pair of the run lacks to the mean load
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const int n_dw = w.dw_tiles / pairs + (edge[k] < r1), n_long = w.long_tiles / pairs + (edge[k] < r2);
+            const int n_dw = w.long_dw / pairs + (edge[k] < r1), n_long = long_tiles / pairs + (edge[k] < r2);
             const int64_t load = (int64_t)n_dw * dw_cost + (int64_t)(n_long - n_dw) * dh_cost;
             share[k] = max((int64_t)0, total - load * pairs);
             all += share[k] * (edge[k + 1] - edge[k]);
         }
         // integers throughout: a pair's last tile and the next one's first come from the same quotient
-        const int shift = max(0, 24 - __clzll(all));  // all < 2^40, n_short < 2^23
+        const int shift = max(0, 33 - __clzll(all));  // sum < 2^31; line_cost < 2^31 as rows x width of a piece is bounded
         int64_t sum = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             share[k] >>= shift;
             sum += share[k] * (edge[k + 1] - edge[k]);
         }
+        // the first tile of the line (dw's, then the logits) that begins in or behind pair p's part of it
         auto first_of = [&](int p) -> int {
-            if (p >= pairs || sum == 0) return p >= pairs ? n_short : 0;
+            if (p >= pairs || sum == 0) return p >= pairs ? line : 0;
             int64_t before = 0;
 #pragma unroll
             for (int k = 0; k < 3; ++k) before += share[k] * (max(edge[k], min(edge[k + 1], p)) - edge[k]);
-            return (int)(before * n_short / sum);
+            const int64_t at = before * line_cost / sum;
+            return at <= line_dw_cost ? (int)((at + dw_cost - 1) / dw_cost)
+                                      : w.line_dw + (int)((at - line_dw_cost + cost - 1) / cost);
         };
         w.first_short = first_of(pair);
         w.shorts = first_of(pair + 1) - w.first_short;
@@ -166,11 +177,12 @@ __device__ __forceinline__ Tile tile_at(const HeadGemm &g, const Walk &w, int i,
     int t, j;
     if (i < w.longs) {
         t = w.pair + i * w.pairs;
-        j = t < w.dw_tiles ? w.dw_job : w.dh_job;
-        if (t >= w.dw_tiles) t -= w.dw_tiles;
+        j = t < w.long_dw ? w.dw_job : w.dh_job;
+        if (t >= w.long_dw) t -= w.long_dw;
     } else {
         t = w.first_short + (i - w.longs) * (w.in_turn ? w.pairs : 1);
-        j = w.short_job;
+        j = t < w.line_dw ? w.dw_job : w.short_job;
+        if (t >= w.line_dw) t -= w.line_dw;
     }
     const HeadJob &q = g.job[j];
     Tile x;

@@ -186,70 +186,84 @@ __device__ __forceinline__ void join(float &m, float &s, float2 x) {
     m = top;
 }
 
-// 32 rows per block, 32 threads per row: each joins every 32nd part, then a warp
-// per row joins the 32 by halves.  The parts' sums leave the target out: S of
-// them, relative to 2^r, and e = 2^(target's logit in log2 - r) give softmax - 1 =
-// -S / (S + e) and the loss log(1 + S / e) without the cancellation that a
-// well-predicted token (S small) would meet in 1 - p and in lse - l.  The last
-// block to finish adds up the blocks' loss sums, in block order.
-__global__ void __launch_bounds__(1024) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
+// ROWS rows per block, LANES threads per row: each joins every LANES-th part, then
+// a warp per row joins what its threads hold by halves.  The parts' sums
+// leave the target out: S of them, relative to 2^r, and e = 2^(target's logit in
+// log2 - r) give softmax - 1 = -S / (S + e) and the loss log(1 + S / e) without
+// the cancellation that a well-predicted token (S small) would meet in 1 - p and
+// in lse - l.  The last block to finish adds up the blocks' loss sums, in block
+// order.
+// Bound by the latency of a thread's reads while the blocks fit on the SMs at once:
+// 8 rows per block then, 126 us for 333 tokens over 50001 x 1000 where 32 take 129;
+// by the width of the reads when they do not: 32 rows then, 26 us for 8192 tokens
+// and 1002 parts where 8 take 49.
+constexpr int kLseThreads = 1024, kLseFew = 8, kLseMany = 32;
+template <int ROWS>
+__global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
                                                        const float *__restrict__ target_logit,
                                                        const int *__restrict__ row_of, HeadState *state,
                                                        float2 *__restrict__ norm, float *__restrict__ row_loss,
                                                        float *__restrict__ block_loss, float *__restrict__ loss) {
-    __shared__ float sm[32][33], ss[32][33], row_sum[32];
-    __shared__ bool last;
+    constexpr int LANES = kLseThreads / ROWS;
+    __shared__ float sm[LANES][ROWS + 1], ss[LANES][ROWS + 1], row_sum[ROWS];
     grid_dependency_launch();
     grid_dependency_wait();
-    const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int rows = state->rows;
+    const int rows = state->rows, row0 = blockIdx.x * ROWS, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float m = -INFINITY, s = 0.f;
-    if (blockIdx.x * 32 + c < rows) {
+    {
+        const int c = threadIdx.x % ROWS, first = threadIdx.x / ROWS;
+        if (row0 + c < rows) {
 #pragma unroll 8
-        for (int p = w; p < parts; p += 32) join(m, s, stats[(int64_t)p * row_cap + blockIdx.x * 32 + c]);
-    }
-    sm[w][c] = m;
-    ss[w][c] = s;
-    __syncthreads();
-    m = sm[c][w];  // from here on warp w has row w of the block, a lane each 32nd of its parts
-    s = ss[c][w];
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        join(m, s, make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
-    if (c == 0) {
-        const int row = blockIdx.x * 32 + w;
-        float l = 0.f;
-        if (row < rows) {
-            // the target's logit in log2, to twice fp32's digits: hi + lo
-            const float lt = target_logit[row], hi = lt * kLog2e;
-            const float lo = fmaf(lt, kLog2e, -hi) + lt * kLog2eRest;
-            const float above = (m - hi) - lo;  // log2 of 2^r / e^target
-            const float total = s + exp2f(-above);
-            norm[row] = make_float2(m + log2f(total), -s / total);
-            // 2^30 S stays far from overflow; beyond it log(total) is no longer a small correction
-            l = above < 30.f ? log1pf(s * exp2f(above)) : (above + log2f(total)) * kLn2;
-            row_loss[row_of[row]] = l;
+            for (int p = first; p < parts; p += LANES) join(m, s, stats[(int64_t)p * row_cap + row0 + c]);
         }
-        row_sum[w] = l;
+        sm[first][c] = m;
+        ss[first][c] = s;
+    }
+    __syncthreads();
+    if (w < ROWS) {  // warp w has row w of the block
+        m = sm[lane][w];
+        s = ss[lane][w];
+#pragma unroll
+        for (int i = 32; i < LANES; i += 32) join(m, s, make_float2(sm[i + lane][w], ss[i + lane][w]));
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            join(m, s, make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
+        if (lane == 0) {
+            const int row = row0 + w;
+            float l = 0.f;
+            if (row < rows) {
+                // the target's logit in log2, to twice fp32's digits: hi + lo
+                const float lt = target_logit[row], hi = lt * kLog2e;
+                const float lo = fmaf(lt, kLog2e, -hi) + lt * kLog2eRest;
+                const float above = (m - hi) - lo;  // log2 of 2^r / e^target
+                const float total = s + exp2f(-above);
+                norm[row] = make_float2(m + log2f(total), -s / total);
+                // 2^30 S stays far from overflow; beyond it log(total) is no longer a small correction
+                l = above < 30.f ? log1pf(s * exp2f(above)) : (above + log2f(total)) * kLn2;
+                row_loss[row_of[row]] = l;
+            }
+            row_sum[w] = l;
+        }
     }
     __syncthreads();
     if (w != 0) return;
-    float l = row_sum[c];
+    float l = lane < ROWS ? row_sum[lane] : 0.f;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (c == 0) {
+    int last = 0;
+    if (lane == 0) {
         block_loss[blockIdx.x] = l;
         __threadfence();
         last = atomicAdd(&state->blocks_done, 1u) == gridDim.x - 1;
     }
-    __syncwarp();
-    if (!last) return;
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
     __threadfence();
     l = 0.f;
-    for (int b = c; b < (int)gridDim.x; b += 32) l += __ldcg(block_loss + b);
+#pragma unroll 8
+    for (int b = lane; b < (int)gridDim.x; b += 32) l += __ldcg(block_loss + b);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (c == 0) *loss = l * state->inv_count;
+    if (lane == 0) *loss = l * state->inv_count;
 }
 
 // dh[t] = factor * sum over the parts of the token's row; zero without a target.
@@ -317,7 +331,7 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
     p.off_target = take(cap * 4);
     p.off_tlogit = take(cap * 4);
     p.off_norm = take(cap * 8);
-    p.off_block_loss = take(ceil_div(cap, 32) * 4);
+    p.off_block_loss = take(ceil_div(cap, kLseFew) * 4);
     p.off_stats = take((int64_t)p.parts * cap * 8);
     p.off_h = take(cap * round_up(dim, 64) * 2);
     p.off_w = p.ld != dim ? take(vocab * p.ld * 2) : 0;
@@ -425,8 +439,10 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     const int64_t tiles = (int64_t)(p.row_cap / kHeadTileM) * (p.parts / 2);
     if (int rc = head_gemm(*g, (int)std::min<int64_t>(tiles, INT32_MAX), "head_stats", c.st)) return rc;
     cudaError_t e = cudaSuccess;
+    const int lse_rows = p.row_cap / kLseFew <= 2 * num_sms() ? kLseFew : kLseMany;  // two blocks an SM
+    auto *lse = lse_rows == kLseFew ? &head_lse_kernel<kLseFew> : &head_lse_kernel<kLseMany>;
     SPCO_LAUNCH("head_lse", c.st,
-                e = launch_dependent(head_lse_kernel, dim3(p.row_cap / 32), dim3(1024), 0, c.st, g->stats, p.parts,
+                e = launch_dependent(lse, dim3(p.row_cap / lse_rows), dim3(kLseThreads), 0, c.st, g->stats, p.parts,
                                      p.row_cap, tlogit, row_of, state, norm, c.row_loss,
                                      reinterpret_cast<float *>(c.ws + p.off_block_loss), c.loss));
     SPECOPTIM_CUDA(e);
