@@ -269,10 +269,10 @@ __device__ __forceinline__ RowOf row_of(const HeadGemm &g, const Walk &w, const 
 // block's maximum.
 constexpr float kMuch = 1.2676506e30f;  // 2^100
 
-__device__ __forceinline__ float sum_exp2(const float (&v)[32], float r) {
+__device__ __forceinline__ float sum_exp2(const float (&v)[32], float log2e, float r) {
     float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) part[i & 3] += ex2(fmaf(v[i], kLog2e, -r));
+    for (int i = 0; i < 32; ++i) part[i & 3] += ex2(fmaf(v[i], log2e, -r));
     return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
@@ -293,16 +293,16 @@ __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Tile &x,
             for (int i = 0; i < 32; ++i)
                 if (v0 + i == target) v[i] = -INFINITY;
         }
-        float t = sum_exp2(v, r);
+        float t = sum_exp2(v, g.log2e, r);
         if (!(t < kMuch)) {
             float top = v[0];
 #pragma unroll
             for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-            const float most = rintf(top * kLog2e);
+            const float most = rintf(top * g.log2e);
             if (most > r) {  // false where only NaN brought us here: it stays in the sum
                 s *= ex2(r - most);
                 r = most;
-                t = sum_exp2(v, r);
+                t = sum_exp2(v, g.log2e, r);
             }
         }
         s += t;
@@ -358,7 +358,7 @@ __device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Tile &x, 
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), 4, [&](int c, float (&v)[32]) {
         const int p0 = first + c * 32;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], kLog2e, -norm.x));
+        for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], g.log2e, -norm.x));
         if ((unsigned)(target - p0) < 32u) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)

@@ -53,6 +53,7 @@ struct HeadGemm {
     int dw_bf16, dw_add;
     int dw_tma;                // dw is stored through tm_dw
     float grad_scale;
+    float log2e;               // times a tensor-core logit: the logit in log2 (see head_log2e)
 };
 
 constexpr int kHeadTileM = 256, kHeadTileN = 256;
