@@ -704,7 +704,9 @@ extern "C" int64_t embed_grad_workspace(int64_t tokens, int64_t vocab, int32_t d
     int64_t bytes = -1;
     entry([&]() -> int {
         if (int rc = check_sizes(tokens, vocab, dim, "embed_grad")) return rc;
-        bytes = plan_grad(tokens, vocab, dim, false).bytes;  // the larger one: alignment is not known yet
+        // Alignment is not known yet.  Neither plan is always the larger one: unaligned rows are wider, which
+        // may make a second column block and with it longer chunks, so fewer partial sums.
+        bytes = std::max(plan_grad(tokens, vocab, dim, true).bytes, plan_grad(tokens, vocab, dim, false).bytes);
         return SPECOPTIM_OK;
     });
     return bytes;

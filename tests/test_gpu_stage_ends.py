@@ -134,6 +134,16 @@ def test_embed_grad_adds_to_a_gradient_and_leaves_other_rows(dim, dout):
     assert bool(absent.any()) and torch.equal(got.cpu()[absent], before[absent])
 
 
+@pytest.mark.parametrize("dim", [8, 248, 256, 1024, 2040, 2048, 4096])
+@pytest.mark.parametrize("tokens", [700, 2600, 8192, 20000])
+def test_embed_grad_workspace_serves_every_alignment(tokens, dim):
+    # the chunks, and with them the partial sums, differ between aligned and unaligned rows
+    g = gen(tokens + dim)
+    ids, dy = zipf(g, tokens, 40), randn(g, (tokens, dim), BF)
+    for given in (dy.cuda(), shifted(dy, 3)):
+        check_grad(se().embed_grad(ids.cuda(), given, 40), ids, dy, 40, 1.0)
+
+
 @pytest.mark.parametrize("ids", [[4] * 700, list(range(600)), [0, 599] * 300, [599] * 3 + [0] * 200 + [300] * 500])
 def test_embed_grad_of_extreme_orders(ids):
     ids = torch.tensor(ids)
