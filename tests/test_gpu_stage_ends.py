@@ -536,3 +536,58 @@ def test_operators_run_on_another_stream():
     got_grad = se().embed_grad(ids, dy, 500, stream=st)
     st.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(base, got)) and torch.equal(grad, got_grad)
+
+
+# ---------------------------------------------------------------- offsets beyond 32 bits
+
+FAR = (600_000, 4096)  # 2.46e9 values
+
+
+def test_embedding_offsets_beyond_32_bits():
+    vocab, dim = FAR
+    g = gen(12)
+    ids = torch.tensor([vocab - 1, 0, vocab - 3, 17]).cuda()
+    dy = randn(g, (4, dim), BF).cuda()
+    grad = se().embed_grad(ids, dy, vocab, dtype=BF)
+    assert torch.equal(grad[ids], dy)
+    assert not bool(grad[18:-3].any()) and not bool(grad[-2].any()) and not bool(grad[1:17].any())
+    assert torch.equal(se().embed_lookup(grad, ids), dy)
+
+
+def test_norm_offsets_beyond_32_bits():
+    rows, dim = FAR
+    x = torch.randn(rows, dim, device="cuda", dtype=BF)
+    gamma = randn(gen(13), (dim,), BF).cuda()
+    kept, s, y = se().residual_norm(x, None, gamma)
+    dx, _, again = se().residual_norm_backward(x, kept, gamma, recompute=True)
+    # rows do not depend on one another
+    tail = slice(rows - 16, rows)
+    kept_t, _, y_t = se().residual_norm(x[tail].clone(), None, gamma)
+    dx_t, _, again_t = se().residual_norm_backward(x[tail].clone(), kept_t, gamma, recompute=True)
+    for a, b in ((y, y_t), (kept.q.view(torch.uint8), kept_t.q.view(torch.uint8)), (kept.scale, kept_t.scale),
+                 (kept.rstd, kept_t.rstd), (dx, dx_t), (again, again_t)):
+        assert torch.equal(a[tail], b)
+
+
+def test_head_offsets_beyond_32_bits():
+    vocab, dim = FAR
+    g = gen(14)
+    w = torch.zeros(vocab, dim, dtype=BF, device="cuda")
+    w[-3:] = (0.05 * randn(g, (3, dim))).to(BF).cuda()
+    h = randn(g, (3, dim), BF).cuda()
+    target = torch.tensor([vocab - 1, vocab - 2, 5])
+    loss, row_loss, dh, dw = se().head_loss_grad(h, w, target.cuda(), dtype=BF)
+    h64, l = h.double().cpu(), h.double().cpu() @ w[-3:].double().cpu().T
+    lse = torch.log(vocab - 3 + l.exp().sum(1))
+    want = lse - torch.tensor([l[0, 2], l[1, 1], 0.0], dtype=torch.float64)
+    # logits: dim / 16 sums, each cut off by up to 2 u32 of it; the exponentials' sum: fewer than 200 roundings
+    off = dim / 16 * 2 * U32 * float(l.abs().max())
+    assert bool(((row_loss.cpu().double() - want).abs() <= off + 200 * U32 + 4 * U32 * want.abs()).all())
+    d = (l - lse[:, None]).exp()
+    d[0, 2] -= 1
+    d[1, 1] -= 1
+    got, want_dw, mag = dw[-3:].double().cpu(), d.T @ h64 / 3, d.abs().T @ h64.abs() / 3
+    # a probability is off by its exponent's error and rounded to 16 bits, as the result is
+    assert bool(((got - want_dw).abs() <= (2 * U16 + 2 * off) * mag + U16 * want_dw.abs()).all())
+    # row 5 is token 2's target: its own term, and probabilities 1e-6 of the other two
+    assert bool(((dw[5].double().cpu() + h64[2] / 3).abs() <= (2 * U16 + 1e-4) * h64.abs().sum(0) / 3).all())
