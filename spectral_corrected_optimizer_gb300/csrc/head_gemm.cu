@@ -26,9 +26,9 @@
 // products) keeps the tensor pipe 81 % busy.  Steps that led there, training step of
 // 8192 tokens: one CTA per 128 x 256 tile 15.0 ms; pairs 12.3; one 128-row box per
 // operand instead of two of 64 rows 10.35; tiles dealt out by load 10.2; column blocks,
-// epilogues through tensor copies 9.8; two slabs handed over at a time 9.4.
-// The epilogue of a logits tile takes 2.2 us whatever the width, so below a width of
-// about 400 it, not the tensor core, sets the pace (3974 x 112636 x 200: 212 us).
+// epilogues through tensor copies 9.8; two slabs handed over at a time 9.5.
+// A logits tile takes at least 2.2 us, its epilogue's time, and 0.6 us of its own beside
+// 0.35 us per 64 k: narrow layers are bound by that (3974 x 112636 x 200: 212 us).
 //
 // Every wait on an mbarrier is bounded, as in gemm_tc.cu.
 #include <algorithm>

@@ -21,8 +21,8 @@
 // those two maxima meet in shared memory.
 //
 // Measured on a GB300 (copy bandwidth 6.78 TB/s), bf16 [65536][2048] with a residual:
-//   forward 183 us, 6.63 TB/s of x, r, s, y and the checkpoint (1.21 GB): 98 % of a copy;
-//   backward with y 216 us, 5.6 TB/s (83 %): issue slots 55 % busy, 32 warps an SM; a
+//   forward 182 us, 6.66 TB/s of x, r, s, y and the checkpoint (1.21 GB): 98 % of a copy;
+//   backward with y 214 us, 5.65 TB/s (83 %): issue slots 55 % busy, 32 warps an SM; a
 //     row's chain of shuffles, barrier and stores is what is waited for.  Two rows at a
 //     time (112 registers, half the warps) took 231 us, registers instead of the ring 249.
 // Odd rows cost more instructions than bytes (440 per 256 values against 240): norm of
