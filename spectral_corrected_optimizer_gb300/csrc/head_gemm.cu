@@ -80,15 +80,18 @@ struct Tile {
 // pair takes as many as bring its load up to the others' (a load is counted in
 // 64-k blocks and a tile's own cost as two of them).  With few rows dw's tiles are
 // short too, less than half of one of dh, and are dealt out by load in front of
-// the logits tiles.  Alone (HEAD_STATS) the logits tiles are dealt out in turn
-// too, so that neighbouring pairs share W's rows in L2.
+// the logits tiles (700 rows over 32001 x 4096: 520 us, in turn 560; 333 over 50001 x
+// 1000: 126 and 139).  Pairs with the same load share a stretch of the short tiles
+// in turn, so that neighbours work on the same rows of W or columns of a piece at
+// the same time: 2048 rows over 128256 x 2048 take 2.59 ms, with a stretch of its
+// own for each pair 2.84; 8192 9.3 and 9.55.
 struct Walk {
     int rows, m_tiles, d_tiles;
     int long_dw, longs;                  // dw tiles dealt out in turn (in front of dh's); this pair's tiles in turn
-    int line_dw, first_short, shorts;    // dw tiles dealt out by load; this pair's tiles of those and the logits
+    int line_dw;                         // dw tiles dealt out by load
+    int first_short, step_short, shorts; // this pair's tiles of those and the logits
     int pair, pairs;
     int dw_job, dh_job, short_job;       // -1: none
-    bool in_turn;
 };
 
 // In 64-k blocks (0.35 us): what a tile costs beside its own, and what a tile of
@@ -127,10 +130,8 @@ __device__ __forceinline__ Walk make_walk(const HeadGemm &g, int pair, int pairs
     w.long_dw = dw_tiles - w.line_dw;
     const int long_tiles = w.long_dw + dh_tiles, line = w.line_dw + n_short;
     w.longs = pair < long_tiles ? (long_tiles - pair + pairs - 1) / pairs : 0;
-    w.in_turn = long_tiles == 0;
-    w.first_short = pair;
-    w.shorts = pair < line ? (line - pair + pairs - 1) / pairs : 0;
-    if (!w.in_turn) {
+    int first = 0, behind = line, p0 = 0, p1 = pairs;  // tiles [first, behind) of the line go to pairs [p0, p1) in turn
+    if (long_tiles > 0) {
         // pairs below r1 have one dw tile more, pairs below r2 one long tile more:
         // three runs of pairs with equal loads
         const int r1 = w.long_dw % pairs, r2 = long_tiles % pairs;
@@ -164,9 +165,15 @@ __device__ __forceinline__ Walk make_walk(const HeadGemm &g, int pair, int pairs
             return at <= line_dw_cost ? (int)((at + dw_cost - 1) / dw_cost)
                                       : w.line_dw + (int)((at - line_dw_cost + cost - 1) / cost);
         };
-        w.first_short = first_of(pair);
-        w.shorts = first_of(pair + 1) - w.first_short;
+        const int run = (pair >= edge[1]) + (pair >= edge[2]);
+        p0 = edge[run];
+        p1 = edge[run + 1];
+        first = first_of(p0);
+        behind = first_of(p1);
     }
+    w.first_short = first + pair - p0;
+    w.step_short = p1 - p0;
+    w.shorts = max(0, (behind - w.first_short + w.step_short - 1) / w.step_short);
     return w;
 }
 
@@ -180,7 +187,7 @@ __device__ __forceinline__ Tile tile_at(const HeadGemm &g, const Walk &w, int i,
         j = t < w.long_dw ? w.dw_job : w.dh_job;
         if (t >= w.long_dw) t -= w.long_dw;
     } else {
-        t = w.first_short + (i - w.longs) * (w.in_turn ? w.pairs : 1);
+        t = w.first_short + (i - w.longs) * w.step_short;
         j = t < w.line_dw ? w.dw_job : w.short_job;
         if (t >= w.line_dw) t -= w.line_dw;
     }
