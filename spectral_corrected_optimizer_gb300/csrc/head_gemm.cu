@@ -21,12 +21,13 @@
 //
 // What bounds it: the power limit.  Measured on a GB300 (library bf16 product 1.88
 // PFLOP/s, 1.66 to 1.76 once the card is at its power limit), H 2048 x 2048, W 128256 x
-// 2048: statistics 572 us, 1.88 PFLOP/s, tensor pipe 85 % busy, before the limit, 610 us
+// 2048: statistics 560 us, 1.92 PFLOP/s, tensor pipe 89 % busy, before the limit, 610 us
 // at it; a launch of gradients (a piece's probabilities beside the piece before's two
-// products) keeps the tensor pipe 81 % busy.  Steps that led there, training step of
+// products) keeps the tensor pipe 86 % busy.  Steps that led there, training step of
 // 8192 tokens: one CTA per 128 x 256 tile 15.0 ms; pairs 12.3; one 128-row box per
 // operand instead of two of 64 rows 10.35; tiles dealt out by load 10.2; column blocks,
-// epilogues through tensor copies 9.8; two slabs handed over at a time 9.5.
+// epilogues through tensor copies 9.8; two slabs handed over at a time 9.55; short
+// tiles in turn among pairs of equal load 9.4.
 // A logits tile takes at least 2.2 us, its epilogue's time, and 0.6 us of its own beside
 // 0.35 us per 64 k: narrow layers are bound by that (3974 x 112636 x 200: 212 us).
 //

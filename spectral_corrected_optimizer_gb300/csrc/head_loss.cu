@@ -20,8 +20,8 @@
 // A piece's logits are formed twice, 8 N V D operations where keeping [N][V] would take
 // 6: that is the price of not keeping them, and of rounding a probability once (bf16,
 // normalised) instead of twice.  Measured on a GB300: 8192 tokens, a tenth without a
-// target, V = 128256, D = 2048: 9.5 ms (9.2 before the power limit sets in), 1.63
-// PFLOP/s; loss alone of 2048 tokens 648 us (579); of one token over 32001 x 4096 62 us
+// target, V = 128256, D = 2048: 9.4 ms (9.1 before the power limit sets in), 1.65
+// PFLOP/s; loss alone of 2048 tokens 650 us (579); of one token over 32001 x 4096 62 us
 // (W once: 39 us; its 126 tiles lie on 76 pairs of SMs, 83 %, and three launches); loss
 // and gradients of 333 tokens, half without a target, over 50001 x 1000 126 us.
 #include <algorithm>
