@@ -27,7 +27,7 @@
 // 8192 tokens: one CTA per 128 x 256 tile 15.0 ms; pairs 12.3; one 128-row box per
 // operand instead of two of 64 rows 10.35; tiles dealt out by load 10.2; column blocks,
 // epilogues through tensor copies 9.8; two slabs handed over at a time 9.55; short
-// tiles in turn among pairs of equal load 9.4.
+// tiles in turn among pairs of equal load 9.4; pieces of 256 MB instead of 128 9.25.
 // A logits tile takes at least 2.2 us, its epilogue's time, and 0.6 us of its own beside
 // 0.35 us per 64 k: narrow layers are bound by that (3974 x 112636 x 200: 212 us).
 //

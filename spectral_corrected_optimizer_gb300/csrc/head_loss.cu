@@ -20,7 +20,7 @@
 // A piece's logits are formed twice, 8 N V D operations where keeping [N][V] would take
 // 6: that is the price of not keeping them, and of rounding a probability once (bf16,
 // normalised) instead of twice.  Measured on a GB300: 8192 tokens, a tenth without a
-// target, V = 128256, D = 2048: 9.4 ms (9.1 before the power limit sets in), 1.65
+// target, V = 128256, D = 2048: 9.25 ms (9.0 before the power limit sets in), 1.68
 // PFLOP/s; loss alone of 2048 tokens 650 us (579); of one token over 32001 x 4096 62 us
 // (W once: 39 us; its 126 tiles lie on 76 pairs of SMs, 83 %, and three launches); loss
 // and gradients of 333 tokens, half without a target, over 50001 x 1000 126 us.
@@ -305,15 +305,17 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const Span<const float> su
 // 0.37) times 2^-24 dim / 32 for dim 256 to 16384 over normal values, with and
 // without a common direction; 0.7 to 2.4 times where all products have one sign.  The
 // mean is given back in the factor of the exponent; without it every
-// log-sum-exp comes out low (1.2e-6 of the loss of one token at 32001 x 4096).
+// log-sum-exp comes out low (1.2e-6 of the loss of one token at 32001 x 4096 where 2e-8 to 5e-7 are left).
 float head_log2e(int dim) { return (float)(1.4426950408889634 * (1.0 + dim * 0x1p-30)); }
 
 // ---- plan ------------------------------------------------------------------------------------
 
-// Bytes of one piece buffer: about the L2, so that a piece is read back from
-// there while it is in use; but at least 4096 vocabulary rows, so that adding
-// up dh stays small beside the products.
-constexpr int64_t kPieceBytes = 128 << 20;
+// Bytes of one piece buffer.  Each piece adds to dh once and ends a launch, so few
+// large ones are better, although a piece of 256 MB does not stay in L2: 8192 tokens
+// over 128256 x 2048 take 9.27 ms with 256 or 192 MB, 9.38 with 128, 9.6 with 64; 16384
+// 21.3 ms with 256, 21.4 with 192, 21.8 with 128 or less.  But at least 4096 vocabulary
+// rows, so that adding up dh stays small beside the products.
+constexpr int64_t kPieceBytes = 256 << 20;
 constexpr int kPieceMin = 4096;
 
 struct HeadPlan {

@@ -438,7 +438,7 @@ def test_head_loss_grad(tokens, vocab, dim, ignored, dtype):
 
 
 def test_head_loss_grad_over_several_pieces():
-    # 17000 tokens: a piece buffer holds 4096 of the vocabulary's rows, three pieces in turn
+    # 17000 tokens: a piece buffer holds 7680 of the vocabulary's rows, two pieces
     g = gen(31)
     tokens, vocab, dim = 17000, 9001, 16
     w, h = randn(g, (vocab, dim), BF, 0.5), randn(g, (tokens, dim), BF)
@@ -448,6 +448,23 @@ def test_head_loss_grad_over_several_pieces():
     want = ref.head(h, w, target, mean=False, grad_scale=0.5)
     check_loss(loss, row_loss, want, dim)
     check_grads(dh, dw, want, h, w)
+
+
+def test_head_loss_grad_over_three_pieces():
+    # 6000 tokens: a piece buffer holds 21760 of the vocabulary's rows, the first buffer is used twice
+    g = gen(32)
+    tokens, vocab, dim = 6000, 47001, 40
+    w, h = randn(g, (vocab, dim), BF, 0.3), randn(g, (tokens, dim), BF)
+    target = torch.randint(0, vocab, (tokens,), generator=g)
+    target[::5] = -100
+    before = randn(g, (vocab, dim), FP, 1e-4)
+    args = h.cuda(), w.cuda(), target.cuda()
+    loss, row_loss, dh, dw = se().head_loss_grad(*args, dw=before.cuda(), accumulate=True)
+    want = ref.head(h, w, target)
+    check_loss(loss, row_loss, want, dim)
+    check_grads(dh, dw, want, h, w, before=before)
+    again = se().head_loss_grad(*args, dw=before.cuda(), accumulate=True)
+    assert torch.equal(again[2], dh) and torch.equal(again[3], dw)
 
 
 @pytest.mark.parametrize("dtype", [FP, BF])
