@@ -42,7 +42,12 @@ namespace spco {
 namespace {
 
 constexpr int kGroup = STAGE_CKPT_GROUP;
-constexpr int kMaxThreads = 512, kMaxDim = kMaxThreads * 8 * 8, kMaxGroups = kMaxDim / kGroup;
+constexpr int kMaxThreads = 512, kMaxDim = kMaxThreads * 8 * 8;
+// Pieces of 8 values per thread.  A row that begins between two 16-byte boundaries touches
+// one piece more than it has: from 32762 values on it needs a ninth per thread.
+constexpr int kMaxPieces = 9;
+constexpr int kMaxHeads = kMaxThreads * kMaxPieces / 16;  // 16 threads' pieces in a row
+static_assert(kMaxThreads * kMaxPieces >= (kMaxDim + 14) / 8, "the widest row at any place");
 constexpr float kFp8Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
 
@@ -248,13 +253,13 @@ template <typename T, int ROWS, int NV>
 __global__ void __launch_bounds__(kMaxThreads, NV * sizeof(T) <= 4 ? 2 : 1) resnorm_forward_kernel(const Forward<T> a) {
     __shared__ __align__(16) float red[2][kMaxWarps];
     // of each 16 threads' pieces: the maximum of their own group, and of the ph values in front of it
-    __shared__ float group_max[2][ROWS == ROWS_VEC ? 1 : kMaxGroups + 2], head_max[2][ROWS == ROWS_VEC ? 1 : kMaxGroups + 2];
+    __shared__ float group_max[2][ROWS == ROWS_VEC ? 1 : kMaxHeads + 1], head_max[2][ROWS == ROWS_VEC ? 1 : kMaxHeads + 1];
     const int dim = a.dim, groups = (dim + kGroup - 1) / kGroup;
     const int ph = ROWS == ROWS_VEC ? 0 : (int)((a.y.lo + (int64_t)blockIdx.x * dim) & 7);
     const int col0 = (int)threadIdx.x * 8 - ph, step = (int)blockDim.x * 8;
     const int hl = threadIdx.x & 15;
     if (ROWS != ROWS_VEC)
-        for (int i = threadIdx.x; i < kMaxGroups + 2; i += blockDim.x) head_max[0][i] = head_max[1][i] = 0.f;
+        for (int i = threadIdx.x; i < kMaxHeads + 1; i += blockDim.x) head_max[0][i] = head_max[1][i] = 0.f;
     const BlockSum block_sum{red, (int)blockDim.x >> 5};
     block_sum.init();
     float gm[NV <= 2 ? NV : 1][8];
@@ -322,10 +327,8 @@ __global__ void __launch_bounds__(kMaxThreads, NV * sizeof(T) <= 4 ? 2 : 1) resn
                 if (hl == 0) a.scale[row * groups + col / kGroup] = sc;
             } else if (hl == 0) {
                 const int h = (k * (int)blockDim.x + (int)threadIdx.x) / 16;
-                if (h <= kMaxGroups) {
-                    group_max[parity][h] = m;
-                    head_max[parity][h] = head;
-                }
+                group_max[parity][h] = m;
+                head_max[parity][h] = head;
             }
         }
         if (ROWS != ROWS_VEC) __syncwarp();  // one warp: block_sum has no barrier
@@ -619,7 +622,7 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float *__restrict__ 
 
 // Values per thread of the forward pass: 16 (NV = 2) up to a width of 8192, so
 // that a row of 2048 takes 4 warps and many rows are in flight on an SM; then 32
-// and 64.  The backward pass keeps four times as much per value and takes 8 (NV
+// and 64 (72 for the widest rows off their boundaries).  The backward pass keeps four times as much per value and takes 8 (NV
 // = 1) up to 4096.
 struct Shape {
     int nv, threads;
@@ -628,6 +631,7 @@ Shape shape_of(int dim, bool vec, bool one) {
     const int64_t vecs = vec ? dim / 8 : (dim + 14) / 8;  // 8-value pieces that a row can touch
     int nv = 1;
     while (nv < 8 && (vecs > kMaxThreads * nv || (!one && nv < 2 && vecs > 32))) nv *= 2;
+    if (vecs > kMaxThreads * nv) nv = kMaxPieces;
     return {nv, (int)round_up(ceil_div(vecs, nv), 32)};
 }
 
@@ -652,9 +656,12 @@ template <typename F> int with_nv(int nv, F &&f) {
         case 1: return f(std::integral_constant<int, 1>{});
         case 2: return f(std::integral_constant<int, 2>{});
         case 4: return f(std::integral_constant<int, 4>{});
-        default: return f(std::integral_constant<int, 8>{});
+        case 8: return f(std::integral_constant<int, 8>{});
+        default: return f(std::integral_constant<int, kMaxPieces>{});
     }
 }
+// the layout of vector rows, which never take the ninth piece
+constexpr int vec_rows(int nv) { return nv == kMaxPieces ? ROWS_ODD : ROWS_VEC; }
 
 int check_sizes(int64_t rows, int32_t dim, int32_t type, const char *what) {
     if (rows < 0 || rows > INT32_MAX)
@@ -673,7 +680,7 @@ template <typename T> int run_forward(const Shape &sh, int rows, const Forward<T
         // 8).  Multiples of 8: a block's rows begin alike.
         const int per_sm = rows == ROWS_VEC ? 64 : std::max(8, 4096 / sh.threads / 8 * 8);
         const int grid = (int)std::min<int64_t>(a.rows, (int64_t)num_sms() * per_sm);
-        auto *k = rows == ROWS_VEC   ? &resnorm_forward_kernel<T, ROWS_VEC, NV>
+        auto *k = rows == ROWS_VEC   ? &resnorm_forward_kernel<T, vec_rows(NV), NV>
                   : rows == ROWS_ODD ? &resnorm_forward_kernel<T, ROWS_ODD, NV>
                                      : &resnorm_forward_kernel<T, ROWS_ANY, NV>;
         SPCO_LAUNCH("resnorm_forward", st, k<<<grid, sh.threads, 0, st>>>(a));
@@ -687,7 +694,7 @@ int run_backward(const Shape &sh, int rows, int blocks, const Backward<T> &a, fl
     return with_nv(sh.nv, [&](auto nv) -> int {
         constexpr int NV = decltype(nv)::value;
         constexpr int RING = ring_of(NV, sizeof(T));
-        auto *k = rows == ROWS_VEC   ? &resnorm_backward_kernel<T, ROWS_VEC, NV, RING>
+        auto *k = rows == ROWS_VEC   ? &resnorm_backward_kernel<T, vec_rows(NV), NV, RING>
                   : rows == ROWS_ODD ? &resnorm_backward_kernel<T, ROWS_ODD, NV, RING>
                                      : &resnorm_backward_kernel<T, ROWS_ANY, NV, RING>;
         const int smem = ring_bytes(sh, sizeof(T));
