@@ -288,7 +288,8 @@ __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Tile &x,
                                                int half) {
     const int target = of.target, first = x.n + half * (BN / 2);
     float r = rintf(of.norm.x * kLog2e), s = 0.f;
-    if (!(fabsf(r) < kMuch)) r = 0.f;  // not finite: the row's loss will say so
+    // no reference in a target's logit that is not finite (an impossible target: -inf): the first block moves r up
+    if (!(fabsf(r) < kMuch)) r = -kMuch;
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), blocks_before(first, g.vocab), [&](int c, float (&v)[32]) {
         const int v0 = first + c * 32;
         if (v0 + 32 > g.vocab) {

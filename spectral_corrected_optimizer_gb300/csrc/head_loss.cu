@@ -235,11 +235,15 @@ __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *__r
                 // the target's logit in log2, to twice fp32's digits: hi + lo
                 const float lt = target_logit[row], hi = lt * kLog2e;
                 const float lo = fmaf(lt, kLog2e, -hi) + lt * kLog2eRest;
-                const float above = (m - hi) - lo;  // log2 of 2^r / e^target
+                // log2 of 2^r / e^target; a target's logit of -inf (or one that overflows in log2) leaves no term
+                const bool none = hi == -INFINITY;
+                const float above = none ? INFINITY : (m - hi) - lo;
                 const float total = s + exp2f(-above);
                 norm[row] = make_float2(m + log2f(total), -s / total);
                 // 2^30 S stays far from overflow; beyond it log(total) is no longer a small correction
-                l = above < 30.f ? log1pf(s * exp2f(above)) : (above + log2f(total)) * kLn2;
+                l = above < 30.f ? log1pf(s * exp2f(above))
+                    : none       ? (m + log2f(total)) * kLn2 - lt
+                                 : (above + log2f(total)) * kLn2;
                 row_loss[row_of[row]] = l;
             }
             row_sum[w] = l;

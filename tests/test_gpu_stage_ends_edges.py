@@ -53,3 +53,39 @@ def test_norm_of_the_widest_rows_off_a_boundary(dim, dtype):
     assert bool(((dx.cpu().double() - w[0]).abs() <= base.u_of(dtype) * w[0].abs() + 100 * U32 * w[1]).all())
     assert bool(((dgamma.cpu().double() - w[2]).abs() <= 15 * U32 * w[3]).all())
     assert bool(((y2.cpu().double() - w[4]).abs() <= (base.u_of(dtype) + 4 * U32) * w[4].abs()).all())
+
+
+# ---------------------------------------------------------------- head: logits that are not finite
+
+@pytest.mark.parametrize("others", [0.0, -200.0, 150.0])
+def test_head_of_an_impossible_target(others):
+    # token 0: the target's logit overflows to -inf, the 599 other logits are equal; token 1 is an ordinary one
+    vocab, dim = 600, 16
+    w, h = torch.zeros(vocab, dim, dtype=BF), torch.zeros(2, dim, dtype=BF)
+    h[0, 0], h[0, 1], h[1, 2] = 3e38, 1.0, 1.0
+    w[:, 1] = others
+    w[7, 0] = -1000.0
+    w[:, 2] = torch.linspace(-2, 2, vocab).to(BF)
+    target = torch.tensor([7, 80])
+    args = h.cuda(), w.cuda(), target.cuda()
+    loss, row_loss, dh, dw = base.se().head_loss_grad(*args)
+    assert float(row_loss[0]) == float("inf") and float(loss) == float("inf")
+    want = ref.head(h[1:], w, target[1:])
+    base.check_loss(row_loss[1], row_loss[1:], want, dim)
+    # softmax - onehot of token 0: -1 at its target, 1 / 599 elsewhere, rounded to bf16; half of it for the mean
+    p = torch.full((vocab,), 1 / 599, dtype=torch.float64)
+    p[7] = -1.0
+    assert bool(((dw[:, 1].cpu().double() - p / 2).abs() <= base.U16 * p.abs() / 2).all())
+    assert bool(dw.isfinite().all()) and bool(dh.isfinite().all())
+    assert torch.equal(base.se().head_loss(*args)[1], row_loss)
+
+
+def test_head_of_a_finite_loss_beyond_1e38():
+    # lse = log(3 + 0), the target's logit is -2.5e38: finite in e, beyond fp32 in log2
+    w, h = torch.zeros(4, 8, dtype=BF), torch.zeros(1, 8, dtype=BF)
+    h[0, 0], w[2, 0] = 2.5e38, -1.0
+    row_loss = base.se().head_loss(h.cuda(), w.cuda(), torch.tensor([2]).cuda())[1]
+    assert abs(float(row_loss[0]) / float(h[0, 0]) - 1) <= 4 * U32
+    # an infinite target's logit and other rows' NaN stay visible
+    w[2, 0] = 1e3
+    assert bool(base.se().head_loss(h.cuda(), w.cuda(), torch.tensor([2]).cuda())[1].isnan().all())
