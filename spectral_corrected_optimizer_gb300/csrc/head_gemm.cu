@@ -254,16 +254,18 @@ __device__ __forceinline__ int blocks_before(int first, int end) { return min(4,
 struct RowOf {
     int row, target;
     bool in;
-    float2 norm;  // HEAD_STATS: x the target's logit; HEAD_PROB: HeadGemm::norm
+    float logit;    // HEAD_STATS: the target's
+    HeadNorm norm;  // HEAD_PROB
 };
 __device__ __forceinline__ RowOf row_of(const HeadGemm &g, const Walk &w, const Tile &x, int q, int lane) {
     RowOf o;
     o.row = x.m + x.rank * CM + q * 32 + lane;
     o.in = x.kind <= HEAD_PROB && o.row < w.rows;
     o.target = o.in ? g.target[o.row] : -1;
-    o.norm = make_float2(0.f, 0.f);
+    o.logit = 0.f;
+    o.norm = HeadNorm{0.f, 0.f, 0.f};
     if (o.in) {
-        if (x.kind == HEAD_STATS) o.norm.x = g.target_logit[o.row];
+        if (x.kind == HEAD_STATS) o.logit = g.target_logit[o.row];
         else o.norm = g.norm[o.row];
     }
     return o;
@@ -287,7 +289,7 @@ __device__ __forceinline__ float sum_exp2(const float (&v)[32], float log2e, flo
 __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Tile &x, const RowOf &of, uint32_t acc, int q,
                                                int half) {
     const int target = of.target, first = x.n + half * (BN / 2);
-    float r = rintf(of.norm.x * kLog2e), s = 0.f;
+    float r = rintf(of.logit * kLog2e), s = 0.f;
     // no reference in a target's logit that is not finite (an impossible target: -inf): the first block moves r up
     if (!(fabsf(r) < kMuch)) r = -kMuch;
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), blocks_before(first, g.vocab), [&](int c, float (&v)[32]) {
@@ -362,16 +364,16 @@ __device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Tile &x, 
     const int row0 = of.row - out.lane;
     const bool in = of.in;
     const int target = in ? of.target - x.v0 : -1;  // column within the piece
-    const float2 norm = of.norm;
+    const HeadNorm norm = of.norm;
     const int first = x.n + half * (BN / 2);
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), 4, [&](int c, float (&v)[32]) {
         const int p0 = first + c * 32;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], g.log2e, -norm.x));
+        for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], g.log2e, -norm.m)) * norm.inv;
         if ((unsigned)(target - p0) < 32u) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (p0 + i == target) v[i] = norm.y;
+                if (p0 + i == target) v[i] = norm.target;
         }
         if (!in || p0 + 32 > x.width) {
 #pragma unroll

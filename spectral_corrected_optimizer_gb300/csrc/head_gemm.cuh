@@ -14,6 +14,15 @@ struct HeadState {
     float inv_count;     // 1 / rows for the mean, 1 for the sum
 };
 
+// What turns a row's logits into probabilities: 2^(logit in log2 - m) * inv.  m is a
+// whole number, so the exponent is rounded once, to its own size; joined with the
+// logarithm of the sum in one fp32 value, a row whose logits are near 1e5 would lose
+// 3e-3 of every probability.
+struct HeadNorm {
+    float m, inv;
+    float target;  // softmax - 1 at the target
+};
+
 enum HeadJobKind : int {
     HEAD_STATS = 0,  // logits tile -> each row's scale and sum of exponentials without the target's
     HEAD_PROB = 1,   // logits tile -> softmax - onehot, bf16, into a piece's buffer
@@ -48,7 +57,7 @@ struct HeadGemm {
     const int *target;         // [row_cap]
     const float *target_logit; // [row_cap]
     float2 *stats;             // [2 * ceil(vocab / 256)][row_cap]: r and the part's sum relative to 2^r
-    const float2 *norm;        // [row_cap]: log2 of the sum of exponentials, softmax - 1 at the target
+    const HeadNorm *norm;      // [row_cap]
     void *dw;                  // [vocab][dim]
     int dw_bf16, dw_add;
     int dw_tma;                // dw is stored through tm_dw

@@ -202,7 +202,7 @@ template <int ROWS>
 __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
                                                        const float *__restrict__ target_logit,
                                                        const int *__restrict__ row_of, HeadState *state,
-                                                       float2 *__restrict__ norm, float *__restrict__ row_loss,
+                                                       HeadNorm *__restrict__ norm, float *__restrict__ row_loss,
                                                        float *__restrict__ block_loss, float *__restrict__ loss) {
     constexpr int LANES = kLseThreads / ROWS;
     __shared__ float sm[LANES][ROWS + 1], ss[LANES][ROWS + 1], row_sum[ROWS];
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *__r
                 const bool none = hi == -INFINITY;
                 const float above = none ? INFINITY : (m - hi) - lo;
                 const float total = s + exp2f(-above);
-                norm[row] = make_float2(m + log2f(total), -s / total);
+                norm[row] = HeadNorm{m, 1.f / total, -s / total};
                 // 2^30 S stays far from overflow; beyond it log(total) is no longer a small correction
                 l = above < 30.f ? log1pf(s * exp2f(above))
                     : none       ? (m + log2f(total)) * kLn2 - lt
@@ -345,7 +345,7 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
     p.off_at = take(cap * 4);
     p.off_target = take(cap * 4);
     p.off_tlogit = take(cap * 4);
-    p.off_norm = take(cap * 8);
+    p.off_norm = take(cap * sizeof(HeadNorm));
     p.off_block_loss = take(ceil_div(cap, kLseFew) * 4);
     p.off_stats = take((int64_t)p.parts * cap * 8);
     p.off_h = take(cap * round_up(dim, 64) * 2);
@@ -409,7 +409,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     int *row_of = reinterpret_cast<int *>(c.ws + p.off_row_of), *at = reinterpret_cast<int *>(c.ws + p.off_at);
     int *target = reinterpret_cast<int *>(c.ws + p.off_target);
     float *tlogit = reinterpret_cast<float *>(c.ws + p.off_tlogit);
-    float2 *norm = reinterpret_cast<float2 *>(c.ws + p.off_norm);
+    HeadNorm *norm = reinterpret_cast<HeadNorm *>(c.ws + p.off_norm);
     uint16_t *hc = reinterpret_cast<uint16_t *>(c.ws + p.off_h);
     const uint16_t *w = static_cast<const uint16_t *>(c.w);
     const int tokens = (int)c.tokens, vocab = (int)c.vocab;

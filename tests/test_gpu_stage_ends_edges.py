@@ -89,3 +89,24 @@ def test_head_of_a_finite_loss_beyond_1e38():
     # an infinite target's logit and other rows' NaN stay visible
     w[2, 0] = 1e3
     assert bool(base.se().head_loss(h.cuda(), w.cuda(), torch.tensor([2]).cuda())[1].isnan().all())
+
+
+# ---------------------------------------------------------------- head: large logits
+
+def test_head_probabilities_of_large_logits():
+    # all 512 logits of token i are L_i, exactly: every probability is 2^-9, which bf16 holds, and an error of
+    # 2^-10 of it (a rounding of fp32 at 1.44 L_i from L_i = 3e4 on) would come out as another value
+    large = torch.tensor([3.0e4, -4.3e4, 6.1e4, -9.9e4, 2.3e5, -3.3e5, 7.7e5, 1.1e6], dtype=BF)
+    n, vocab, dim = len(large), 512, 16
+    h, w = torch.zeros(n, dim, dtype=BF), torch.zeros(vocab, dim, dtype=BF)
+    h[:, :n] = torch.diag(large)
+    w[:, :n] = 1.0
+    target = torch.arange(n) * 60
+    row_loss, dw = [base.se().head_loss_grad(h.cuda(), w.cuda(), target.cuda())[i].cpu() for i in (1, 3)]
+    want = (large.float() / vocab / n).expand(vocab, n).clone()
+    want[target, torch.arange(n)] = 0
+    got = dw[:, :n].clone()
+    got[target, torch.arange(n)] = 0
+    assert torch.equal(got, want)
+    onto = dw[target, torch.arange(n)].double() / large.double() * n
+    assert bool(((onto + 511 / 512).abs() <= base.U16).all()) and bool(row_loss.isfinite().all())
