@@ -87,8 +87,13 @@ int resnorm_backward(const void *dy, const void *ds, const void *q, const float 
 
 /* Softmax cross entropy of the vocabulary head, from bf16 hidden states
  * h: [tokens][dim] and bf16 weights w: [vocab][dim]:
- *   l_i = h_i w^T (fp32),  row_loss_i = log sum_v exp(l_iv) - l_i,target_i,
+ *   l_i = h_i w^T (fp32 sums),  row_loss_i = log sum_v exp(l_iv) - l_i,target_i,
  *   loss = sum_i row_loss_i / (mean ? number of tokens with a target : 1).
+ * The sums run on the tensor cores, which cut off what falls below fp32's last place
+ * every 16 products; their mean loss, dim 2^-30 of a logit, is given back.  What is left
+ * of a logit's error is within some dim 2^-30 of it either way, for exact sums of dense h
+ * too; the target's logit is a separate fp32 dot product, and a logit to which only one
+ * group of 16 values of h contributes is exact to fp32.
  * Tokens whose target is ignore_index have row_loss 0 and cost nothing; if no
  * token has a target, loss = 0.  row_loss: [tokens] fp32, loss: one fp32. */
 int64_t head_loss_workspace(int64_t tokens, int64_t vocab, int32_t dim);

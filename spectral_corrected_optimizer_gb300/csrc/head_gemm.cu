@@ -254,7 +254,7 @@ __device__ __forceinline__ int blocks_before(int first, int end) { return min(4,
 struct RowOf {
     int row, target;
     bool in;
-    float logit;    // HEAD_STATS: the target's
+    HeadRow h;
     HeadNorm norm;  // HEAD_PROB
 };
 __device__ __forceinline__ RowOf row_of(const HeadGemm &g, const Walk &w, const Tile &x, int q, int lane) {
@@ -262,11 +262,11 @@ __device__ __forceinline__ RowOf row_of(const HeadGemm &g, const Walk &w, const 
     o.row = x.m + x.rank * CM + q * 32 + lane;
     o.in = x.kind <= HEAD_PROB && o.row < w.rows;
     o.target = o.in ? g.target[o.row] : -1;
-    o.logit = 0.f;
+    o.h = HeadRow{0.f, 0.f};
     o.norm = HeadNorm{0.f, 0.f, 0.f};
     if (o.in) {
-        if (x.kind == HEAD_STATS) o.logit = g.target_logit[o.row];
-        else o.norm = g.norm[o.row];
+        o.h = g.rows[o.row];
+        if (x.kind == HEAD_PROB) o.norm = g.norm[o.row];
     }
     return o;
 }
@@ -289,7 +289,8 @@ __device__ __forceinline__ float sum_exp2(const float (&v)[32], float log2e, flo
 __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Tile &x, const RowOf &of, uint32_t acc, int q,
                                                int half) {
     const int target = of.target, first = x.n + half * (BN / 2);
-    float r = rintf(of.logit * kLog2e), s = 0.f;
+    const float log2e = of.h.log2e;
+    float r = rintf(of.h.target_logit * kLog2e), s = 0.f;
     // no reference in a target's logit that is not finite (an impossible target: -inf): the first block moves r up
     if (!(fabsf(r) < kMuch)) r = -kMuch;
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), blocks_before(first, g.vocab), [&](int c, float (&v)[32]) {
@@ -304,16 +305,16 @@ __device__ __forceinline__ void epilogue_stats(const HeadGemm &g, const Tile &x,
             for (int i = 0; i < 32; ++i)
                 if (v0 + i == target) v[i] = -INFINITY;
         }
-        float t = sum_exp2(v, g.log2e, r);
+        float t = sum_exp2(v, log2e, r);
         if (!(t < kMuch)) {
             float top = v[0];
 #pragma unroll
             for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-            const float most = rintf(top * g.log2e);
+            const float most = rintf(top * log2e);
             if (most > r) {  // false where only NaN brought us here: it stays in the sum
                 s *= ex2(r - most);
                 r = most;
-                t = sum_exp2(v, g.log2e, r);
+                t = sum_exp2(v, log2e, r);
             }
         }
         s += t;
@@ -365,11 +366,12 @@ __device__ __forceinline__ void epilogue_prob(const HeadGemm &g, const Tile &x, 
     const bool in = of.in;
     const int target = in ? of.target - x.v0 : -1;  // column within the piece
     const HeadNorm norm = of.norm;
+    const float log2e = of.h.log2e;
     const int first = x.n + half * (BN / 2);
     for_columns(acc + half * (BN / 2) + ((uint32_t)(q * 32) << 16), 4, [&](int c, float (&v)[32]) {
         const int p0 = first + c * 32;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], g.log2e, -norm.m)) * norm.inv;
+        for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(v[i], log2e, -norm.m)) * norm.inv;
         if ((unsigned)(target - p0) < 32u) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)

@@ -14,6 +14,12 @@ struct HeadState {
     float inv_count;     // 1 / rows for the mean, 1 for the sum
 };
 
+// What the products need of a compact row of h.
+struct HeadRow {
+    float target_logit;
+    float log2e;  // times a tensor-core logit: the logit in log2 (row_log2e)
+};
+
 // What turns a row's logits into probabilities: 2^(logit in log2 - m) * inv.  m is a
 // whole number, so the exponent is rounded once, to its own size; joined with the
 // logarithm of the sum in one fp32 value, a row whose logits are near 1e5 would lose
@@ -55,14 +61,13 @@ struct HeadGemm {
     int row_cap;               // rows of the compact buffers (a multiple of the tile height)
     const HeadState *state;
     const int *target;         // [row_cap]
-    const float *target_logit; // [row_cap]
+    const HeadRow *rows;       // [row_cap]
     float2 *stats;             // [2 * ceil(vocab / 256)][row_cap]: r and the part's sum relative to 2^r
     const HeadNorm *norm;      // [row_cap]
     void *dw;                  // [vocab][dim]
     int dw_bf16, dw_add;
     int dw_tma;                // dw is stored through tm_dw
     float grad_scale;
-    float log2e;               // times a tensor-core logit: the logit in log2 (see head_log2e)
 };
 
 constexpr int kHeadTileM = 256, kHeadTileN = 256;

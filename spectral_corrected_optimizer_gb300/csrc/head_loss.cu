@@ -52,6 +52,26 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float s) {
     return fmaf(hi_f(a), hi_f(b), fmaf(lo_f(a), lo_f(b), s));
 }
 
+// The tensor cores cut off, rather than round, what falls below the last place of
+// each of the dim / 16 sums on the way to a logit, which leaves it short in the
+// mean.  In units of 2^-24 dim / 32 of the logit, measured for dim 512 to 65536: 0.38
+// to 0.54 over normal values with and without a common direction (standard deviation
+// 0.15 to 0.4); 0.7 to 2.9 where all products have one sign; 0 where the sums are
+// exact.  Half a unit, dim 2^-30, is given back in the factor of the exponent: the
+// loss of one token at 32001 x 4096 is 2e-8 to 5e-7 off, 1.2e-6 without.  16 products
+// of which h holds only zeros cut nothing off and do not count, so a logit of a few
+// values of h is left as it is.  Where dense h and w make exact sums (small whole
+// numbers), the logits other than the target's come out dim 2^-30 of themselves too far
+// from 0, as inexact ones would come out too near it without the factor.
+__device__ __forceinline__ float row_log2e(int blocks) {  // of 16 values of h, not all 0
+    return kLog2e + fmaf(kLog2e, (float)max(blocks - 1, 0) * 0x1p-26f, kLog2eRest);
+}
+// how many of the 16 blocks of a warp's 32 pieces (8 values) hold anything but zeros
+__device__ __forceinline__ int blocks_of(uint4 a) {
+    const unsigned b = __ballot_sync(0xffffffffu, ((a.x | a.y | a.z | a.w) & 0x7fff7fffu) != 0);
+    return __popc((b | b >> 1) & 0x55555555u);
+}
+
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 
 // Lists the tokens with a target in token order (row_of[r] = token of row r,
@@ -64,7 +84,7 @@ constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 //
 // On the way the logit of each row's target is formed as an fp32 dot product:
 // the loss is the difference between it and the log-sum-exp, and a tensor core's
-// logit is off by more than fp32's rounding (head_log2e).
+// logit is off by more than fp32's rounding (row_log2e).
 constexpr int kPadBlocks = 8;
 template <typename ID>
 __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__restrict__ targets, int64_t ignore, int tokens,
@@ -73,10 +93,11 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
                                                         const uint16_t *__restrict__ w, int dim, int row_cap, int h_vec,
                                                         int w_vec, HeadState *state, int *__restrict__ row_of,
                                                         int *__restrict__ at, int *__restrict__ target,
-                                                        uint16_t *__restrict__ out, float *__restrict__ target_logit,
+                                                        uint16_t *__restrict__ out, HeadRow *__restrict__ head_row,
                                                         float *__restrict__ row_loss, unsigned *flag) {
     __shared__ int red[2][kRowWarps], own_token[kRowThreads], own_target[kRowThreads];
     __shared__ float dots[kRowWarps];
+    __shared__ int held[kRowWarps];
     grid_dependency_launch();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int pad = (int)blockIdx.x - own_blocks;  // >= 0: a block of zero rows, which counts all targets
@@ -128,22 +149,31 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
         if (count == 0) return;
         const uint16_t *hr = h + (int64_t)own_token[0] * dim, *wr = w + (int64_t)own_target[0] * dim;
         float s = 0.f;
-        for (int v = threadIdx.x; v < vecs; v += kRowThreads) {
+        int n = 0;
+        for (int v0 = wp * 32; v0 < vecs; v0 += kRowThreads) {
+            const int v = v0 + lane;
             uint4 a = make_uint4(0, 0, 0, 0);
             if (v * 8 < dim) {
                 a = row_vec(hr, v, dim, h_vec);
                 const uint4 b = row_vec(wr, v, dim, w_vec);
                 s += dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, 0.f))));
             }
-            reinterpret_cast<uint4 *>(out + ((int64_t)(v / 8) * row_cap + before) * 64)[v % 8] = a;
+            if (v < vecs) reinterpret_cast<uint4 *>(out + ((int64_t)(v / 8) * row_cap + before) * 64)[v % 8] = a;
+            n += blocks_of(a);
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) dots[wp] = s;
+        if (lane == 0) {
+            dots[wp] = s;
+            held[wp] = n;
+        }
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int i = 1; i < kRowWarps; ++i) s += dots[i];
-            target_logit[before] = s;
+            for (int i = 1; i < kRowWarps; ++i) {
+                s += dots[i];
+                n += held[i];
+            }
+            head_row[before] = HeadRow{s, row_log2e(n)};
         }
         return;
     }
@@ -152,19 +182,22 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
         const uint16_t *hr = i < count ? h + (int64_t)own_token[i] * dim : nullptr;
         const uint16_t *wr = i < count ? w + (int64_t)own_target[i] * dim : nullptr;
         float s = 0.f;
+        int n = 0;
 #pragma unroll 4
-        for (int v = lane; v < vecs; v += 32) {
+        for (int v0 = 0; v0 < vecs; v0 += 32) {
+            const int v = v0 + lane;
             uint4 a = make_uint4(0, 0, 0, 0);
             if (hr && v * 8 < dim) {
                 a = row_vec(hr, v, dim, h_vec);
                 const uint4 b = row_vec(wr, v, dim, w_vec);
                 s += dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, 0.f))));
             }
-            reinterpret_cast<uint4 *>(out + ((int64_t)(v / 8) * row_cap + r) * 64)[v % 8] = a;
+            if (v < vecs) reinterpret_cast<uint4 *>(out + ((int64_t)(v / 8) * row_cap + r) * 64)[v % 8] = a;
+            n += blocks_of(a);
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0 && i < count) target_logit[r] = s;
+        if (lane == 0 && i < count) head_row[r] = HeadRow{s, row_log2e(n)};
     }
 }
 
@@ -200,7 +233,7 @@ __device__ __forceinline__ void join(float &m, float &s, float2 x) {
 constexpr int kLseThreads = 1024, kLseFew = 8, kLseMany = 32;
 template <int ROWS>
 __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
-                                                       const float *__restrict__ target_logit,
+                                                       const HeadRow *__restrict__ head_row,
                                                        const int *__restrict__ row_of, HeadState *state,
                                                        HeadNorm *__restrict__ norm, float *__restrict__ row_loss,
                                                        float *__restrict__ block_loss, float *__restrict__ loss) {
@@ -233,7 +266,7 @@ __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *__r
             float l = 0.f;
             if (row < rows) {
                 // the target's logit in log2, to twice fp32's digits: hi + lo
-                const float lt = target_logit[row], hi = lt * kLog2e;
+                const float lt = head_row[row].target_logit, hi = lt * kLog2e;
                 const float lo = fmaf(lt, kLog2e, -hi) + lt * kLog2eRest;
                 // log2 of 2^r / e^target; a target's logit of -inf (or one that overflows in log2) leaves no term
                 const bool none = hi == -INFINITY;
@@ -303,15 +336,6 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const Span<const float> su
     }
 }
 
-// The tensor cores cut off, rather than round, what falls below the last place of
-// each of the dim / 16 sums on the way to a logit, which leaves it dim 2^-30 of
-// itself short in the mean: measured 0.39 to 0.53 (standard deviation 0.15 to
-// 0.37) times 2^-24 dim / 32 for dim 256 to 16384 over normal values, with and
-// without a common direction; 0.7 to 2.4 times where all products have one sign.  The
-// mean is given back in the factor of the exponent; without it every
-// log-sum-exp comes out low (1.2e-6 of the loss of one token at 32001 x 4096 where 2e-8 to 5e-7 are left).
-float head_log2e(int dim) { return (float)(1.4426950408889634 * (1.0 + dim * 0x1p-30)); }
-
 // ---- plan ------------------------------------------------------------------------------------
 
 // Bytes of one piece buffer.  Each piece adds to dh once and ends a launch, so few
@@ -324,7 +348,7 @@ constexpr int kPieceMin = 4096;
 
 struct HeadPlan {
     int row_cap, ld, parts, piece, pieces, splits, dh_ld;
-    int64_t off_state, off_row_of, off_at, off_target, off_tlogit, off_norm, off_block_loss, off_stats, off_h, off_w,
+    int64_t off_state, off_row_of, off_at, off_target, off_head_row, off_norm, off_block_loss, off_stats, off_h, off_w,
         off_p0, off_p1, off_dh, bytes;
 };
 
@@ -344,7 +368,7 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
     p.off_row_of = take(cap * 4);
     p.off_at = take(cap * 4);
     p.off_target = take(cap * 4);
-    p.off_tlogit = take(cap * 4);
+    p.off_head_row = take(cap * sizeof(HeadRow));
     p.off_norm = take(cap * sizeof(HeadNorm));
     p.off_block_loss = take(ceil_div(cap, kLseFew) * 4);
     p.off_stats = take((int64_t)p.parts * cap * 8);
@@ -408,7 +432,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     HeadState *state = reinterpret_cast<HeadState *>(c.ws + p.off_state);
     int *row_of = reinterpret_cast<int *>(c.ws + p.off_row_of), *at = reinterpret_cast<int *>(c.ws + p.off_at);
     int *target = reinterpret_cast<int *>(c.ws + p.off_target);
-    float *tlogit = reinterpret_cast<float *>(c.ws + p.off_tlogit);
+    HeadRow *head_row = reinterpret_cast<HeadRow *>(c.ws + p.off_head_row);
     HeadNorm *norm = reinterpret_cast<HeadNorm *>(c.ws + p.off_norm);
     uint16_t *hc = reinterpret_cast<uint16_t *>(c.ws + p.off_h);
     const uint16_t *w = static_cast<const uint16_t *>(c.w);
@@ -423,7 +447,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
                     head_rows_kernel<ID><<<blocks + (grad ? kPadBlocks : 0), kRowThreads, 0, c.st>>>(
                         static_cast<const ID *>(c.targets), c.ignore, tokens, vocab, c.mean, share, blocks,
                         static_cast<const uint16_t *>(c.h), w, c.dim, p.row_cap, h_vec, w_vec, state, row_of, at, target,
-                        hc, tlogit, c.row_loss, stage_flag_ptr()));
+                        hc, head_row, c.row_loss, stage_flag_ptr()));
     };
     if (c.id_bytes == 8) rows(int64_t{});
     else rows(int32_t{});
@@ -444,10 +468,9 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     g->vocab = vocab;
     g->dim = c.dim;
     g->row_cap = p.row_cap;
-    g->log2e = head_log2e(c.dim);
     g->state = state;
     g->target = target;
-    g->target_logit = tlogit;
+    g->rows = head_row;
     g->stats = reinterpret_cast<float2 *>(c.ws + p.off_stats);
     g->norm = norm;
     g->jobs = 1;
@@ -459,7 +482,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     auto *lse = lse_rows == kLseFew ? &head_lse_kernel<kLseFew> : &head_lse_kernel<kLseMany>;
     SPCO_LAUNCH("head_lse", c.st,
                 e = launch_dependent(lse, dim3(p.row_cap / lse_rows), dim3(kLseThreads), 0, c.st, g->stats, p.parts,
-                                     p.row_cap, tlogit, row_of, state, norm, c.row_loss,
+                                     p.row_cap, head_row, row_of, state, norm, c.row_loss,
                                      reinterpret_cast<float *>(c.ws + p.off_block_loss), c.loss));
     SPECOPTIM_CUDA(e);
     return SPECOPTIM_OK;

@@ -110,3 +110,83 @@ def test_head_probabilities_of_large_logits():
     assert torch.equal(got, want)
     onto = dw[target, torch.arange(n)].double() / large.double() * n
     assert bool(((onto + 511 / 512).abs() <= base.U16).all()) and bool(row_loss.isfinite().all())
+
+
+# ---------------------------------------------------------------- head: what a logit's sum may lose
+#
+# A row's logits other than the target's carry the tensor cores' truncation, of which the mean over normal values
+# (0.38 to 0.54 times UNIT(dim) of the logit) is given back as half a unit.
+
+def unit(dim):
+    return 2.0 ** -24 * dim / 32
+
+
+def loss_error(h, w, target):
+    """(error of row_loss, the float64 loss, lse, largest magnitude of a row's logits)."""
+    row = base.se().head_loss(h.cuda(), w.cuda(), target.cuda())[1].double()
+    logits = h.cuda().double() @ w.cuda().double().T
+    lse = torch.logsumexp(logits, 1)
+    want = lse - logits.gather(1, target.cuda()[:, None])[:, 0]
+    return (row - want).cpu(), want.cpu(), lse.cpu(), logits.abs().amax(1).cpu()
+
+
+@pytest.mark.parametrize("dim,held", [(4096, 1), (4096, 3), (65536, 1), (2056, 2)])
+@pytest.mark.parametrize("tokens", [40, 700])
+def test_head_keeps_exact_sums_of_a_few_values(tokens, dim, held):
+    # `held` values of h per token that are not 0, whole numbers of 8 bits in w: every sum is exact, so what is left are
+    # the exponents' factor (2^-24 of it, and 2^-26 per group of 16 values behind the first) and exp and log
+    g, vocab = base.gen(dim + held), 300
+    h, w = torch.zeros(tokens, dim, dtype=BF), torch.randint(-255, 256, (vocab, dim), generator=g).to(BF)
+    for _ in range(held):
+        h[torch.arange(tokens), torch.randint(0, dim, (tokens,), generator=g)] = 1.0
+    err, _, lse, most = loss_error(h, w, torch.randint(0, vocab, (tokens,), generator=g))
+    assert bool((err.abs() <= 2.0 ** -23 * most + 2.0 ** -22 * (lse.abs() + 8)).all()), float(err.abs().max())
+
+
+@pytest.mark.parametrize("dim", [2048, 4096])
+def test_head_bounds_the_error_of_exact_dense_sums(dim):
+    g, tokens, vocab = base.gen(dim), 200, 300
+    h = torch.randint(-3, 4, (tokens, dim), generator=g).to(BF)
+    w = (torch.randint(-2, 3, (vocab, dim), generator=g) * 0.5).to(BF)
+    err, _, lse, most = loss_error(h, w, torch.randint(0, vocab, (tokens,), generator=g))
+    assert bool((err.abs() <= (unit(dim) / 2 + 2.0 ** -23) * most + 2.0 ** -22 * (lse.abs() + 8)).all())
+
+
+@pytest.mark.parametrize("dim", [2048, 4096])
+@pytest.mark.parametrize("common", [True, False])
+def test_head_gives_the_mean_truncation_back(dim, common):
+    # common: all rows of w point the same way, so that all logits of a token are near one another and the loss shows
+    # the truncation of their common part; otherwise one logit of size 50 stands out over 0s
+    g, tokens, vocab = base.gen(dim), 2048, 512
+    r = torch.randn(dim, generator=g)
+    h = torch.randn(tokens, dim, generator=g)
+    if common:
+        r *= 20 / dim ** 0.5
+        h += 2.5 * r / r.norm()
+        w = (r + 0.02 * torch.randn(vocab, dim, generator=g)).to(BF)
+        target = torch.randint(0, vocab, (tokens,), generator=g)
+    else:
+        w = torch.zeros(vocab, dim, dtype=BF)
+        w[1] = r * 60 / dim ** 0.5
+        target = torch.zeros(tokens, dtype=torch.int64)
+    h = h.to(BF)
+    err, want, lse, _ = loss_error(h, w, target)
+    rows = lse > 25
+    assert int(rows.sum()) > 500
+    rel = (err / lse)[rows] / unit(dim)
+    # the mean: 0.12 units, and four deviations of 0.4 / sqrt(rows); a missing or doubled factor leaves 0.4 or more
+    assert abs(float(rel.mean())) <= 0.12 + 1.6 / int(rows.sum()) ** 0.5
+    assert float(rel.square().mean().sqrt()) <= 0.5
+
+
+def test_head_loss_of_well_predicted_tokens_keeps_its_digits():
+    # the target's logit is 8 to 60, the 599 others 0: loss = log(1 + 599 e^-l), down to 5e-24
+    vocab, tokens = 600, 14
+    h, w = torch.zeros(tokens, 64, dtype=BF), torch.zeros(vocab, 64, dtype=BF)
+    h[:, 0], w[5, 0] = torch.arange(8, 64, 4).to(BF), 1.0
+    row, dw = [base.se().head_loss_grad(h.cuda(), w.cuda(), torch.full((tokens,), 5).cuda(), reduction="sum")[i].cpu().double()
+               for i in (1, 3)]
+    want = torch.log1p(599 * torch.exp(-h[:, 0].double()))
+    # the exponent is off by 2^-23 of the logit at most, exp, log1p and the sum of 600 terms by 2^-20
+    assert bool(((row / want - 1).abs() <= 2.0 ** -23 * h[:, 0].double() + 2.0 ** -20).all())
+    assert abs(float(dw[5, 0]) / float(-((1 - torch.exp(-want)) * h[:, 0].double()).sum()) - 1) <= base.U16
