@@ -183,7 +183,7 @@ __device__ __forceinline__ void fill_rows(const Fill &f, int64_t group, const bo
 }
 
 // the rows that have a token by the map of them
-__device__ __forceinline__ void fill_by_map(const Fill &f, int64_t group, const uint32_t *__restrict__ map) {
+__device__ __forceinline__ void fill_by_map(const Fill &f, int64_t group, const uint32_t *map) {
     __shared__ bool present[kZeroRows];
     const int64_t row0 = (f.first + group) * kZeroRows;
     for (int i = threadIdx.x; i < kZeroRows; i += blockDim.x)
@@ -260,11 +260,12 @@ __device__ __forceinline__ void sort_tile(SortShared &sh, const ID *ids, int64_t
     for (int b = tid; b < kSortWarps * kBins; b += kSortThreads) (&sh.where[0][0])[b] = 0;
     __syncthreads();
     const int64_t base = tile * kTile + w * kWarpItems;
-    uint32_t key[kWarpItems / 32];
+    uint32_t key[kWarpItems / 32], val[kWarpItems / 32];
 #pragma unroll
     for (int i = 0; i < kWarpItems / 32; ++i) {
         const int64_t t = base + i * 32 + lane;
         key[i] = t < n ? (FIRST ? key_of(ids, t, vocab, padding, flag) : keys[t]) : 0u;
+        val[i] = FIRST || t >= n ? (uint32_t)t : vals[t];
         if (t < n) atomicAdd(&sh.where[w][(key[i] >> shift) & (kBins - 1)], 1u);
     }
     __syncthreads();
@@ -308,7 +309,7 @@ __device__ __forceinline__ void sort_tile(SortShared &sh, const ID *ids, int64_t
         if (in) {
             const uint32_t to = sh.where[w][d] + __popc(peers & ((1u << lane) - 1u));
             keys_out[to] = key[i];
-            vals_out[to] = FIRST ? (uint32_t)t : vals[t];
+            vals_out[to] = val[i];
             if (next_hist)
                 atomicAdd(&next_hist[(int64_t)(to / kTile) * kBins + ((key[i] >> (shift + kBits)) & (kBins - 1))], 1u);
         }
@@ -322,10 +323,10 @@ __device__ __forceinline__ void sort_tile(SortShared &sh, const ID *ids, int64_t
 // scan kernel of its own would cost a launch).
 template <typename ID, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(
-    const ID *__restrict__ ids, int64_t vocab, int64_t padding, const uint32_t *__restrict__ keys,
-    const uint32_t *__restrict__ vals, int64_t n, int shift, const uint32_t *__restrict__ hist, int blocks,
+    const ID *ids, int64_t vocab, int64_t padding, const uint32_t *keys,
+    const uint32_t *vals, int64_t n, int shift, const uint32_t *hist, int blocks,
     uint32_t *__restrict__ keys_out, uint32_t *__restrict__ vals_out, uint32_t *__restrict__ next_hist,
-    uint32_t *__restrict__ clear_hist, const Fill fill, const uint32_t *__restrict__ map) {
+    uint32_t *__restrict__ clear_hist, const Fill fill, const uint32_t *map) {
     // beside a fill the successor's blocks would wait in slots that the fill can use (+6 us on 65536 x 2048)
     if ((int)gridDim.x == blocks) grid_dependency_launch();
     grid_dependency_wait();
@@ -410,7 +411,7 @@ __device__ __forceinline__ void put_row(const Span<TG> &grad, int64_t row, int d
     const int64_t from = grad.lo + row * dim, at = from + j * 8 - phase<TG, VEC>(grad, row, dim);
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] *= scale;
-    if (accumulate) {  // nobody else writes these values, so the read-only path is safe
+    if (accumulate) {
         float old[8];
         if (VEC) load8(static_cast<const TG *>(grad.p) + at, old);
         else load_any(grad.read(), at, old);
@@ -431,7 +432,7 @@ template <typename TD, typename TG, bool VEC>
 __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const Span<const TD> dy, int64_t vocab,
                                                           int dim, int col_blocks, float scale, bool accumulate,
                                                           const Span<TG> grad, float *__restrict__ partial, int pitch,
-                                                          const Fill fill, const uint32_t *__restrict__ map) {
+                                                          const Fill fill, const uint32_t *map) {
     __shared__ uint32_t sk[kMaxChunk + 2], sv[kMaxChunk];
     if (s.chunks * col_blocks == (int64_t)gridDim.x) grid_dependency_launch();
     grid_dependency_wait();
@@ -463,8 +464,8 @@ __global__ void __launch_bounds__(256) segment_sum_kernel(const Sorted s, const 
         for (int u = 0; u < kBatch; ++u) {
             if (i0 + u >= len) continue;
             const int64_t at = dy.lo + (int64_t)sv[i0 + u] * dim + j * 8 - phase<TG, VEC>(grad, sk[i0 + u + 1], dim);
-            if (VEC) load8(dy.p + at, x[u]);
-            else load_any(dy, at, x[u]);
+            if (VEC) load8<kLasting>(dy.p + at, x[u]);
+            else load_any<kLasting>(dy, at, x[u]);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -494,8 +495,8 @@ template <typename TG, bool VEC>
 __global__ void __launch_bounds__(256) segment_join_kernel(const Sorted s, int64_t vocab, int dim, int col_blocks,
                                                            int threads,
                                                            float scale, bool accumulate, const Span<TG> grad,
-                                                           const float *__restrict__ partial, int pitch,
-                                                           const Fill fill, const uint32_t *__restrict__ map) {
+                                                           const float *partial, int pitch,
+                                                           const Fill fill, const uint32_t *map) {
     grid_dependency_wait();
     const int64_t joins = s.chunks * col_blocks;
     if ((int64_t)blockIdx.x >= joins) {

@@ -232,9 +232,9 @@ __device__ __forceinline__ void join(float &m, float &s, float2 x) {
 // and 1002 parts where 8 take 49.
 constexpr int kLseThreads = 1024, kLseFew = 8, kLseMany = 32;
 template <int ROWS>
-__global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *__restrict__ stats, int parts, int row_cap,
-                                                       const HeadRow *__restrict__ head_row,
-                                                       const int *__restrict__ row_of, HeadState *state,
+__global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *stats, int parts, int row_cap,
+                                                       const HeadRow *head_row,
+                                                       const int *row_of, HeadState *state,
                                                        HeadNorm *__restrict__ norm, float *__restrict__ row_loss,
                                                        float *__restrict__ block_loss, float *__restrict__ loss) {
     constexpr int LANES = kLseThreads / ROWS;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *__r
 // The sums' rows are read from where dh's 16-byte pieces begin (VEC: column 0).
 template <bool VEC>
 __global__ void __launch_bounds__(256) head_dh_kernel(const Span<const float> sums, int parts, int row_cap, int ld,
-                                                      const int *__restrict__ at, const HeadState *__restrict__ state,
+                                                      const int *at, const HeadState *state,
                                                       float grad_scale, int tokens, int dim, const Span<bf16> dh) {
     grid_dependency_wait();
     const float factor = grad_scale * state->inv_count;

@@ -139,7 +139,7 @@ template <int ROWS, typename T> __device__ __forceinline__ Raw8<T> load_raw(cons
     if (ROWS == ROWS_VEC || (ROWS == ROWS_ODD && i + 8 <= s.hi)) {
         const uint4 *q = reinterpret_cast<const uint4 *>(s.p + i);
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.a[k] = __ldg(q + k);
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.a[k] = q[k];  // plain: the call may be writing in place
     } else {
         float v[8];
         if (ROWS == ROWS_ANY) {
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) resnorm_backward
 
 // dgamma[j] = sum over blocks of partial[block][j]: 32 columns per block, 32
 // threads per column, joined in a fixed order.
-__global__ void __launch_bounds__(1024) dgamma_kernel(const float *__restrict__ partial, int blocks, int dim,
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float *partial, int blocks, int dim,
                                                       int pitch, float *__restrict__ dgamma) {
     __shared__ float red[32][33];
     grid_dependency_wait();

@@ -40,14 +40,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Loads are plain ones, not read-only: callers read what the launch before them wrote while
+// they were resident already, and pieces of which other threads write their own part (in-place
+// calls, sums that are added to).  kLasting: nobody writes the tensor while the kernel is
+// resident, so loads may be moved ahead of the kernel's stores (65536 rows of dy summed by id:
+// 248 us with, 341 without).
+constexpr bool kLasting = true;
+template <bool LASTING, typename V> __device__ __forceinline__ V load_piece(const V *p) { return LASTING ? __ldg(p) : *p; }
+
 // p[0..7] of a 16-byte aligned address
-__device__ __forceinline__ void load8(const bf16 *p, float (&v)[8]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+template <bool LASTING = false> __device__ __forceinline__ void load8(const bf16 *p, float (&v)[8]) {
+    const uint4 u = load_piece<LASTING>(reinterpret_cast<const uint4 *>(p));
     v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
     v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
 }
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+template <bool LASTING = false> __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 *q = reinterpret_cast<const float4 *>(p);
+    const float4 a = load_piece<LASTING>(q), b = load_piece<LASTING>(q + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 __device__ __forceinline__ void store8(bf16 *p, const float (&v)[8]) {
@@ -85,15 +94,16 @@ __device__ __forceinline__ void pick_words(const uint32_t (&w)[8], int o, uint32
 }
 
 // values i .. i + 7 of the span; 0 outside it
+template <bool LASTING = false>
 __device__ __forceinline__ void load_any(const Span<const bf16> &s, int64_t i, float (&v)[8]) {
     const int64_t a = i & ~(int64_t)7;
     const int sh = (int)(i & 7);
     if (a >= s.lo && a + (sh ? 16 : 8) <= s.hi) {
         const uint4 *q = reinterpret_cast<const uint4 *>(s.p + a);
-        const uint4 x = __ldg(q);
+        const uint4 x = load_piece<LASTING>(q);
         uint32_t r[5] = {x.x, x.y, x.z, x.w, 0};
         if (sh) {
-            const uint4 y = __ldg(q + 1);
+            const uint4 y = load_piece<LASTING>(q + 1);
             const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
             pick_words(w, sh >> 1, r);
         }
@@ -108,15 +118,16 @@ __device__ __forceinline__ void load_any(const Span<const bf16> &s, int64_t i, f
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = i + k >= s.lo && i + k < s.hi ? to_f(s.p[i + k]) : 0.f;
 }
+template <bool LASTING = false>
 __device__ __forceinline__ void load_any(const Span<const float> &s, int64_t i, float (&v)[8]) {
     const int64_t a = i & ~(int64_t)3;
     const int sh = (int)(i & 3);
     if (a >= s.lo && a + (sh ? 12 : 8) <= s.hi) {
         const float4 *q = reinterpret_cast<const float4 *>(s.p + a);
-        const float4 x = __ldg(q), y = __ldg(q + 1);
+        const float4 x = load_piece<LASTING>(q), y = load_piece<LASTING>(q + 1);
         float w[12] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, 0.f, 0.f, 0.f, 0.f};
         if (sh) {
-            const float4 z = __ldg(q + 2);
+            const float4 z = load_piece<LASTING>(q + 2);
             w[8] = z.x; w[9] = z.y; w[10] = z.z; w[11] = z.w;
         }
         float t[10];
@@ -135,9 +146,9 @@ __device__ __forceinline__ uint2 load_any8(const Span<const uint8_t> &s, int64_t
     const int sh = (int)(i & 7);
     if (a >= s.lo && a + (sh ? 16 : 8) <= s.hi) {
         const uint2 *q = reinterpret_cast<const uint2 *>(s.p + a);
-        const uint2 x = __ldg(q);
+        const uint2 x = q[0];
         if (!sh) return x;
-        const uint2 y = __ldg(q + 1);
+        const uint2 y = q[1];
         const uint32_t w0 = (sh & 4) ? x.y : x.x, w1 = (sh & 4) ? y.x : x.y, w2 = (sh & 4) ? y.y : y.x;
         return make_uint2(__funnelshift_r(w0, w1, 8 * (sh & 3)), __funnelshift_r(w1, w2, 8 * (sh & 3)));
     }

@@ -190,3 +190,44 @@ def test_head_loss_of_well_predicted_tokens_keeps_its_digits():
     # the exponent is off by 2^-23 of the logit at most, exp, log1p and the sum of 600 terms by 2^-20
     assert bool(((row / want - 1).abs() <= 2.0 ** -23 * h[:, 0].double() + 2.0 ** -20).all())
     assert abs(float(dw[5, 0]) / float(-((1 - torch.exp(-want)) * h[:, 0].double()).sum()) - 1) <= base.U16
+
+
+# ---------------------------------------------------------------- residual norm in place
+
+def entry(name, *args):
+    """A C entry point called on the current stream, tensors as their pointers."""
+    import spectral_corrected_optimizer_gb300 as so
+    ptr = lambda a: a.data_ptr() if isinstance(a, torch.Tensor) else a  # noqa: E731
+    so._check(getattr(so.lib(), name)(*map(ptr, args), torch.cuda.current_stream().cuda_stream), name)
+
+
+# rows: more than blocks; widths: one, two (a ring of rows in the backward pass), eight and nine pieces per thread
+@pytest.mark.parametrize("rows,dim", [(10000, 64), (10000, 67), (1300, 2048), (1300, 2051), (700, 8200), (330, 16400),
+                                      (330, 16403), (160, 32766)])
+@pytest.mark.parametrize("by", [0, 1])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_norm_in_place(rows, dim, by, dtype):
+    g, op = torch.Generator("cuda").manual_seed(rows + dim), base.se()
+    code, eps = (0 if dtype == BF else 1), 1e-5
+    x, r, dy, ds = [base.shifted(torch.randn(rows, dim, generator=g, device="cuda").to(dtype), by) for _ in range(4)]
+    gamma = base.shifted(torch.randn(dim, generator=g, device="cuda").to(dtype), by)
+    q = base.shifted(torch.zeros(rows, dim, dtype=torch.uint8), by)
+    y, scale, rstd = torch.empty_like(x), torch.empty(rows, -(-dim // 128), device="cuda"), torch.empty(rows, device="cuda")
+    kept, s, want_y = op.residual_norm(x, r, gamma, eps)
+    for over in (0, 1):
+        pair = [base.shifted(t, by) for t in (x, r)]
+        entry("resnorm_forward", *pair, gamma, code, eps, pair[over], y, q, scale, rstd, rows, dim)
+        assert torch.equal(pair[over], s) and torch.equal(pair[1 - over], (x, r)[1 - over]) and torch.equal(y, want_y)
+        assert torch.equal(q, kept.q.view(torch.uint8)) and torch.equal(scale, kept.scale) and torch.equal(rstd, kept.rstd)
+    import spectral_corrected_optimizer_gb300 as so
+    ws = torch.empty(so.lib().resnorm_backward_workspace(rows, dim), dtype=torch.uint8, device="cuda")
+
+    def backward(dy, ds, dx):  # dx begins where dy and ds do: its place decides how a row's sums are grouped
+        dgamma = torch.empty(dim, device="cuda")
+        entry("resnorm_backward", dy, ds, q, scale, rstd, gamma, code, dx, dgamma, y, rows, dim, ws, ws.numel())
+        return dx, dgamma, y.clone()
+
+    want = backward(dy, ds, base.shifted(torch.zeros_like(x), by))
+    for over in (0, 1):
+        pair = [base.shifted(t, by) for t in (dy, ds)]
+        assert all(torch.equal(a, b) for a, b in zip(backward(*pair, pair[over]), want))
