@@ -231,3 +231,39 @@ def test_norm_in_place(rows, dim, by, dtype):
     for over in (0, 1):
         pair = [base.shifted(t, by) for t in (dy, ds)]
         assert all(torch.equal(a, b) for a, b in zip(backward(*pair, pair[over]), want))
+
+
+# ---------------------------------------------------------------- embedding gradient: long lists, large vocabularies
+
+@pytest.mark.parametrize("tokens,vocab,dim,passes", [(5000, 300, 8, 1), (70000, 200000, 16, 2), (70000, 300000, 16, 3),
+                                                     (262144 + 5, 300000, 8, 3), (1200001, 1000, 3, 2),
+                                                     (1200001, 300000, 8, 3), (300000, 2 ** 27 + 3, 1, 4)])
+def test_embed_grad_of_many_tiles_and_passes(tokens, vocab, dim, passes):
+    # several tiles of 2048 tokens, 9 bits of the ids a pass; from 128 tiles on their counts are scanned by a launch
+    assert (vocab.bit_length() + 8) // 9 == passes
+    g = base.gen(tokens + vocab)
+    ids = torch.where(torch.rand(tokens, generator=g) < 0.5, base.zipf(g, tokens, vocab),
+                      torch.randint(0, vocab, (tokens,), generator=g))
+    dy = base.randn(g, (tokens, dim), BF)
+    grad = base.se().embed_grad(ids.cuda(), dy.cuda(), vocab)
+    some, at = ids.unique(return_inverse=True)
+    base.check_grad(grad[some.cuda()], at, dy, len(some), 1.0)
+    grad[some.cuda()] = 0
+    assert not bool(grad.any())
+
+
+def test_embed_grad_grows_with_the_tokens_not_with_their_square():
+    def best(tokens):
+        ids = torch.randint(0, 5000, (tokens,), device="cuda")
+        dy, out = torch.ones(tokens, 1, dtype=BF, device="cuda"), torch.empty(5000, 1, device="cuda")
+        times = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            base.se().embed_grad(ids, dy, 5000, out=out)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    # 32 times the tokens; with a pass that grew with their square it was over 90 times the time
+    assert best(2 ** 25) < 50 * best(2 ** 20)
