@@ -74,12 +74,28 @@ __device__ __forceinline__ int blocks_of(uint4 a) {
 
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 
+__device__ __forceinline__ bool has_target(int64_t id, int64_t ignore, int vocab) {
+    return id != ignore && id >= 0 && id < vocab;
+}
+
+// Targets among each kStretch neighbouring tokens.
+constexpr int kStretch = 4096;
+template <typename ID>
+__global__ void __launch_bounds__(kRowThreads) head_count_kernel(const ID *__restrict__ targets, int64_t ignore,
+                                                                 int vocab, int *__restrict__ counts) {
+    const ID *from = targets + (int64_t)blockIdx.x * kStretch;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kStretch; i += kRowThreads) n += __syncthreads_count(has_target((int64_t)from[i + threadIdx.x], ignore, vocab));
+    if (threadIdx.x == 0) counts[blockIdx.x] = n;
+}
+
 // Lists the tokens with a target in token order (row_of[r] = token of row r,
 // at[t] = row of token t or -1, target[r]) and copies their rows of h together,
 // in column blocks of 64 (zero behind dim).  Each block takes `share`
 // neighbouring tokens (at most one per thread), counts the targets in front of
 // them itself -- the ids come from L2, a kernel of its own for the list would
-// cost more -- and then copies its rows, a warp per row.  The last block appends the
+// cost more; behind many tokens whole stretches are counted by one (counts) -- and then copies its rows, a warp per row.  The last block appends the
 // zero rows up to the next multiple of the tile height.
 //
 // On the way the logit of each row's target is formed as an fp32 dot product:
@@ -88,7 +104,7 @@ constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kPadBlocks = 8;
 template <typename ID>
 __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__restrict__ targets, int64_t ignore, int tokens,
-                                                        int vocab, int mean, int share, int own_blocks,
+                                                        int vocab, int mean, int share, int own_blocks, const int *counts,
                                                         const uint16_t *__restrict__ h,
                                                         const uint16_t *__restrict__ w, int dim, int row_cap, int h_vec,
                                                         int w_vec, HeadState *state, int *__restrict__ row_of,
@@ -102,15 +118,19 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int pad = (int)blockIdx.x - own_blocks;  // >= 0: a block of zero rows, which counts all targets
     const int t0 = pad >= 0 ? tokens : (int)blockIdx.x * share, t1 = min(t0 + share, tokens);
-    auto usable = [&](int64_t id) { return id != ignore && id >= 0 && id < vocab; };
-    int before = 0;
+    int before = 0, first = 0;  // tokens in front of `first` are in counts
+    if (counts) {
+        const int whole = t0 / kStretch;
+        for (int i = threadIdx.x; i < whole; i += kRowThreads) before += counts[i];
+        first = whole * kStretch;
+    }
 #pragma unroll 4
-    for (int t = threadIdx.x; t < t0; t += kRowThreads) before += usable((int64_t)targets[t]);
+    for (int t = first + threadIdx.x; t < t0; t += kRowThreads) before += has_target((int64_t)targets[t], ignore, vocab);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     const int t = t0 + threadIdx.x;
     const int64_t id = t < t1 ? (int64_t)targets[t] : ignore;
-    const bool has = usable(id);
+    const bool has = has_target(id, ignore, vocab);
     if (id != ignore && !has) atomicExch(flag, kSiteTarget);
     const unsigned ballot = __ballot_sync(0xffffffffu, has);
     if (lane == 0) {
@@ -348,7 +368,7 @@ constexpr int kPieceMin = 4096;
 
 struct HeadPlan {
     int row_cap, ld, parts, piece, pieces, splits, dh_ld;
-    int64_t off_state, off_row_of, off_at, off_target, off_head_row, off_norm, off_block_loss, off_stats, off_h, off_w,
+    int64_t off_state, off_counts, off_row_of, off_at, off_target, off_head_row, off_norm, off_block_loss, off_stats, off_h, off_w,
         off_p0, off_p1, off_dh, bytes;
 };
 
@@ -365,6 +385,7 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
     };
     const int64_t cap = p.row_cap;
     p.off_state = take(sizeof(HeadState));
+    p.off_counts = take(tokens / kStretch * 4);
     p.off_row_of = take(cap * 4);
     p.off_at = take(cap * 4);
     p.off_target = take(cap * 4);
@@ -426,6 +447,11 @@ int check_call(const HeadCall &c, const HeadPlan &p, const std::string &what) {
     return SPECOPTIM_OK;
 }
 
+// From so many tokens on their targets are counted in stretches first; below, each block counts
+// all of those in front of it, which grows with the square of the tokens but saves the launch (width
+// 8, listing / count + listing: 32768 tokens 22 / 6 + 15 us, 65536 35 / 7 + 22, 2^20 1056 / 8 + 207).
+constexpr int kCountTokens = 1 << 16;
+
 // Steps 1 and 2: afterwards loss, row_loss and the rows' norms exist.
 int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     std::memset(g, 0, sizeof(*g));
@@ -441,11 +467,16 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     const int share = std::max(1, std::min(kRowThreads, tokens / (num_sms() * 4)));
     const int blocks = (int)std::max<int64_t>(1, ceil_div(tokens, share));
     const bool w_vec = c.dim % 8 == 0, h_vec = w_vec && aligned16(c.h);
+    int *counts = tokens >= kCountTokens ? reinterpret_cast<int *>(c.ws + p.off_counts) : nullptr;
     auto rows = [&](auto id) {
         using ID = decltype(id);
+        if (counts)
+            SPCO_LAUNCH("head_count", c.st,
+                        head_count_kernel<ID><<<tokens / kStretch, kRowThreads, 0, c.st>>>(
+                            static_cast<const ID *>(c.targets), c.ignore, vocab, counts));
         SPCO_LAUNCH("head_rows", c.st,
                     head_rows_kernel<ID><<<blocks + (grad ? kPadBlocks : 0), kRowThreads, 0, c.st>>>(
-                        static_cast<const ID *>(c.targets), c.ignore, tokens, vocab, c.mean, share, blocks,
+                        static_cast<const ID *>(c.targets), c.ignore, tokens, vocab, c.mean, share, blocks, counts,
                         static_cast<const uint16_t *>(c.h), w, c.dim, p.row_cap, h_vec, w_vec, state, row_of, at, target,
                         hc, head_row, c.row_loss, stage_flag_ptr()));
     };

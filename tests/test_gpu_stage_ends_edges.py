@@ -267,3 +267,39 @@ def test_embed_grad_grows_with_the_tokens_not_with_their_square():
         return min(times)
     # 32 times the tokens; with a pass that grew with their square it was over 90 times the time
     assert best(2 ** 25) < 50 * best(2 ** 20)
+
+
+# ---------------------------------------------------------------- head: many tokens
+
+@pytest.mark.parametrize("tokens", [65535, 65536, 70001, 150000])
+@pytest.mark.parametrize("idt", [torch.int64, torch.int32])
+def test_head_of_many_tokens(tokens, idt):
+    # from 65536 tokens on a launch of its own counts the targets of whole stretches of 4096
+    g, vocab, dim = base.gen(tokens), 40, 8
+    h, w = base.randn(g, (tokens, dim), BF), base.randn(g, (vocab, dim), BF)
+    target = torch.randint(0, vocab, (tokens,), generator=g, dtype=idt)
+    target[torch.rand(tokens, generator=g) < 0.3] = -100
+    target[4096:12288] = -100
+    loss, row_loss, dh, dw = base.se().head_loss_grad(h.cuda(), w.cuda(), target.cuda())
+    want = ref.head(h, w, target)
+    base.check_loss(loss, row_loss, want, dim)
+    base.check_grads(dh, dw, want, h, w)
+    only = base.se().head_loss(h.cuda(), w.cuda(), target.cuda())
+    assert torch.equal(only[0], loss) and torch.equal(only[1], row_loss)
+
+
+def test_head_grows_with_the_tokens_not_with_their_square():
+    def best(tokens):
+        target = torch.randint(0, 8, (tokens,), device="cuda")
+        h, w = torch.ones(tokens, 8, dtype=BF, device="cuda"), torch.ones(8, 8, dtype=BF, device="cuda")
+        times = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            base.se().head_loss(h, w, target)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    # 32 times the tokens; counting targets with their square it was over 200 times the time
+    assert best(2 ** 23) < 50 * best(2 ** 18)
