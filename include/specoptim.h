@@ -266,9 +266,11 @@ int specoptim_selftest_wait_timeout(uint32_t spin_limit, void *stream);
 
 /* Synchronises `stream` and reports whether a bounded device-side wait of any
  * of the library's kernels (the asynchronous calls of this header, of
- * mask_fused.h and of dpsync.h) gave up since the last check:
+ * mask_fused.h, of dpsync.h and of stage_ends.h) gave up since the last check:
  * SPECOPTIM_ERR_TIMEOUT (the flag is cleared; the results of the kernels
  * launched since the last check are not to be trusted) or SPECOPTIM_OK.
+ * SPECOPTIM_ERR_BOUNDS reports, once, that a call of stage_ends.h skipped a
+ * token id or target outside the vocabulary.
  * A library built with -DSPECOPTIM_CHECK (a test build) also verifies, in the
  * mask kernels, that every kept index is below H; a failure skips the access
  * and is reported here as SPECOPTIM_ERR_BOUNDS. */

@@ -313,7 +313,8 @@ def gemm_nt(A, B, precision: int = PREC_TF32, out=None, stream=None):
 
 
 def check_device(stream=None):
-    """Synchronise the stream; raise if a bounded device-side wait of the library gave up."""
+    """Synchronise the stream; raise if a bounded device-side wait of the library gave up,
+    or if a token id or target outside the vocabulary was skipped."""
     _check(lib().specoptim_check_device(_stream(stream)), "specoptim_check_device")
 
 

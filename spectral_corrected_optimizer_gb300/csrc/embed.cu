@@ -42,13 +42,27 @@ unsigned *stage_flag_ptr() {
     return ptr;
 }
 
+// The calling thread's page-locked word: a copy into it does not hold the host up.
+static unsigned *host_word() {
+    static thread_local unsigned *word = nullptr;
+    if (!word) {
+        void *p = nullptr;
+        if (cudaMallocHost(&p, sizeof(unsigned)) == cudaSuccess) word = static_cast<unsigned *>(p);
+    }
+    return word;
+}
+
+int read_stage_flag(cudaStream_t st) {
+    unsigned *p = stage_flag_ptr(), *v = host_word();
+    if (!p || !v) return fail(SPECOPTIM_ERR_CUDA, "no memory for the flag of token ids");
+    SPECOPTIM_CUDA(cudaMemcpyAsync(v, p, sizeof(*v), cudaMemcpyDeviceToHost, st));
+    return SPECOPTIM_OK;
+}
+
 int check_stage_flag(cudaStream_t st) {
-    unsigned *p = stage_flag_ptr(), v = 0;
-    if (!p) return SPECOPTIM_OK;
-    SPECOPTIM_CUDA(cudaMemcpyAsync(&v, p, sizeof(v), cudaMemcpyDeviceToHost, st));
-    SPECOPTIM_CUDA(cudaStreamSynchronize(st));
+    const unsigned v = *host_word();
     if (!v) return SPECOPTIM_OK;
-    SPECOPTIM_CUDA(cudaMemsetAsync(p, 0, sizeof(v), st));
+    SPECOPTIM_CUDA(cudaMemsetAsync(stage_flag_ptr(), 0, sizeof(v), st));
     SPECOPTIM_CUDA(cudaStreamSynchronize(st));
     return fail(SPECOPTIM_ERR_BOUNDS, v == kSiteTokenId ? "a token id lies outside the vocabulary"
                                                         : "a target lies outside the vocabulary");

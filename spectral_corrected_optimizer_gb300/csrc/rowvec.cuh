@@ -22,7 +22,7 @@ namespace spco {
 using bf16 = __nv_bfloat16;
 
 // What a kernel writes to the stage-end operators' device flag when it skips an
-// id outside the vocabulary; check_stage_flag() (embed.cu) reads and clears it.
+// id outside the vocabulary; read_stage_flag() and check_stage_flag() (embed.cu) read and clear it.
 constexpr unsigned kSiteTokenId = 1, kSiteTarget = 2;
 unsigned *stage_flag_ptr();
 

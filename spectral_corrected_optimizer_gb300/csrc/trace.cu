@@ -45,7 +45,10 @@ void recycle_all() {
 
 }  // namespace
 
-int check_stage_flag(cudaStream_t st);  // embed.cu
+// embed.cu: read_stage_flag() begins a copy of the flag, check_stage_flag() looks at it
+// once the stream is synchronised
+int read_stage_flag(cudaStream_t st);
+int check_stage_flag(cudaStream_t st);
 
 int trace_begin(const char *name, cudaStream_t st) {
     g_launches.fetch_add(1, std::memory_order_relaxed);
@@ -144,7 +147,9 @@ extern "C" int specoptim_selftest_wait_timeout(uint32_t spin_limit, void *stream
 extern "C" int specoptim_check_device(void *stream) {
     clear_error();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (int rc = check_device_flag(st)) return rc;
+    if (int rc = bind_device()) return rc;
+    if (int rc = read_stage_flag(st)) return rc;
+    if (int rc = check_device_flag(st)) return rc;  // synchronises the stream
     return check_stage_flag(st);
 }
 

@@ -303,3 +303,43 @@ def test_head_grows_with_the_tokens_not_with_their_square():
         return min(times)
     # 32 times the tokens; counting targets with their square it was over 200 times the time
     assert best(2 ** 23) < 50 * best(2 ** 18)
+
+
+# ---------------------------------------------------------------- reports
+
+def test_check_device_costs_little_more_than_one_read():
+    import time
+
+    import spectral_corrected_optimizer_gb300 as so
+
+    def best(f):
+        times = []
+        for _ in range(400):
+            t = time.perf_counter()
+            f()
+            times.append(time.perf_counter() - t)
+        return min(times)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    # both flags in one synchronisation: 1.3 reads of a word; one after the other they took 2
+    assert best(so.check_device) < 1.7 * best(word.item)
+
+
+def test_reports_of_ids_come_once_and_in_any_thread():
+    import threading
+
+    import spectral_corrected_optimizer_gb300 as so
+    table, ids = torch.ones(4, 8, device="cuda"), torch.tensor([9], device="cuda")
+    errors = []
+
+    def check():
+        try:
+            so.check_device()
+        except so.SpecOptimError as e:
+            errors.append(e.code)
+    for _ in range(2):
+        base.se().embed_lookup(table, ids)
+        torch.cuda.synchronize()
+        for t in [threading.Thread(target=check) for _ in range(3)]:
+            t.start()
+            t.join()
+    assert errors == [so.ERR_BOUNDS] * 2
