@@ -31,7 +31,8 @@
 // A logits tile takes at least 2.2 us, its epilogue's time, and 0.6 us of its own beside
 // 0.35 us per 64 k: narrow layers are bound by that (3974 x 112636 x 200: 212 us).
 //
-// Every wait on an mbarrier is bounded, as in gemm_tc.cu.
+// Every wait on an mbarrier is bounded; where one gives up, a pair waits, again with a
+// limit, for its loads and MMAs in flight before it frees TMEM and leaves.
 #include <algorithm>
 #include <cstring>
 #include <mutex>
@@ -57,6 +58,7 @@ constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr uint32_t OUT_BYTES = 32 * 128;  // one warp's block of 32 rows on its way out
 constexpr size_t SMEM_BYTES = (size_t)STAGES * STAGE_BYTES + EPI_WARPS * OUT_BYTES + 1024 + 256;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
+constexpr uint32_t kDrainLimit = 1u << 14;  // probes of up to 4 us, for what takes microseconds
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -453,7 +455,8 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
     uint64_t *empty = full + STAGES;                                             // each CTA's own
     uint64_t *tfull = empty + STAGES;                                            // each CTA's own
     uint64_t *tempty = tfull + 2;                                                // rank 0's: both CTAs' epilogues
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
+    uint64_t *drained = tempty + 2;                                              // all MMAs of the pair are done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = (int)cluster_rank();
     if (threadIdx.x == 0) {
@@ -465,6 +468,7 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
             mbar_init(&tfull[a], 1);
             mbar_init(&tempty[a], 2 * EPI_WARPS);
         }
+        mbar_init(drained, 1);
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc_pair(tmem_slot, TMEM_COLS);
@@ -527,6 +531,12 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
                 }
             }
         }
+        // Given up: the loads of the last stages may be on their way.  Rank 0's barriers count
+        // both CTAs'; a stage that the other CTA filled alone never completes and the wait for it is
+        // the time that its loads have to land.
+        if (!ok && rank == 0)
+            for (uint32_t j = it < (uint32_t)STAGES ? 0 : it - STAGES; j <= it; ++j)
+                mbar_wait_limit(&full[j % STAGES], (j / STAGES) & 1u, nullptr, 0u, kDrainLimit);
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---------------- MMA issuer of the pair
         // The tensor core takes 128 cycles for an MMA of 16 k, so what this thread does per
@@ -565,6 +575,9 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
             }
             mma_commit_pair(&tfull[acc]);
         }
+        // usually long done (the epilogues wait for the last tile)
+        mma_commit_pair(drained);
+        mbar_wait_limit(drained, 0, nullptr, 0u, kDrainLimit);
     } else if (warp >= 2) {
         // ---------------- epilogue of this CTA's rows
         const int q = warp % 4;           // TMEM lane quarter this warp may access
@@ -576,7 +589,8 @@ head_gemm_kernel(const __grid_constant__ HeadGemm g, unsigned *flag) {
             const Tile x = tile_at(g, walk, t, rank);
             const RowOf of = row_of(g, walk, x, q, lane);
             const uint32_t a = local & 1u, aph = (local >> 1) & 1u;
-            if (!mbar_wait_bounded(&tfull[a], aph, flag, 0x604u)) break;
+            // the lanes go on or give up together
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[a], aph, flag, 0x604u))) break;
             tc_fence_after();
             const uint32_t acc = tmem_base + a * BN;
             if (x.kind == HEAD_STATS) epilogue_stats(g, x, of, acc, q, half);
