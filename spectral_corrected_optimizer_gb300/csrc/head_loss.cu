@@ -400,7 +400,9 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
         const int64_t fit = kPieceBytes / (cap * 2) / kHeadTileN * kHeadTileN;
         p.piece = (int)std::min(all, std::max<int64_t>(fit, kPieceMin));
         p.pieces = (int)ceil_div(vocab, p.piece);
-        // few rows: the long sum over the vocabulary is split until every pair of SMs has a tile
+        // few rows: the long sum over the vocabulary is split until every pair of SMs has a tile (one
+        // token over 128256 x 2048 424 us, 850 unsplit; 167 over 50001 x 1000 145 and 342; 2048 over
+        // 32001 x 1000 369 and 379)
         p.dh_ld = (int)round_up(dim, 32);
         const int64_t tiles = (cap / kHeadTileM) * ceil_div(dim, kHeadTileN);
         const int64_t blocks = ceil_div(std::min<int64_t>(vocab, p.piece), 64);

@@ -24,7 +24,8 @@
 //   forward 182 us, 6.66 TB/s of x, r, s, y and the checkpoint (1.21 GB): 98 % of a copy;
 //   backward with y 214 us, 5.65 TB/s (83 %): issue slots 55 % busy, 32 warps an SM; a
 //     row's chain of shuffles, barrier and stores is what is waited for.  Two rows at a
-//     time (112 registers, half the warps) took 231 us, registers instead of the ring 249.
+//     time (112 registers, half the warps) took 231 us.  Without ds and y 170 us; y alone,
+//     from the checkpoint, 74 us.
 // Odd rows cost more instructions than bytes (440 per 256 values against 240): norm of
 // 9749 x 6030 109 us (44 at the copy's rate), backward of 30001 x 3001 271 us (120).
 //
@@ -439,8 +440,7 @@ template <int N> __device__ __forceinline__ void copy_async_wait() {
 // RING > 0 (up to 16 values per thread and tensor): the rows ahead are copied to
 // shared memory asynchronously, RING - 1 of them at a time, each piece by the
 // thread that will use it, so no barrier is needed for them and the bytes in
-// flight do not depend on registers.  In registers the same width held 40 KB per
-// SM in flight, a third of what the DRAM's latency asks for at full rate.
+// flight do not depend on registers (figures at ring_of).
 template <typename T, int ROWS, int NV, int RING>
 __global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) resnorm_backward_kernel(const Backward<T> a) {
     __shared__ __align__(16) float red[2][kMaxWarps];
@@ -622,8 +622,13 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float *partial, int 
 
 // Values per thread of the forward pass: 16 (NV = 2) up to a width of 8192, so
 // that a row of 2048 takes 4 warps and many rows are in flight on an SM; then 32
-// and 64 (72 for the widest rows off their boundaries).  The backward pass keeps four times as much per value and takes 8 (NV
-// = 1) up to 4096.
+// and 64 (72 for the widest rows off their boundaries).  fp32 and odd rows take 8 up to
+// 4096.  Forward, 8 / 16 values per thread, cold: bf16 65536 x 512 57 / 55 us, x 1024 109 / 98, x 2048
+// 215 / 184, 32768 x 4096 231 / 188; fp32 65536 x 1024 172 / 174, 16384 x 4096 184 / 191; odd 65536 x
+// 1022 178 / 182.  The backward pass keeps four times as much per value and takes 8 up to
+// 4096.  8 / 16, cold: bf16 65536 x 512 82 / 76 us, x 2048 219 / 191, 32768 x 4096 229 / 195, x 2046 201 /
+// 160; fp32 65536 x 1024 250 / 260, 32768 x 2048 240 / 255, 16384 x 4096 270 / 240: for bf16 and from
+// 4096 on 16 would be the better choice.
 struct Shape {
     int nv, threads;
 };
@@ -636,7 +641,10 @@ Shape shape_of(int dim, bool vec, bool one) {
 }
 
 // Rows in the ring of the backward pass: four (three on their way while one is
-// worked on), two where four do not fit, none for wide rows.
+// worked on), two where four do not fit, none for wide rows.  By this rule / with two rows /
+// without a ring, cold: bf16 65536 x 2048 219 / 219 / 217 us, 32768 x 2046 201 / 217 / 208, 16384 x 8192
+// 199 / 201 / 285; fp32 32768 x 2048 240 / 248 / 182, 16384 x 4096 270 / 231 / 178, 8192 x 8192 277 / 277 /
+// 229: fp32 rows would do better without one.
 constexpr int ring_of(int nv, int value_bytes) { return nv == 1 ? 4 : nv == 2 ? (value_bytes == 2 ? 4 : 2) : 0; }
 constexpr int ring_bytes(const Shape &sh, int value_bytes) {
     return sh.threads * sh.nv * ring_of(sh.nv, value_bytes) * (2 * 8 * value_bytes + 8);
