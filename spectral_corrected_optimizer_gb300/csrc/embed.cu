@@ -46,14 +46,18 @@ unsigned *stage_flag_ptr() {
     return ptr;
 }
 
-// The calling thread's page-locked word: a copy into it does not hold the host up.
-static unsigned *host_word() {
-    static thread_local unsigned *word = nullptr;
-    if (!word) {
-        void *p = nullptr;
-        if (cudaMallocHost(&p, sizeof(unsigned)) == cudaSuccess) word = static_cast<unsigned *>(p);
+// A page-locked word per thread that asks, so that copies into it do not hold the host up.
+struct HostWord {
+    unsigned *p = nullptr;
+    HostWord() {
+        void *q = nullptr;
+        if (cudaMallocHost(&q, sizeof(unsigned)) == cudaSuccess) p = static_cast<unsigned *>(q);
     }
-    return word;
+    ~HostWord() { cudaFreeHost(p); }
+};
+static unsigned *host_word() {
+    static thread_local HostWord word;
+    return word.p;
 }
 
 int read_stage_flag(cudaStream_t st) {
