@@ -21,9 +21,9 @@
 //   lookup, fp32 table to bf16: 84 us, 5.2 TB/s of the bytes that have to move (64 us
 //     at the copy's rate).  The rows are read 3.3 times over from L2, 537 MB beside
 //     432 MB of DRAM traffic.
-//   gradient, bf16 to dense fp32: 244 us, 5.4 TB/s (195 us at the copy's rate).  Sums
-//     and zero rows run at 5.9 to 6.2 TB/s; the ids' count (6 us), the sort's two
-//     passes (8 us each, a third covered by zero rows) and five launches are the rest.
+//   gradient, bf16 to dense fp32: 244 us, 5.4 TB/s (195 us at the copy's rate).  The
+//     sums move 5.7 TB/s with the zero rows beside them, the joins 4.7; the ids' count and
+//     the sort's two passes (21 to 23 us each, with a sixth of their writes as zero rows) are latency.
 //     Added to what is there: 188 us (no zero rows); bf16 gradient 176; fp32 dy 279.
 // Small calls are launch and latency bound: 777 tokens 24 us in three launches.
 #include <algorithm>
