@@ -23,7 +23,7 @@
 //     432 MB of DRAM traffic.
 //   gradient, bf16 to dense fp32: 244 us, 5.4 TB/s (195 us at the copy's rate).  The
 //     sums move 5.7 TB/s with the zero rows beside them, the joins 4.7; the ids' count and
-//     the sort's two passes (21 to 23 us each, with a sixth of their writes as zero rows) are latency.
+//     the sort's two passes (21 to 23 us each, an eighth of the zero rows beside each) are latency.
 //     Added to what is there: 188 us (no zero rows); bf16 gradient 176; fp32 dy 279.
 // Small calls are launch and latency bound: 777 tokens 24 us in three launches.
 #include <algorithm>

@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(kRowThreads) head_count_kernel(const ID *__res
     const ID *from = targets + (int64_t)blockIdx.x * kStretch;
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < kStretch; i += kRowThreads) n += __syncthreads_count(has_target((int64_t)from[i + threadIdx.x], ignore, vocab));
+    for (int i = 0; i < kStretch; i += kRowThreads)
+        n += __syncthreads_count(has_target((int64_t)from[i + threadIdx.x], ignore, vocab));
     if (threadIdx.x == 0) counts[blockIdx.x] = n;
 }
 
@@ -95,8 +96,9 @@ __global__ void __launch_bounds__(kRowThreads) head_count_kernel(const ID *__res
 // in column blocks of 64 (zero behind dim).  Each block takes `share`
 // neighbouring tokens (at most one per thread), counts the targets in front of
 // them itself -- the ids come from L2, a kernel of its own for the list would
-// cost more; behind many tokens whole stretches are counted by one (counts) -- and then copies its rows, a warp per row.  The last block appends the
-// zero rows up to the next multiple of the tile height.
+// cost more; among many tokens whole stretches come counted (counts, null for
+// few) -- and then copies its rows, a warp per row.  The last blocks append the
+// zero rows up to the next multiple of 64.
 //
 // On the way the logit of each row's target is formed as an fp32 dot product:
 // the loss is the difference between it and the log-sum-exp, and a tensor core's
@@ -368,8 +370,8 @@ constexpr int kPieceMin = 4096;
 
 struct HeadPlan {
     int row_cap, ld, parts, piece, pieces, splits, dh_ld;
-    int64_t off_state, off_counts, off_row_of, off_at, off_target, off_head_row, off_norm, off_block_loss, off_stats, off_h, off_w,
-        off_p0, off_p1, off_dh, bytes;
+    int64_t off_state, off_counts, off_row_of, off_at, off_target, off_head_row, off_norm, off_block_loss, off_stats,
+        off_h, off_w, off_p0, off_p1, off_dh, bytes;
 };
 
 HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
