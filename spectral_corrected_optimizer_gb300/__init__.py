@@ -11,7 +11,9 @@ Method: "Communication-Efficient LLM Adaptation over Decentralized GPU Meshes"
 (spectral-correction optimizer); key design 4 (PowerSGD-compressed outer
 synchronisation) is bound in the ``dpsync`` submodule, the operators of the
 pipeline's end stages (embedding, residual norm with an 8-bit checkpoint,
-vocabulary head's loss) in the ``stage_ends`` submodule.
+vocabulary head's loss) in the ``stage_ends`` submodule, those of a fine-tuning
+step (LayerNorm, log-probabilities, preference and policy losses, gradient
+clipping) in the ``finetune`` submodule.
 """
 from __future__ import annotations
 
@@ -113,6 +115,23 @@ SIGNATURES = [
     ("head_loss_grad_workspace", _i64, [_i64, _i64, _i32]),
     ("head_loss_grad", _int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _i32, _i32,
                               _vp, _i64, _vp]),
+    ("layernorm_forward", _int, [_vp, _vp, _vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp, _i64, _i32, _vp]),
+    ("layernorm_backward_workspace", _i64, [_i64, _i32]),
+    ("layernorm_backward", _int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _i64, _vp]),
+    ("head_logp_workspace", _i64, [_i64, _i64, _i32]),
+    ("head_logp", _int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _i64, _vp]),
+    ("head_logp_backward_workspace", _i64, [_i64, _i64, _i32]),
+    ("head_logp_backward", _int, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _i64,
+                                  _vp]),
+    ("preference_loss_workspace", _i64, [_i64, _i64]),
+    ("preference_loss", _int, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _f32, _f32, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
+                               _vp, _i64, _vp]),
+    ("policy_loss_workspace", _i64, [_i64, _i64]),
+    ("policy_loss", _int, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i64, _i64, _f64, _f64, _f32, _i32, _f32, _vp, _vp,
+                           _vp, _vp, _i64, _vp]),
+    ("grad_norm_workspace", _i64, [_i32]),
+    ("grad_norm", _int, [_vp, _vp, _vp, _i32, _f32, _i32, _vp, _vp, _i64, _vp]),
+    ("clip_grads", _int, [_vp, _vp, _vp, _vp, _vp, _i32, _f32, _f32, _i32, _vp, _vp, _i64, _vp]),
 ]
 
 _lib = None

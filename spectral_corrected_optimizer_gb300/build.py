@@ -45,7 +45,8 @@ def _sources():
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
         os.path.join(INCLUDE, "specoptim.h"), os.path.join(INCLUDE, "dpsync.h"),
-        os.path.join(INCLUDE, "mask_fused.h"), os.path.join(INCLUDE, "stage_ends.h")]
+        os.path.join(INCLUDE, "mask_fused.h"), os.path.join(INCLUDE, "stage_ends.h"),
+        os.path.join(INCLUDE, "finetune.h")]
 
 
 def needs_build(check: bool = False) -> bool:

@@ -72,8 +72,9 @@ int check_stage_flag(cudaStream_t st) {
     if (!v) return SPECOPTIM_OK;
     SPECOPTIM_CUDA(cudaMemsetAsync(stage_flag_ptr(), 0, sizeof(v), st));
     SPECOPTIM_CUDA(cudaStreamSynchronize(st));
-    return fail(SPECOPTIM_ERR_BOUNDS, v == kSiteTokenId ? "a token id lies outside the vocabulary"
-                                                        : "a target lies outside the vocabulary");
+    return fail(SPECOPTIM_ERR_BOUNDS, v == kSiteTokenId  ? "a token id lies outside the vocabulary"
+                                      : v == kSiteTarget ? "a target lies outside the vocabulary"
+                                                         : "offsets of sequences descend or lie outside the tokens");
 }
 
 namespace {

@@ -1,5 +1,6 @@
 // Softmax cross entropy of the vocabulary head and its gradients
-// (include/stage_ends.h): the last stage of the training pipeline.
+// (include/stage_ends.h): the last stage of the training pipeline; and the tokens'
+// log-probabilities with the gradient of any loss over them (include/finetune.h).
 //
 //   l_i = h_i W^T,  row_loss_i = log sum_v exp(l_iv) - l_i,target,
 //   d = (softmax(l) - onehot) * factor,  dh = d W,  dW = d^T h
@@ -17,6 +18,12 @@
 //      and no [N][V] tensor does.  dh sums up in fp32 over the pieces.
 // The products are in head_gemm.cu.
 //
+// head_logp is steps 1 and 2 and keeps each row's normalisation; head_logp_backward is
+// steps 1 and 3 from what was kept (6 N V D), with d times -dlogp_i: the factor goes into
+// the normalisation that turns logits into probabilities, so a weighted d is rounded to
+// bf16 once, like any other, and the products do not know of it.  Tokens whose dlogp is 0
+// are left out in step 1.
+//
 // A piece's logits are formed twice, 8 N V D operations where keeping [N][V] would take
 // 6: that is the price of not keeping them, and of rounding a probability once (bf16,
 // normalised) instead of twice.  Measured on a GB300: 8192 tokens, a tenth without a
@@ -28,6 +35,7 @@
 #include <cstring>
 #include <string>
 
+#include "../../include/finetune.h"
 #include "head_gemm.cuh"
 
 namespace spco {
@@ -112,7 +120,8 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
                                                         int w_vec, HeadState *state, int *__restrict__ row_of,
                                                         int *__restrict__ at, int *__restrict__ target,
                                                         uint16_t *__restrict__ out, HeadRow *__restrict__ head_row,
-                                                        float *__restrict__ row_loss, unsigned *flag) {
+                                                        float *__restrict__ row_loss, float *__restrict__ kept,
+                                                        unsigned *flag) {
     __shared__ int red[2][kRowWarps], own_token[kRowThreads], own_target[kRowThreads];
     __shared__ float dots[kRowWarps];
     __shared__ int held[kRowWarps];
@@ -155,7 +164,8 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
         own_token[k] = t;
         own_target[k] = (int)id;
     } else if (t < t1) {
-        row_loss[t] = 0.f;
+        if (row_loss) row_loss[t] = 0.f;
+        if (kept) kept[t] = kept[tokens + t] = kept[2 * tokens + t] = 0.f;
     }
     __syncthreads();
     const int vecs = (dim + 63) / 64 * 8;
@@ -258,6 +268,7 @@ __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *sta
                                                        const HeadRow *head_row,
                                                        const int *row_of, HeadState *state,
                                                        HeadNorm *__restrict__ norm, float *__restrict__ row_loss,
+                                                       float sign, float *__restrict__ kept, int tokens,
                                                        float *__restrict__ block_loss, float *__restrict__ loss) {
     constexpr int LANES = kLseThreads / ROWS;
     __shared__ float sm[LANES][ROWS + 1], ss[LANES][ROWS + 1], row_sum[ROWS];
@@ -299,7 +310,13 @@ __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *sta
                 l = above < 30.f ? log1pf(s * exp2f(above))
                     : none       ? (m + log2f(total)) * kLn2 - lt
                                  : (above + log2f(total)) * kLn2;
-                row_loss[row_of[row]] = l;
+                const int t = row_of[row];
+                row_loss[t] = sign * l;
+                if (kept) {
+                    kept[t] = m;
+                    kept[tokens + t] = 1.f / total;
+                    kept[2 * tokens + t] = s / total;
+                }
             }
             row_sum[w] = l;
         }
@@ -323,6 +340,32 @@ __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *sta
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) *loss = l * state->inv_count;
+}
+
+// What turns the rows' logits into -dlogp (softmax - onehot), from what the forward pass kept.
+__global__ void __launch_bounds__(256) head_weight_kernel(const float *dlogp, const float *kept, int tokens, const int *row_of,
+                                                          const HeadState *state, HeadNorm *norm) {
+    grid_dependency_launch();
+    grid_dependency_wait();
+    const int rows = state->rows;
+    for (int r = blockIdx.x * 256 + threadIdx.x; r < rows; r += gridDim.x * 256) {
+        const int t = row_of[r];
+        const float g = dlogp[t];
+        norm[r] = HeadNorm{kept[t], -g * kept[tokens + t], g * kept[2 * tokens + t]};
+    }
+}
+
+// The targets of the tokens that have a gradient, -1 for the others.
+template <typename ID>
+__global__ void __launch_bounds__(256) head_select_kernel(const ID *__restrict__ targets, int64_t ignore, int tokens, int vocab,
+                                                          const float *__restrict__ dlogp, int *__restrict__ out,
+                                                          unsigned *flag) {
+    for (int t = blockIdx.x * 256 + threadIdx.x; t < tokens; t += gridDim.x * 256) {
+        const int64_t id = (int64_t)targets[t];
+        const bool has = has_target(id, ignore, vocab);
+        if (id != ignore && !has) atomicExch(flag, kSiteTarget);
+        out[t] = has && dlogp[t] != 0.f ? (int)id : -1;
+    }
 }
 
 // dh[t] = factor * sum over the parts of the token's row; zero without a target.
@@ -371,10 +414,11 @@ constexpr int kPieceMin = 4096;
 struct HeadPlan {
     int row_cap, ld, parts, piece, pieces, splits, dh_ld;
     int64_t off_state, off_counts, off_row_of, off_at, off_target, off_head_row, off_norm, off_block_loss, off_stats,
-        off_h, off_w, off_p0, off_p1, off_dh, bytes;
+        off_h, off_w, off_p0, off_p1, off_dh, off_loss, off_selected, bytes;
 };
 
-HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
+// stats: the row statistics are formed; grad: the gradients
+HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad, bool stats = true) {
     HeadPlan p{};
     p.row_cap = (int)round_up(std::max<int64_t>(tokens, 1), kHeadTileM);
     p.ld = (int)round_up(dim, 8);
@@ -393,8 +437,8 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
     p.off_target = take(cap * 4);
     p.off_head_row = take(cap * sizeof(HeadRow));
     p.off_norm = take(cap * sizeof(HeadNorm));
-    p.off_block_loss = take(ceil_div(cap, kLseFew) * 4);
-    p.off_stats = take((int64_t)p.parts * cap * 8);
+    p.off_block_loss = stats ? take(ceil_div(cap, kLseFew) * 4) : 0;
+    p.off_stats = stats ? take((int64_t)p.parts * cap * 8) : 0;
     p.off_h = take(cap * round_up(dim, 64) * 2);
     p.off_w = p.ld != dim ? take(vocab * p.ld * 2) : 0;
     if (grad) {
@@ -413,6 +457,8 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad) {
         p.off_p1 = p.pieces > 1 ? take(cap * p.piece * 2) : p.off_p0;
         p.off_dh = take((int64_t)p.splits * cap * p.dh_ld * 4);
     }
+    p.off_loss = take(4);
+    p.off_selected = stats ? 0 : take(tokens * 4);
     p.bytes = at;
     return p;
 }
@@ -437,11 +483,14 @@ struct HeadCall {
     char *ws;
     int64_t ws_bytes;
     cudaStream_t st;
+    float *kept = nullptr;   // log-probabilities instead of losses, and what their backward pass needs
+    bool backward = false;   // that pass: loss and row_loss are not there
 };
 
 int check_call(const HeadCall &c, const HeadPlan &p, const std::string &what) {
     if (c.id_bytes != 4 && c.id_bytes != 8) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": id_bytes must be 4 or 8");
-    if (!c.w || !c.loss || !c.ws || (c.tokens > 0 && (!c.h || !c.targets || !c.row_loss)))
+    if (!c.w || !c.ws || (c.tokens > 0 && (!c.h || !c.targets)) ||
+        (!c.backward && (!c.loss || (c.tokens > 0 && !c.row_loss))))
         return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": null pointer");
     if (!aligned_to(c.h, 2) || !aligned_to(c.targets, c.id_bytes) || !aligned_to(c.loss, 4) ||
         !aligned_to(c.row_loss, 4) || !aligned16(c.w) || !aligned16(c.ws))
@@ -456,8 +505,8 @@ int check_call(const HeadCall &c, const HeadPlan &p, const std::string &what) {
 // 8, listing / count + listing: 32768 tokens 22 / 6 + 15 us, 65536 35 / 7 + 22, 2^20 1056 / 8 + 207).
 constexpr int kCountTokens = 1 << 16;
 
-// Steps 1 and 2: afterwards loss, row_loss and the rows' norms exist.
-int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
+// Step 1: afterwards the rows that take part are listed and copied, and the products' operands known.
+int run_rows(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     std::memset(g, 0, sizeof(*g));
     HeadState *state = reinterpret_cast<HeadState *>(c.ws + p.off_state);
     int *row_of = reinterpret_cast<int *>(c.ws + p.off_row_of), *at = reinterpret_cast<int *>(c.ws + p.off_at);
@@ -482,7 +531,7 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
                     head_rows_kernel<ID><<<blocks + (grad ? kPadBlocks : 0), kRowThreads, 0, c.st>>>(
                         static_cast<const ID *>(c.targets), c.ignore, tokens, vocab, c.mean, share, blocks, counts,
                         static_cast<const uint16_t *>(c.h), w, c.dim, p.row_cap, h_vec, w_vec, state, row_of, at, target,
-                        hc, head_row, c.row_loss, stage_flag_ptr()));
+                        hc, head_row, c.row_loss, c.kept, stage_flag_ptr()));
     };
     if (c.id_bytes == 8) rows(int64_t{});
     else rows(int32_t{});
@@ -508,8 +557,18 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     g->rows = head_row;
     g->stats = reinterpret_cast<float2 *>(c.ws + p.off_stats);
     g->norm = norm;
+    return SPECOPTIM_OK;
+}
+
+// Steps 1 and 2: afterwards loss, row_loss and the rows' norms exist.
+int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
+    if (int rc = run_rows(c, p, grad, g)) return rc;
+    HeadState *state = reinterpret_cast<HeadState *>(c.ws + p.off_state);
+    const int *row_of = reinterpret_cast<const int *>(c.ws + p.off_row_of);
+    const HeadRow *head_row = reinterpret_cast<const HeadRow *>(c.ws + p.off_head_row);
+    HeadNorm *norm = reinterpret_cast<HeadNorm *>(c.ws + p.off_norm);
     g->jobs = 1;
-    g->job[0] = HeadJob{HEAD_STATS, 0, 0, vocab, 1, 0};
+    g->job[0] = HeadJob{HEAD_STATS, 0, 0, (int)c.vocab, 1, 0};
     const int64_t tiles = (int64_t)(p.row_cap / kHeadTileM) * (p.parts / 2);
     if (int rc = head_gemm(*g, (int)std::min<int64_t>(tiles, INT32_MAX), "head_stats", c.st)) return rc;
     cudaError_t e = cudaSuccess;
@@ -517,9 +576,75 @@ int run_loss(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     auto *lse = lse_rows == kLseFew ? &head_lse_kernel<kLseFew> : &head_lse_kernel<kLseMany>;
     SPCO_LAUNCH("head_lse", c.st,
                 e = launch_dependent(lse, dim3(p.row_cap / lse_rows), dim3(kLseThreads), 0, c.st, g->stats, p.parts,
-                                     p.row_cap, head_row, row_of, state, norm, c.row_loss,
-                                     reinterpret_cast<float *>(c.ws + p.off_block_loss), c.loss));
+                                     p.row_cap, head_row, row_of, state, norm, c.row_loss, c.kept ? -1.f : 1.f, c.kept,
+                                     (int)c.tokens, reinterpret_cast<float *>(c.ws + p.off_block_loss), c.loss));
     SPECOPTIM_CUDA(e);
+    return SPECOPTIM_OK;
+}
+
+// Step 3: dh and dw from the rows' norms.
+int run_grad(const HeadCall &c, const HeadPlan &p, HeadGemm *g, void *dh, void *dw, int32_t dw_type, int32_t accumulate,
+             float grad_scale) {
+    const int dim = c.dim;
+    const int64_t vocab = c.vocab;
+    const int64_t p_lines = (int64_t)(p.piece / 64) * p.row_cap;
+    for (int b = 0; b < std::min(p.pieces, 2); ++b) {
+        char *piece = c.ws + (b ? p.off_p1 : p.off_p0);
+        if (int rc = make_tmap_2d_bf16(&g->tm_p_k[b], piece, p_lines, 64, 64, 128)) return rc;
+        if (int rc = make_tmap_2d_bf16(&g->tm_p[b], piece, p_lines, 64, 64, 64)) return rc;
+        if (int rc = make_tmap_2d_bf16(&g->tm_p_st[b], piece, p_lines, 64, 64, 32)) return rc;
+    }
+    float *dh_sums = reinterpret_cast<float *>(c.ws + p.off_dh);
+    if (int rc = make_tmap_2d(&g->tm_dh, dh_sums, (int64_t)p.splits * p.row_cap, p.dh_ld, p.dh_ld, 32, 32)) return rc;
+    g->dw = dw;
+    g->dw_bf16 = dw_type == STAGE_BF16;
+    g->dw_add = accumulate != 0;
+    g->dw_tma = aligned16(dw) && dim * type_bytes(dw_type) % 16 == 0 && !(g->dw_bf16 && g->dw_add);
+    if (g->dw_tma && g->dw_bf16) {
+        if (int rc = make_tmap_2d_bf16(&g->tm_dw, dw, vocab, dim, dim, 32)) return rc;
+    } else if (g->dw_tma) {
+        if (int rc = make_tmap_2d(&g->tm_dw, static_cast<float *>(dw), vocab, dim, dim, 32, 32)) return rc;
+    }
+    g->grad_scale = grad_scale;
+    const int64_t m_tiles = p.row_cap / kHeadTileM, d_tiles = ceil_div(dim, kHeadTileN);
+    for (int i = 0; i <= p.pieces; ++i) {
+        g->jobs = 0;
+        int64_t tiles = 0;
+        if (i < p.pieces) {
+            const int v0 = i * p.piece, width = (int)std::min<int64_t>(p.piece, vocab - v0);
+            g->job[g->jobs++] = HeadJob{HEAD_PROB, i & 1, v0, width, 1, 0};
+            tiles += m_tiles * ceil_div(width, kHeadTileN);
+        }
+        if (i > 0) {
+            const int v0 = (i - 1) * p.piece, width = (int)std::min<int64_t>(p.piece, vocab - v0);
+            g->job[g->jobs++] = HeadJob{HEAD_DH, (i - 1) & 1, v0, width, p.splits, i > 1};
+            g->job[g->jobs++] = HeadJob{HEAD_DW, (i - 1) & 1, v0, width, 1, 0};
+            tiles += m_tiles * d_tiles * p.splits + ceil_div(width, kHeadTileM) * d_tiles;
+        }
+        if (int rc = head_gemm(*g, (int)std::min<int64_t>(tiles, INT32_MAX), "head_grad", c.st)) return rc;
+    }
+    if (c.tokens > 0) {
+        const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim, 8), 32));
+        const int grid = (int)std::min<int64_t>(c.tokens, num_sms() * 16);
+        const bool vec = dim % 8 == 0 && aligned16(dh);
+        auto *k = vec ? &head_dh_kernel<true> : &head_dh_kernel<false>;
+        cudaError_t e = cudaSuccess;
+        SPCO_LAUNCH("head_dh", c.st,
+                    e = launch_dependent(k, dim3(grid), dim3(threads), 0, c.st,
+                                         Span<const float>(dh_sums, (int64_t)p.splits * p.row_cap * p.dh_ld),
+                                         p.splits, p.row_cap, p.dh_ld, reinterpret_cast<const int *>(c.ws + p.off_at),
+                                         g->state, grad_scale, (int)c.tokens, dim,
+                                         Span<bf16>(static_cast<bf16 *>(dh), c.tokens * dim)));
+        SPECOPTIM_CUDA(e);
+    }
+    return SPECOPTIM_OK;
+}
+
+int check_grad(const HeadCall &c, const void *dh, const void *dw, int32_t dw_type, const std::string &what) {
+    if (!dw || (c.tokens > 0 && !dh)) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": null pointer");
+    if (!type_ok(dw_type)) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": dw_type must be STAGE_BF16 or STAGE_FP32");
+    if (!aligned_to(dh, 2) || !aligned_to(dw, type_bytes(dw_type)))
+        return fail(SPECOPTIM_ERR_MISALIGNED, what + ": dh and dw must be aligned to their elements");
     return SPECOPTIM_OK;
 }
 
@@ -573,64 +698,94 @@ extern "C" int head_loss_grad(const void *h, const void *w, const void *targets,
         const HeadCall c{h, w, targets, id_bytes, ignore_index, tokens, vocab, dim, mean, loss, row_loss,
                          static_cast<char *>(workspace), workspace_bytes, static_cast<cudaStream_t>(stream)};
         if (int rc = check_call(c, p, "head_loss_grad")) return rc;
-        if (!dw || (tokens > 0 && !dh)) return fail(SPECOPTIM_ERR_INVALID_ARG, "head_loss_grad: null pointer");
-        if (!type_ok(dw_type))
-            return fail(SPECOPTIM_ERR_INVALID_ARG, "head_loss_grad: dw_type must be STAGE_BF16 or STAGE_FP32");
-        if (!aligned_to(dh, 2) || !aligned_to(dw, type_bytes(dw_type)))
-            return fail(SPECOPTIM_ERR_MISALIGNED, "head_loss_grad: dh and dw must be aligned to their elements");
+        if (int rc = check_grad(c, dh, dw, dw_type, "head_loss_grad")) return rc;
         if (int rc = bind_device()) return rc;
         HeadGemm g;
         if (int rc = run_loss(c, p, true, &g)) return rc;
-        const int64_t p_lines = (int64_t)(p.piece / 64) * p.row_cap;
-        for (int b = 0; b < std::min(p.pieces, 2); ++b) {
-            char *piece = c.ws + (b ? p.off_p1 : p.off_p0);
-            if (int rc = make_tmap_2d_bf16(&g.tm_p_k[b], piece, p_lines, 64, 64, 128)) return rc;
-            if (int rc = make_tmap_2d_bf16(&g.tm_p[b], piece, p_lines, 64, 64, 64)) return rc;
-            if (int rc = make_tmap_2d_bf16(&g.tm_p_st[b], piece, p_lines, 64, 64, 32)) return rc;
-        }
-        float *dh_sums = reinterpret_cast<float *>(c.ws + p.off_dh);
-        if (int rc = make_tmap_2d(&g.tm_dh, dh_sums, (int64_t)p.splits * p.row_cap, p.dh_ld, p.dh_ld, 32, 32)) return rc;
-        g.dw = dw;
-        g.dw_bf16 = dw_type == STAGE_BF16;
-        g.dw_add = accumulate != 0;
-        g.dw_tma = aligned16(dw) && dim * type_bytes(dw_type) % 16 == 0 && !(g.dw_bf16 && g.dw_add);
-        if (g.dw_tma && g.dw_bf16) {
-            if (int rc = make_tmap_2d_bf16(&g.tm_dw, dw, vocab, dim, dim, 32)) return rc;
-        } else if (g.dw_tma) {
-            if (int rc = make_tmap_2d(&g.tm_dw, static_cast<float *>(dw), vocab, dim, dim, 32, 32)) return rc;
-        }
-        g.grad_scale = grad_scale;
-        const int64_t m_tiles = p.row_cap / kHeadTileM, d_tiles = ceil_div(dim, kHeadTileN);
-        for (int i = 0; i <= p.pieces; ++i) {
-            g.jobs = 0;
-            int64_t tiles = 0;
-            if (i < p.pieces) {
-                const int v0 = i * p.piece, width = (int)std::min<int64_t>(p.piece, vocab - v0);
-                g.job[g.jobs++] = HeadJob{HEAD_PROB, i & 1, v0, width, 1, 0};
-                tiles += m_tiles * ceil_div(width, kHeadTileN);
-            }
-            if (i > 0) {
-                const int v0 = (i - 1) * p.piece, width = (int)std::min<int64_t>(p.piece, vocab - v0);
-                g.job[g.jobs++] = HeadJob{HEAD_DH, (i - 1) & 1, v0, width, p.splits, i > 1};
-                g.job[g.jobs++] = HeadJob{HEAD_DW, (i - 1) & 1, v0, width, 1, 0};
-                tiles += m_tiles * d_tiles * p.splits + ceil_div(width, kHeadTileM) * d_tiles;
-            }
-            if (int rc = head_gemm(g, (int)std::min<int64_t>(tiles, INT32_MAX), "head_grad", c.st)) return rc;
-        }
-        if (tokens > 0) {
-            const int threads = (int)std::min<int64_t>(256, round_up(ceil_div(dim, 8), 32));
-            const int grid = (int)std::min<int64_t>(tokens, num_sms() * 16);
-            const bool vec = dim % 8 == 0 && aligned16(dh);
-            auto *k = vec ? &head_dh_kernel<true> : &head_dh_kernel<false>;
-            cudaError_t e = cudaSuccess;
-            SPCO_LAUNCH("head_dh", c.st,
-                        e = launch_dependent(k, dim3(grid), dim3(threads), 0, c.st,
-                                             Span<const float>(dh_sums, (int64_t)p.splits * p.row_cap * p.dh_ld),
-                                             p.splits, p.row_cap, p.dh_ld, reinterpret_cast<const int *>(c.ws + p.off_at),
-                                             g.state, grad_scale, (int)tokens, dim,
-                                             Span<bf16>(static_cast<bf16 *>(dh), tokens * dim)));
-            SPECOPTIM_CUDA(e);
-        }
+        return run_grad(c, p, &g, dh, dw, dw_type, accumulate, grad_scale);
+    });
+}
+
+extern "C" int64_t head_logp_workspace(int64_t tokens, int64_t vocab, int32_t dim) {
+    int64_t bytes = -1;
+    entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "head_logp")) return rc;
+        bytes = plan_head(tokens, vocab, dim, false).bytes;
         return SPECOPTIM_OK;
+    });
+    return bytes;
+}
+
+extern "C" int head_logp(const void *h, const void *w, const void *targets, int32_t id_bytes, int64_t ignore_index,
+                         int64_t tokens, int64_t vocab, int32_t dim, float *logp, float *kept, void *workspace,
+                         int64_t workspace_bytes, void *stream) {
+    return entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "head_logp")) return rc;
+        if (!workspace || (tokens > 0 && !kept)) return fail(SPECOPTIM_ERR_INVALID_ARG, "head_logp: null pointer");
+        if (!aligned_to(kept, 4)) return fail(SPECOPTIM_ERR_MISALIGNED, "head_logp: kept must be aligned to its elements");
+        const HeadPlan p = plan_head(tokens, vocab, dim, false);
+        char *ws = static_cast<char *>(workspace);
+        HeadCall c{h, w, targets, id_bytes, ignore_index, tokens, vocab, dim, 0, reinterpret_cast<float *>(ws + p.off_loss),
+                   logp, ws, workspace_bytes, static_cast<cudaStream_t>(stream)};
+        c.kept = kept;
+        if (int rc = check_call(c, p, "head_logp")) return rc;
+        if (tokens == 0) return SPECOPTIM_OK;
+        if (int rc = bind_device()) return rc;
+        HeadGemm g;
+        return run_loss(c, p, false, &g);
+    });
+}
+
+extern "C" int64_t head_logp_backward_workspace(int64_t tokens, int64_t vocab, int32_t dim) {
+    int64_t bytes = -1;
+    entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "head_logp_backward")) return rc;
+        bytes = plan_head(tokens, vocab, dim, true, false).bytes;
+        return SPECOPTIM_OK;
+    });
+    return bytes;
+}
+
+extern "C" int head_logp_backward(const float *dlogp, const float *kept, const void *h, const void *w, const void *targets,
+                                  int32_t id_bytes, int64_t ignore_index, int64_t tokens, int64_t vocab, int32_t dim,
+                                  void *dh, void *dw, int32_t dw_type, int32_t accumulate, void *workspace,
+                                  int64_t workspace_bytes, void *stream) {
+    return entry([&]() -> int {
+        if (int rc = check_sizes(tokens, vocab, dim, "head_logp_backward")) return rc;
+        if (tokens > 0 && (!dlogp || !kept)) return fail(SPECOPTIM_ERR_INVALID_ARG, "head_logp_backward: null pointer");
+        if (!aligned_to(dlogp, 4) || !aligned_to(kept, 4))
+            return fail(SPECOPTIM_ERR_MISALIGNED, "head_logp_backward: dlogp and kept must be aligned to their elements");
+        const HeadPlan p = plan_head(tokens, vocab, dim, true, false);
+        HeadCall c{h, w, targets, id_bytes, ignore_index, tokens, vocab, dim, 0, nullptr, nullptr,
+                   static_cast<char *>(workspace), workspace_bytes, static_cast<cudaStream_t>(stream)};
+        c.backward = true;
+        if (int rc = check_call(c, p, "head_logp_backward")) return rc;
+        if (int rc = check_grad(c, dh, dw, dw_type, "head_logp_backward")) return rc;
+        if (int rc = bind_device()) return rc;
+        // the targets of the tokens with a gradient stand in for all of them
+        int *selected = reinterpret_cast<int *>(c.ws + p.off_selected);
+        const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(tokens, 256), num_sms() * 8));
+        auto select = [&](auto id) {
+            using ID = decltype(id);
+            SPCO_LAUNCH("head_select", c.st,
+                        head_select_kernel<ID><<<blocks, 256, 0, c.st>>>(static_cast<const ID *>(targets), ignore_index,
+                                                                         (int)tokens, (int)vocab, dlogp, selected,
+                                                                         stage_flag_ptr()));
+        };
+        if (id_bytes == 8) select(int64_t{});
+        else select(int32_t{});
+        SPECOPTIM_LAUNCHED("head_select_kernel");
+        c.targets = selected;
+        c.id_bytes = 4;
+        c.ignore = -1;
+        HeadGemm g;
+        if (int rc = run_rows(c, p, true, &g)) return rc;
+        cudaError_t e = cudaSuccess;
+        SPCO_LAUNCH("head_weight", c.st,
+                    e = launch_dependent(head_weight_kernel, dim3(blocks), dim3(256), 0, c.st, dlogp, kept, (int)tokens,
+                                         reinterpret_cast<const int *>(c.ws + p.off_row_of), g.state,
+                                         reinterpret_cast<HeadNorm *>(c.ws + p.off_norm)));
+        SPECOPTIM_CUDA(e);
+        return run_grad(c, p, &g, dh, dw, dw_type, accumulate, 1.f);
     });
 }

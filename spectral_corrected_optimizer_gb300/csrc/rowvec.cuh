@@ -22,8 +22,9 @@ namespace spco {
 using bf16 = __nv_bfloat16;
 
 // What a kernel writes to the stage-end operators' device flag when it skips an
-// id outside the vocabulary; read_stage_flag() and check_stage_flag() (embed.cu) read and clear it.
-constexpr unsigned kSiteTokenId = 1, kSiteTarget = 2;
+// id outside the vocabulary, or moves a sequence's offset into the tokens;
+// read_stage_flag() and check_stage_flag() (embed.cu) read and clear it.
+constexpr unsigned kSiteTokenId = 1, kSiteTarget = 2, kSiteOffset = 3;
 unsigned *stage_flag_ptr();
 
 __device__ __forceinline__ float to_f(float x) { return x; }
