@@ -43,31 +43,136 @@ static_assert(kMaxThreads * kMaxPieces >= (kMaxDim + 14) / 8, "the widest row at
 // but all tensors from a 16-byte boundary; anything else.
 enum Rows : int { ROWS_VEC = 0, ROWS_ODD = 1, ROWS_ANY = 2 };
 
-// values i .. i + 7 of the tensor
-template <int ROWS, typename T> __device__ __forceinline__ void load_piece8(const Span<const T> &s, int64_t i, float (&v)[8]) {
-    if (ROWS == ROWS_VEC || (ROWS == ROWS_ODD && i + 8 <= s.hi)) {
-        load8(s.p + i, v);
-    } else if (ROWS == ROWS_ANY) {
-        load_any(s, s.lo + i, v);
-    } else {  // the tensor's last piece is cut short
+// Two fp32 values that one instruction works on.  These kernels have little time per
+// byte, and what they run out of is issue slots.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+    const float2 f = both(a);
+    return f.x + f.y;
+}
+
+// 8 values as they lie in memory
+template <typename T> struct Raw8 {
+    uint4 a[sizeof(T) / 2];
+};
+__device__ __forceinline__ void values(const Raw8<bf16> &r, float (&v)[8]) {
+    const uint4 u = r.a[0];
+    v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
+    v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
+}
+__device__ __forceinline__ void values(const Raw8<float> &r, float (&v)[8]) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = i + k < s.hi ? to_f(s.p[i + k]) : 0.f;
+    for (int i = 0; i < 2; ++i) {
+        v[4 * i] = __uint_as_float(r.a[i].x);
+        v[4 * i + 1] = __uint_as_float(r.a[i].y);
+        v[4 * i + 2] = __uint_as_float(r.a[i].z);
+        v[4 * i + 3] = __uint_as_float(r.a[i].w);
     }
+}
+__device__ __forceinline__ void raw_of(const float (&v)[8], Raw8<bf16> &r) {
+    r.a[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void raw_of(const float (&v)[8], Raw8<float> &r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        r.a[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                            __float_as_uint(v[4 * i + 3]));
+}
+
+__device__ __forceinline__ void values(const Raw8<bf16> &r, F2 (&v)[4]) {
+    const uint4 u = r.a[0];
+    v[0] = pair(lo_f(u.x), hi_f(u.x));
+    v[1] = pair(lo_f(u.y), hi_f(u.y));
+    v[2] = pair(lo_f(u.z), hi_f(u.z));
+    v[3] = pair(lo_f(u.w), hi_f(u.w));
+}
+__device__ __forceinline__ void values(const Raw8<float> &r, F2 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[2 * i] = pair(__uint_as_float(r.a[i].x), __uint_as_float(r.a[i].y));
+        v[2 * i + 1] = pair(__uint_as_float(r.a[i].z), __uint_as_float(r.a[i].w));
+    }
+}
+template <typename T> __device__ __forceinline__ void raw_of(const F2 (&v)[4], Raw8<T> &r) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = both(v[i]);
+        f[2 * i] = x.x;
+        f[2 * i + 1] = x.y;
+    }
+    raw_of(f, r);
+}
+
+// values i .. i + 7 of the tensor
+template <int ROWS, typename T> __device__ __forceinline__ Raw8<T> load_piece(const Span<const T> &s, int64_t i) {
+    Raw8<T> r;
+    if (ROWS == ROWS_VEC || (ROWS == ROWS_ODD && i + 8 <= s.hi)) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(s.p + i);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.a[k] = q[k];  // plain: the call may be writing in place
+    } else {
+        float v[8];
+        if (ROWS == ROWS_ANY) {
+            load_any(s, s.lo + i, v);
+        } else {  // the tensor's last piece is cut short
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = i + k < s.hi ? to_f(s.p[i + k]) : 0.f;
+        }
+        raw_of(v, r);  // exact: the values are the tensor's own
+    }
+    return r;
 }
 
 // v to columns col .. col + 7 of the row that begins at value `row`, as far as they exist
 template <int ROWS, typename T>
-__device__ __forceinline__ void store_piece8(const Span<T> &s, int64_t row, int col, int dim, const float (&v)[8]) {
+__device__ __forceinline__ void store_piece(const Span<T> &s, int64_t row, int col, int dim, const Raw8<T> &r) {
     T *p = s.p + s.lo + row + col;
     const bool whole = ROWS == ROWS_VEC || (col >= 0 && col + 8 <= dim &&
                                             (ROWS == ROWS_ODD || (reinterpret_cast<uintptr_t>(p) & 15) == 0));
     if (whole) {
-        store8(p, v);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) reinterpret_cast<uint4 *>(p)[k] = r.a[k];
     } else {
+        float v[8];
+        values(r, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (col + i >= 0 && col + i < dim) p[i] = from_f<T>(v[i]);
     }
+}
+template <int ROWS, typename T, typename V>
+__device__ __forceinline__ void store_values(const Span<T> &s, int64_t row, int col, int dim, const V &v) {
+    Raw8<T> r;
+    raw_of(v, r);
+    store_piece<ROWS>(s, row, col, dim, r);
 }
 
 // zeros for the values that belong to the rows in front and behind
@@ -79,10 +184,45 @@ template <int ROWS> __device__ __forceinline__ void mask_piece(float (&v)[8], in
     }
 }
 
+// the same for values as they lie in memory: words that keep the row's
+template <typename T> __device__ __forceinline__ Raw8<T> row_words(int col, int dim) {
+    Raw8<T> m;
+    uint32_t w[2 * sizeof(T)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t in = col + i >= 0 && col + i < dim ? 0xffffffffu : 0u;
+        if (sizeof(T) == 4) w[i] = in;
+        else w[i / 2] = i & 1 ? w[i / 2] | (in & 0xffff0000u) : in & 0xffffu;
+    }
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) m.a[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    return m;
+}
+template <int ROWS, typename T> __device__ __forceinline__ void keep_words(Raw8<T> &r, const Raw8<T> &m) {
+    if (ROWS != ROWS_VEC)
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+            r.a[k] = make_uint4(r.a[k].x & m.a[k].x, r.a[k].y & m.a[k].y, r.a[k].z & m.a[k].z, r.a[k].w & m.a[k].w);
+}
+template <int ROWS> __device__ __forceinline__ void mask_piece(F2 (&v)[4], int col, int dim) {
+    if (ROWS != ROWS_VEC && (col < 0 || col + 8 > dim)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = both(v[i]);
+            const int c = col + 2 * i;
+            v[i] = pair(c < 0 || c >= dim ? 0.f : f.x, c + 1 < 0 || c + 1 >= dim ? 0.f : f.y);
+        }
+    }
+}
+
 // a vector of dim values (gamma, beta), at any place
-template <int ROWS, typename T> __device__ __forceinline__ void load_vector(const Span<const T> &s, int col, float (&v)[8]) {
-    if (ROWS == ROWS_VEC) load8(s.p + col, v);
-    else load_any(s, s.lo + col, v);
+template <int ROWS, typename T> __device__ __forceinline__ Raw8<T> load_vector(const Span<const T> &s, int col) {
+    if (ROWS == ROWS_VEC) return load_piece<ROWS_VEC>(s, col);
+    float v[8];
+    Raw8<T> r;
+    load_any(s, s.lo + col, v);
+    raw_of(v, r);
+    return r;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -92,6 +232,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // ---- forward -----------------------------------------------------------------------------
+
+// Whether a row is loaded while the one in front is worked on.  Pays where the registers allow it: cold,
+// with / without, bf16 65536 x 2048 163 / 168 us, 32768 x 4096 164 / 171, fp32 32768 x 2048 158 / 164; more
+// pieces of fp32, or rows that are shifted into place, spill (fp32 16384 x 4096 with 4 pieces 202 / 176).
+template <typename T> constexpr bool loads_ahead(int rows, int nv) {
+    return rows == ROWS_VEC && nv * (int)sizeof(T) <= 8;
+}
 
 template <typename T> struct Forward {
     Span<const T> x, r, gamma, beta;  // r.p, beta.p null: none
@@ -104,9 +251,10 @@ template <typename T> struct Forward {
 
 // A row per block (WARP: per warp), NV pieces of 8 values per thread.
 template <typename T, int ROWS, int NV, bool WARP>
-__global__ void __launch_bounds__(kMaxThreads, NV * sizeof(T) <= 4 ? 2 : 1) layernorm_forward_kernel(const Forward<T> a) {
-    __shared__ float2 red[2][kMaxWarps];   // each warp's mean and sum of squares about it
-    __shared__ float count_of[kMaxWarps];  // its values
+__global__ void __launch_bounds__(kMaxThreads, ROWS != ROWS_VEC && NV * sizeof(T) <= 4 ? 2 : 1) layernorm_forward_kernel(const Forward<T> a) {
+    // of each warp: the mean of its values, the squares about it, and how many they are; zeros behind the last
+    __shared__ __align__(16) float red[2][2][kMaxWarps], count_of[kMaxWarps];
+    constexpr bool AHEAD = loads_ahead<T>(ROWS, NV);
     const int dim = a.dim, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int threads = WARP ? 32 : blockDim.x, tid = WARP ? lane : threadIdx.x;
     const int64_t first = WARP ? (int64_t)blockIdx.x * warps + warp : blockIdx.x;
@@ -119,80 +267,113 @@ __global__ void __launch_bounds__(kMaxThreads, NV * sizeof(T) <= 4 ? 2 : 1) laye
     own = warp_sum(own);
     const float inv_own = own > 0.f ? 1.f / own : 0.f;
     if (!WARP) {
+        for (int i = threadIdx.x; i < 4 * kMaxWarps; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+        if (threadIdx.x < kMaxWarps) count_of[threadIdx.x] = 0.f;
+        __syncthreads();
         if (lane == 0) count_of[warp] = own;
         __syncthreads();
     }
     // the vectors stay in registers where a thread has few pieces
-    float gm[NV <= 2 ? NV : 1][8], bt[NV <= 2 ? NV : 1][8];
-    if (NV <= 2) {
+    Raw8<T> gm[NV <= 4 ? NV : 1], bt[NV <= 4 ? NV : 1];
+    if (NV <= 4) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int col = col0 + k * step;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) bt[k < 2 ? k : 0][i] = 0.f;
+            bt[k < 4 ? k : 0] = Raw8<T>{};
             if (col >= dim) continue;
-            load_vector<ROWS>(a.gamma, col, gm[k < 2 ? k : 0]);
-            if (a.beta.p) load_vector<ROWS>(a.beta, col, bt[k < 2 ? k : 0]);
+            gm[k < 4 ? k : 0] = load_vector<ROWS>(a.gamma, col);
+            if (a.beta.p) bt[k < 4 ? k : 0] = load_vector<ROWS>(a.beta, col);
         }
     }
     int parity = 0;
-    for (int64_t row = first; row < a.rows; row += stride, parity ^= 1) {
-        const int64_t base = row * dim;
-        float s[NV][8];
+    Raw8<T> x[NV], r[NV];
+    auto fetch = [&](int64_t row) {
+        if (row >= a.rows) return;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if (col0 + k * step < dim) load_piece8<ROWS>(a.x, base + col0 + k * step, s[k]);
+            if (col0 + k * step < dim) x[k] = load_piece<ROWS>(a.x, row * dim + col0 + k * step);
         if (a.r.p) {
-            float b[NV][8];
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (col0 + k * step < dim) load_piece8<ROWS>(a.r, base + col0 + k * step, b[k]);
+                if (col0 + k * step < dim) r[k] = load_piece<ROWS>(a.r, row * dim + col0 + k * step);
+        }
+    };
+    if (AHEAD) fetch(first);
+    for (int64_t row = first; row < a.rows; row += stride, parity ^= 1) {
+        const int64_t base = row * dim;
+        Raw8<T> s[NV];
+        if (!AHEAD) fetch(row);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) s[k] = x[k];
+        if (a.r.p) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = col0 + k * step;
                 if (col >= dim) continue;
+                F2 v[4], b[4];
+                values(s[k], v);
+                values(r[k], b);
                 // the stream is held in T: the norm is that of the rounded sum
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[k][i] = to_f(from_f<T>(s[k][i] + b[k][i]));
-                store_piece8<ROWS>(a.s, base, col, dim, s[k]);
+                for (int i = 0; i < 4; ++i) v[i] = v[i] + b[i];
+                raw_of(v, s[k]);
+                store_piece<ROWS>(a.s, base, col, dim, s[k]);
             }
         }
-        float sum = 0.f;
+        if (AHEAD) fetch(row + stride);
+        F2 sums = pair(0.f, 0.f), squares = sums;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (col0 + k * step >= dim) continue;
-            mask_piece<ROWS>(s[k], col0 + k * step, dim);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum += s[k][i];
+            F2 v[4];
+            values(s[k], v);
+            mask_piece<ROWS>(v, col0 + k * step, dim);
+            sums = sums + ((v[0] + v[1]) + (v[2] + v[3]));
         }
-        const float mid = warp_sum(sum) * inv_own;
-        float sq = 0.f;
+        const float mid = warp_sum(sum2(sums)) * inv_own;
+        const F2 minus_mid = pair(-mid, -mid);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int col = col0 + k * step;
             if (col >= dim) continue;
+            F2 v[4];
+            values(s[k], v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = s[k][i] - mid;
-                if (ROWS == ROWS_VEC || (col + i >= 0 && col + i < dim)) sq = fmaf(d, d, sq);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = v[i] + minus_mid;
+            mask_piece<ROWS>(v, col, dim);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) squares = fma2(v[i], v[i], squares);
         }
-        sq = warp_sum(sq);
+        float sq = warp_sum(sum2(squares));
         float mean = mid;
         if (!WARP) {
-            if (lane == 0) red[parity][warp] = make_float2(mid, sq);
+            if (lane == 0) {
+                red[parity][0][warp] = mid;
+                red[parity][1][warp] = sq;
+            }
             __syncthreads();
+            const float4 *mids = reinterpret_cast<const float4 *>(red[parity][0]);
+            const float4 *sqs = reinterpret_cast<const float4 *>(red[parity][1]);
+            const float4 *counts = reinterpret_cast<const float4 *>(count_of);
             mean = 0.f;
-            for (int w = 0; w < warps; ++w) mean = fmaf(count_of[w], red[parity][w].x, mean);
+#pragma unroll
+            for (int i = 0; i < kMaxWarps / 4; ++i) {
+                if (4 * i >= warps) break;
+                const float4 m = mids[i], c = counts[i];
+                mean += fmaf(c.x, m.x, c.y * m.y) + fmaf(c.z, m.z, c.w * m.w);
+            }
             mean *= a.inv_dim;
             sq = 0.f;
-            for (int w = 0; w < warps; ++w) {
-                const float2 p = red[parity][w];
-                const float d = p.x - mean;
-                sq += fmaf(count_of[w] * d, d, p.y);
+#pragma unroll
+            for (int i = 0; i < kMaxWarps / 4; ++i) {
+                if (4 * i >= warps) break;
+                const float4 m = mids[i], c = counts[i], q = sqs[i];
+                const float dx = m.x - mean, dy = m.y - mean, dz = m.z - mean, dw = m.w - mean;
+                sq += (fmaf(c.x * dx, dx, q.x) + fmaf(c.y * dy, dy, q.y)) + (fmaf(c.z * dz, dz, q.z) + fmaf(c.w * dw, dw, q.w));
             }
         }
         const float rs = rsqrtf(fmaf(sq, a.inv_dim, a.eps));
+        const F2 minus_mean = pair(-mean, -mean), scale = pair(rs, rs);
         if (tid == 0) {
             a.mean[row] = mean;
             a.rstd[row] = rs;
@@ -201,17 +382,18 @@ __global__ void __launch_bounds__(kMaxThreads, NV * sizeof(T) <= 4 ? 2 : 1) laye
         for (int k = 0; k < NV; ++k) {
             const int col = col0 + k * step;
             if (col >= dim) continue;
-            if (NV <= 2) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[k][i] = fmaf((s[k][i] - mean) * rs, gm[k < 2 ? k : 0][i], bt[k < 2 ? k : 0][i]);
+            F2 v[4], g[4], b[4];
+            values(s[k], v);
+            if (NV <= 4) {
+                values(gm[k < 4 ? k : 0], g);
+                values(bt[k < 4 ? k : 0], b);
             } else {
-                float g[8], b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                load_vector<ROWS>(a.gamma, col, g);
-                if (a.beta.p) load_vector<ROWS>(a.beta, col, b);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[k][i] = fmaf((s[k][i] - mean) * rs, g[i], b[i]);
+                values(load_vector<ROWS>(a.gamma, col), g);
+                values(a.beta.p ? load_vector<ROWS>(a.beta, col) : Raw8<T>{}, b);
             }
-            store_piece8<ROWS>(a.y, base, col, dim, s[k]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = fma2((v[i] + minus_mean) * scale, g[i], b[i]);
+            store_values<ROWS>(a.y, base, col, dim, v);
         }
     }
 }
@@ -250,6 +432,27 @@ template <int N> __device__ __forceinline__ float warp_sums(float (&v)[N]) {
     return r;
 }
 
+// 8 values of a row in shared memory
+template <typename T> __device__ __forceinline__ Raw8<T> load_shared(const T *p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.a[k] = reinterpret_cast<const uint4 *>(p)[k];
+    return r;
+}
+
+// the sum of what the warps left
+__device__ __forceinline__ float row_sum(const float *red, int warps) {
+    const float4 *p = reinterpret_cast<const float4 *>(red);
+    float4 v = p[0];
+#pragma unroll
+    for (int i = 1; i < kMaxWarps / 4; ++i) {
+        if (4 * i >= warps) break;
+        const float4 x = p[i];
+        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    }
+    return (v.x + v.y) + (v.z + v.w);
+}
+
 __device__ __forceinline__ void group_barrier(int group, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
 }
@@ -261,7 +464,7 @@ template <typename T, int ROWS, int NV, int R>
 __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(const Backward<T> a, unsigned *flag) {
     extern __shared__ __align__(16) unsigned char ring_raw[];
     __shared__ uint64_t full_bars[kMaxGroups][kMaxStages];
-    __shared__ float red_raw[kMaxGroups][2][2 * R][kMaxWarps];
+    __shared__ __align__(16) float red_raw[kMaxGroups][2][2 * R][kMaxWarps];  // zeros behind the last warp
     const int threads = a.threads, group = threadIdx.x / threads, tid = threadIdx.x % threads, groups = blockDim.x / threads;
     const int lane = threadIdx.x & 31, warp = tid >> 5, warps = threads >> 5;
     const int dim = a.dim, tensors = a.ds.p ? 3 : 2;
@@ -271,6 +474,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
     uint64_t *full = full_bars[group];
     unsigned char *ring = ring_raw + (size_t)group * a.stages * R * tensors * a.slot;
     grid_dependency_launch();
+    for (int i = threadIdx.x; i < kMaxGroups * 2 * 2 * R * kMaxWarps; i += blockDim.x) (&red_raw[0][0][0][0])[i] = 0.f;
     if (tid == 0) {
         for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
         fence_mbar_init();
@@ -281,46 +485,51 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
     };
     // one thread of the group asks for a tile's rows
     auto fetch = [&](int64_t tile, int stage) {
-        uint32_t bytes = 0;
-        int64_t from[R];
-        uint32_t size[R];
+        uint32_t bytes = 0, size[R];
+        const int64_t row = first + tile * R * a.stride;
+        int64_t from = row * dim - ph;
+        const int64_t from0 = from, hop = a.stride * dim;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t row = first + (tile * R + r) * a.stride;
+        for (int r = 0; r < R; ++r, from += hop) {
             size[r] = 0;
-            if (row >= a.rows) continue;
-            from[r] = row * dim - ph;
-            const int64_t values = min((int64_t)pieces * 8, a.dy.hi - from[r]);
-            size[r] = (uint32_t)(values * sizeof(T)) & ~15u;
-            if (ROWS != ROWS_VEC) {  // what the tensor's last 16 bytes lack
-                for (int64_t i = size[r] / sizeof(T); i < values; ++i) {
-                    slot_of(stage, r, 0)[i] = a.dy.p[from[r] + i];
-                    slot_of(stage, r, 1)[i] = a.s.p[from[r] + i];
-                    if (tensors == 3) slot_of(stage, r, 2)[i] = a.ds.p[from[r] + i];
+            if (row + r * a.stride >= a.rows) continue;
+            if (ROWS == ROWS_VEC) {
+                size[r] = (uint32_t)dim * sizeof(T);
+            } else {
+                const int64_t values = min((int64_t)pieces * 8, a.dy.hi - from);
+                size[r] = (uint32_t)(values * sizeof(T)) & ~15u;
+                for (int64_t i = size[r] / sizeof(T); i < values; ++i) {  // what the tensor's last 16 bytes lack
+                    slot_of(stage, r, 0)[i] = a.dy.p[from + i];
+                    slot_of(stage, r, 1)[i] = a.s.p[from + i];
+                    if (tensors == 3) slot_of(stage, r, 2)[i] = a.ds.p[from + i];
                 }
             }
             bytes += size[r] * tensors;
         }
         mbar_arrive_expect_tx(&full[stage], bytes);
+        from = from0;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < R; ++r, from += hop) {
             if (!size[r]) continue;
-            bulk_load(slot_of(stage, r, 0), a.dy.p + from[r], size[r], &full[stage]);
-            bulk_load(slot_of(stage, r, 1), a.s.p + from[r], size[r], &full[stage]);
-            if (tensors == 3) bulk_load(slot_of(stage, r, 2), a.ds.p + from[r], size[r], &full[stage]);
+            bulk_load(slot_of(stage, r, 0), a.dy.p + from, size[r], &full[stage]);
+            bulk_load(slot_of(stage, r, 1), a.s.p + from, size[r], &full[stage]);
+            if (tensors == 3) bulk_load(slot_of(stage, r, 2), a.ds.p + from, size[r], &full[stage]);
         }
     };
     const int64_t own_rows = first < a.rows ? (a.rows - first + a.stride - 1) / a.stride : 0;
     const int64_t tiles = (own_rows + R - 1) / R;
     if (tid == 0)
         for (int i = 0; i < a.stages && i < tiles; ++i) fetch(i, i);
-    float dg[NV][8], db[NV][8], gm[NV][8];
+    const F2 zero = pair(0.f, 0.f);
+    F2 dg[NV][4], db[NV][4], gm[NV][4];
+    Raw8<T> own[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dg[k][i] = db[k][i] = gm[k][i] = 0.f;
+        for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = gm[k][i] = zero;
         const int j = tid + k * threads;
-        if (j < pieces) load_vector<ROWS>(a.gamma, j * 8 - ph, gm[k]);
+        if (j < pieces) values(load_vector<ROWS>(a.gamma, j * 8 - ph), gm[k]);
+        own[k] = row_words<T>(j * 8 - ph, dim);
     }
     float mean[R], rstd[R];
     auto fetch_statistics = [&](int64_t tile) {
@@ -340,39 +549,44 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
     for (int64_t tile = 0; tile < tiles; ++tile) {
         // a wait that gives up leaves its code in the flag; later ones do not wait again
         ok = ok && mbar_wait_bounded(&full[stage], phase, flag, 0x701u);
-        float mu[R], rs[R], sums[2 * R];
+        float rs[R], sums[2 * R];
+        F2 c[R][NV][4], g[R][NV][4];  // s - mean and rstd gamma dy
+        Raw8<T> add[R][NV];
+        const int64_t left = own_rows - tile * R;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            mu[r] = mean[r];
             rs[r] = rstd[r];
             sums[2 * r] = sums[2 * r + 1] = 0.f;
-        }
-        const int64_t left = own_rows - tile * R;
-        if (tile + 1 < tiles) fetch_statistics(tile + 1);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
             if (r >= left) continue;
+            const F2 minus_mean = pair(-mean[r], -mean[r]), scale = pair(rs[r], rs[r]);
+            F2 s1 = zero, s2 = zero;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int j = tid + k * threads;
                 if (j >= pieces) continue;
-                float d[8], n[8];
-                load8(slot_of(stage, r, 0) + j * 8, d);
-                load8(slot_of(stage, r, 1) + j * 8, n);
+                F2 d[4];
+                Raw8<T> dy = load_shared(slot_of(stage, r, 0) + j * 8), x = load_shared(slot_of(stage, r, 1) + j * 8);
+                if (tensors == 3) add[r][k] = load_shared(slot_of(stage, r, 2) + j * 8);
+                // of the rows in front and behind: dy 0, s 0, so that their products are 0 whatever they hold
+                keep_words<ROWS>(dy, own[k]);
+                keep_words<ROWS>(x, own[k]);
+                values(dy, d);
+                values(x, c[r][k]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) n[i] = (n[i] - mu[r]) * rs[r];
-                mask_piece<ROWS>(d, j * 8 - ph, dim);
-                mask_piece<ROWS>(n, j * 8 - ph, dim);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dg[k][i] = fmaf(d[i], n[i], dg[k][i]);
-                    db[k][i] += d[i];
-                    const float g = d[i] * gm[k][i];
-                    sums[2 * r] += g;
-                    sums[2 * r + 1] = fmaf(g, n[i], sums[2 * r + 1]);
+                for (int i = 0; i < 4; ++i) {
+                    c[r][k][i] = c[r][k][i] + minus_mean;
+                    db[k][i] = db[k][i] + d[i];
+                    d[i] = d[i] * scale;
+                    dg[k][i] = fma2(d[i], c[r][k][i], dg[k][i]);
+                    g[r][k][i] = d[i] * gm[k][i];
+                    s1 = s1 + g[r][k][i];
+                    s2 = fma2(g[r][k][i], c[r][k][i], s2);
                 }
             }
+            sums[2 * r] = sum2(s1);
+            sums[2 * r + 1] = sum2(s2);
         }
+        if (tile + 1 < tiles) fetch_statistics(tile + 1);
         float (*red)[kMaxWarps] = red_raw[group][tile & 1];
         {
             const float v = warp_sums(sums);
@@ -380,34 +594,29 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
             if (lane % LANES == 0) red[lane / LANES][warp] = v;
         }
         group_barrier(group, threads);
-        // the tile in front is done with: its place is for the one `stages` behind it
-        if (tid == 0 && tile > 0 && tile - 1 + a.stages < tiles)
-            fetch(tile - 1 + a.stages, stage == 0 ? a.stages - 1 : stage - 1);
+        // the tile is in registers: its place is for the one `stages` behind it
+        if (tid == 0 && tile + a.stages < tiles) fetch(tile + a.stages, stage);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r >= left) continue;
-            float m1 = 0.f, m2 = 0.f;
-            for (int w = 0; w < warps; ++w) {
-                m1 += red[2 * r][w];
-                m2 += red[2 * r + 1][w];
-            }
-            m1 *= a.inv_dim;
-            m2 *= a.inv_dim;
+            // rstd mean g and rstd^2 mean(g n), negative
+            const float m1 = -row_sum(red[2 * r], warps) * a.inv_dim;
+            const float m2 = -row_sum(red[2 * r + 1], warps) * a.inv_dim * rs[r] * rs[r];
+            const F2 m1s = pair(m1, m1), m2s = pair(m2, m2);
             const int64_t row = first + (tile * R + r) * a.stride;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int j = tid + k * threads;
                 if (j >= pieces) continue;
-                float d[8], n[8], b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                load8(slot_of(stage, r, 0) + j * 8, d);
-                load8(slot_of(stage, r, 1) + j * 8, n);
-                if (tensors == 3) load8(slot_of(stage, r, 2) + j * 8, b);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float t = fmaf(d[i], gm[k][i], -m1) - (n[i] - mu[r]) * rs[r] * m2;
-                    b[i] = fmaf(rs[r], t, b[i]);
+                for (int i = 0; i < 4; ++i) g[r][k][i] = fma2(c[r][k][i], m2s, g[r][k][i] + m1s);
+                if (tensors == 3) {
+                    F2 b[4];
+                    values(add[r][k], b);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) g[r][k][i] = g[r][k][i] + b[i];
                 }
-                store_piece8<ROWS>(a.dx, row * dim, j * 8 - ph, dim, b);
+                store_values<ROWS>(a.dx, row * dim, j * 8 - ph, dim, g[r][k]);
             }
         }
         if (++stage == a.stages) {
@@ -426,8 +635,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (col + i >= 0 && col + i < dim) {
-                    share[(size_t)group * 2 * a.pitch + col + i] = dg[k][i];
-                    share[(size_t)group * 2 * a.pitch + a.pitch + col + i] = db[k][i];
+                    share[(size_t)group * 2 * a.pitch + col + i] = i & 1 ? both(dg[k][i / 2]).y : both(dg[k][i / 2]).x;
+                    share[(size_t)group * 2 * a.pitch + a.pitch + col + i] = i & 1 ? both(db[k][i / 2]).y : both(db[k][i / 2]).x;
                 }
         }
         __syncthreads();
@@ -445,8 +654,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (col + i >= 0 && col + i < dim) {
-                out[col + i] = dg[k][i];
-                out[a.pitch + col + i] = db[k][i];
+                out[col + i] = i & 1 ? both(dg[k][i / 2]).y : both(dg[k][i / 2]).x;
+                out[a.pitch + col + i] = i & 1 ? both(db[k][i / 2]).y : both(db[k][i / 2]).x;
             }
     }
 }
@@ -501,26 +710,48 @@ __global__ void __launch_bounds__(kMaxThreads) layernorm_dx_kernel(const Backwar
             if (a.ds.p) load_any(a.ds, a.ds.lo + base + col, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) b[i] = fmaf(rs, d[i] - m1 - n[i] * m2, b[i]);
-            store_piece8<ROWS_ANY>(a.dx, base, col, dim, b);
+            store_values<ROWS_ANY>(a.dx, base, col, dim, b);
         }
     }
 }
-// The vectors' gradients beside it: a thread per column, blockIdx.y a share of the rows.
+// The vectors' gradients beside it: a warp's threads have 8 columns each, the block's 8
+// warps and blockIdx.y shares of the rows.
 template <typename T> __global__ void __launch_bounds__(256) layernorm_columns_kernel(const Backward<T> a) {
-    const int col = blockIdx.x * 256 + threadIdx.x;
+    __shared__ float red[8][2][256];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col0 = blockIdx.x * 256 + lane * 8;
     grid_dependency_launch();
-    if (col >= a.dim) return;
-    const T *dy = a.dy.p + a.dy.lo + col, *s = a.s.p + a.s.lo + col;
-    float dg = 0.f, db = 0.f;
-#pragma unroll 4
-    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        const float d = to_f(dy[row * a.dim]);
-        dg = fmaf(d, (to_f(s[row * a.dim]) - a.mean[row]) * a.rstd[row], dg);
-        db += d;
+    float dg[8], db[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dg[i] = db[i] = 0.f;
+    if (col0 < a.dim) {
+#pragma unroll 2
+        for (int64_t row = (int64_t)blockIdx.y * 8 + warp; row < a.rows; row += gridDim.y * 8) {
+            const float mu = a.mean[row], rs = a.rstd[row];
+            float d[8], n[8];
+            load_any(a.dy, a.dy.lo + row * a.dim + col0, d);
+            load_any(a.s, a.s.lo + row * a.dim + col0, n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // what lies behind the row reaches columns that nobody asks for
+                dg[i] = fmaf(d[i], (n[i] - mu) * rs, dg[i]);
+                db[i] += d[i];
+            }
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        red[warp][0][lane * 8 + i] = dg[i];
+        red[warp][1][lane * 8 + i] = db[i];
+    }
+    __syncthreads();
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col >= a.dim) return;
     float *out = a.partial + (int64_t)blockIdx.y * 2 * a.pitch + col;
-    out[0] = dg;
-    out[a.pitch] = db;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float v = red[0][k][threadIdx.x];
+        for (int w = 1; w < 8; ++w) v += red[w][k][threadIdx.x];
+        out[k * a.pitch] = v;
+    }
 }
 
 // dgamma[j] (blockIdx.y 0) and dbeta[j] (1) from the blocks' partials: 32 columns
@@ -551,52 +782,37 @@ int rows_of(int dim, std::initializer_list<const void *> tensors) {
     return dim % 8 == 0 ? ROWS_VEC : ROWS_ODD;
 }
 
-// Forward: pieces and threads of a row; a warp has a row to itself up to 2 pieces a lane.
+// Forward: pieces per thread and threads of a row.  A warp has a row to itself up to 256 or 512 values
+// (bf16: 1024).  Then 2 pieces, or 4 of aligned bf16 (fewer warps wait at a row's barrier): cold, 2 / 4 pieces,
+// bf16 65536 x 1024 91 / 89 us, x 2048 178 / 163, 16384 x 8192 205 / 185; fp32 16384 x 4096 172 / 176,
+// 8192 x 8192 233 / 202; odd 32768 x 2046 153 / 162.  Rows above 8192 take as many as there are (bf16
+// 4096 x 16384 with 8 pieces 92 us, 126 with 4 and twice the warps).
 struct Shape {
     int nv, threads;
 };
-Shape forward_shape(int dim, int rows) {
+template <typename T> Shape forward_shape(int dim, int rows) {
     const int64_t pieces = rows == ROWS_VEC ? dim / 8 : (dim + 14) / 8;
     int nv = pieces <= 32 ? 1 : 2;
-    while (nv < 8 && pieces > kMaxThreads * nv) nv *= 2;
-    if (pieces > kMaxThreads * nv) nv = kMaxPieces;
+    if (rows == ROWS_VEC && pieces > (sizeof(T) == 2 ? 64 : kMaxThreads)) nv = 4;
+    if (pieces > kMaxThreads * 2) nv = rows == ROWS_VEC ? 8 : kMaxPieces;
     return {nv, (int)round_up(ceil_div(pieces, nv), 32)};
 }
 
-template <typename F> int with_nv(int nv, F &&f) {
-    switch (nv) {
-        case 1: return f(std::integral_constant<int, 1>{});
-        case 2: return f(std::integral_constant<int, 2>{});
-        case 4: return f(std::integral_constant<int, 4>{});
-        case 8: return f(std::integral_constant<int, 8>{});
-        default: return f(std::integral_constant<int, kMaxPieces>{});
-    }
-}
-// the layout of vector rows, which never take the ninth piece
-constexpr int vec_rows(int nv) { return nv == kMaxPieces ? ROWS_ODD : ROWS_VEC; }
-
-template <typename T> int run_forward(const Forward<T> &a, int rows, cudaStream_t st) {
-    const Shape sh = forward_shape(a.dim, rows);
-    return with_nv(sh.nv, [&](auto nv) -> int {
-        constexpr int NV = decltype(nv)::value;
-        if (NV <= 2 && sh.threads == 32) {  // a warp per row, 8 rows per block
-            const int64_t grid = std::min<int64_t>(ceil_div(a.rows, 8), (int64_t)num_sms() * 8);
-            constexpr int N = NV <= 2 ? NV : 1;
-            auto *k = rows == ROWS_VEC   ? &layernorm_forward_kernel<T, ROWS_VEC, N, true>
-                      : rows == ROWS_ODD ? &layernorm_forward_kernel<T, ROWS_ODD, N, true>
-                                         : &layernorm_forward_kernel<T, ROWS_ANY, N, true>;
-            SPCO_LAUNCH("layernorm_forward", st, k<<<(unsigned)grid, 256, 0, st>>>(a));
-        } else {
-            // multiples of 8 blocks: a block's rows then begin alike
-            const int64_t grid = std::min<int64_t>(a.rows, (int64_t)num_sms() * 64);
-            auto *k = rows == ROWS_VEC   ? &layernorm_forward_kernel<T, vec_rows(NV), NV, false>
-                      : rows == ROWS_ODD ? &layernorm_forward_kernel<T, ROWS_ODD, NV, false>
-                                         : &layernorm_forward_kernel<T, ROWS_ANY, NV, false>;
-            SPCO_LAUNCH("layernorm_forward", st, k<<<(unsigned)grid, sh.threads, 0, st>>>(a));
-        }
-        SPECOPTIM_LAUNCHED("layernorm_forward_kernel");
-        return SPECOPTIM_OK;
-    });
+template <typename T, int ROWS> int run_forward(const Forward<T> &a, cudaStream_t st) {
+    const Shape sh = forward_shape<T>(a.dim, ROWS);
+    constexpr bool VEC = ROWS == ROWS_VEC;
+    const bool warp = sh.threads == 32;
+    auto *k = sh.nv == 1   ? &layernorm_forward_kernel<T, ROWS, 1, true>
+              : sh.nv == 2 ? (warp ? &layernorm_forward_kernel<T, ROWS, 2, true> : &layernorm_forward_kernel<T, ROWS, 2, false>)
+              : sh.nv == 4 ? (warp ? &layernorm_forward_kernel<T, ROWS, VEC && sizeof(T) == 2 ? 4 : 1, true>
+                                   : &layernorm_forward_kernel<T, ROWS, VEC ? 4 : 2, false>)
+                           : &layernorm_forward_kernel<T, ROWS, VEC ? 8 : kMaxPieces, false>;
+    // 8 rows per block, or multiples of 8 blocks: a thread's rows then begin alike
+    const int64_t grid = warp ? std::min<int64_t>(ceil_div(a.rows, 8), (int64_t)num_sms() * 8)
+                              : std::min<int64_t>(a.rows, (int64_t)num_sms() * 64);
+    SPCO_LAUNCH("layernorm_forward", st, k<<<(unsigned)grid, warp ? 256 : sh.threads, 0, st>>>(a));
+    SPECOPTIM_LAUNCHED("layernorm_forward_kernel");
+    return SPECOPTIM_OK;
 }
 
 // Backward: how a launch is cut.
@@ -606,29 +822,26 @@ struct Plan {
     int groups, blocks;
     int tile, stages, slot, smem;
 };
-constexpr int kRingDim = 8192;
-
 Plan backward_plan(int64_t rows, int dim, int layout, int value_bytes, int tensors) {
     Plan p{};
-    if (layout == ROWS_ANY || dim > kRingDim) {
-        p.blocks = (int)std::max<int64_t>(1, std::min<int64_t>({rows, num_sms() * 4, 512}));
+    const int pieces = layout == ROWS_VEC ? dim / 8 : (dim + 14) / 8;
+    if (layout == ROWS_ANY || pieces > 2 * kMaxThreads) {
+        // shares of the rows beside the columns' blocks, 8 rows at a time each
+        p.blocks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(rows, 8), ceil_div(num_sms() * 8, ceil_div(dim, 256))));
         return p;
     }
     p.ring = true;
-    const int pieces = layout == ROWS_VEC ? dim / 8 : (dim + 14) / 8;
-    p.nv = pieces <= kMaxThreads ? 1 : pieces <= 2 * kMaxThreads ? 2 : 4;
+    p.nv = pieces <= kMaxThreads ? 1 : 2;
     p.threads = (int)round_up(ceil_div(pieces, p.nv), 32);
     p.groups = std::max(1, std::min(kMaxGroups, 256 / p.threads));
     p.slot = (int)round_up((int64_t)pieces * 8 * value_bytes, 16);
-    p.tile = 2;
-    p.stages = 3;
-    const int row_bytes = p.slot * tensors;
-    const int room = 220 * 1024;
-    while (p.stages > 2 && p.groups * p.stages * p.tile * row_bytes > room) --p.stages;
-    if (p.groups * p.stages * p.tile * row_bytes > room) p.tile = 1;
-    p.smem = std::max<int>(p.groups * p.stages * p.tile * row_bytes,
-                           p.groups > 1 ? p.groups * 2 * (int)round_up(dim, 8) * 4 : 0);
-    const int per_sm = std::max(1, std::min({room / (p.smem + 3072), 1024 / (p.threads * p.groups)}));
+    // Two rows a tile: a barrier and its sums for two (bf16 65536 x 2048: 179 us, 206 with one; four spill).
+    // 512 threads an SM: the ring's bytes are in flight all the same (163 against 171 us without ds).
+    p.tile = p.nv == 1 ? 2 : 1;
+    const int stage_bytes = p.groups * p.tile * p.slot * tensors, room = 220 * 1024;
+    p.stages = std::max(1, std::min(3, room / stage_bytes));
+    p.smem = std::max<int>(p.stages * stage_bytes, p.groups > 1 ? p.groups * 2 * (int)round_up(dim, 8) * 4 : 0);
+    const int per_sm = std::max(1, std::min(room / (p.smem + 3072), 512 / (p.threads * p.groups)));
     p.blocks = (int)std::min<int64_t>(ceil_div(rows, p.groups), (int64_t)num_sms() * per_sm / 8 * 8);
     p.blocks = std::max(p.blocks, 1);
     return p;
@@ -641,16 +854,12 @@ template <typename T> int run_backward(Backward<T> a, const Plan &p, int layout,
         a.slot = p.slot;
         a.stages = p.stages;
         a.stride = (int64_t)p.blocks * p.groups;
-        auto pick = [&](auto nv) {
-            constexpr int NV = decltype(nv)::value;
-            return layout == ROWS_VEC ? (p.tile == 2 ? &layernorm_backward_kernel<T, ROWS_VEC, NV, 2>
-                                                     : &layernorm_backward_kernel<T, ROWS_VEC, NV, 1>)
-                                      : (p.tile == 2 ? &layernorm_backward_kernel<T, ROWS_ODD, NV, 2>
-                                                     : &layernorm_backward_kernel<T, ROWS_ODD, NV, 1>);
+        auto pick = [&](auto rows) {
+            constexpr int ROWS = decltype(rows)::value;
+            return p.nv == 2     ? &layernorm_backward_kernel<T, ROWS, 2, 1>
+                                 : &layernorm_backward_kernel<T, ROWS, 1, 2>;
         };
-        auto *k = p.nv == 1   ? pick(std::integral_constant<int, 1>{})
-                  : p.nv == 2 ? pick(std::integral_constant<int, 2>{})
-                              : pick(std::integral_constant<int, 4>{});
+        auto *k = layout == ROWS_VEC ? pick(std::integral_constant<int, ROWS_VEC>{}) : pick(std::integral_constant<int, ROWS_ODD>{});
         if (int rc = set_smem_limit(reinterpret_cast<const void *>(k), p.smem)) return rc;
         SPCO_LAUNCH("layernorm_backward", st,
                     k<<<p.blocks, p.threads * p.groups, p.smem, st>>>(a, device_flag_ptr()));
@@ -717,7 +926,10 @@ extern "C" int layernorm_forward(const void *x, const void *r, const void *gamma
                                dim,
                                1.f / (float)dim,
                                eps};
-            return run_forward<T>(a, layout, static_cast<cudaStream_t>(stream));
+            cudaStream_t st = static_cast<cudaStream_t>(stream);
+            return layout == ROWS_VEC   ? run_forward<T, ROWS_VEC>(a, st)
+                   : layout == ROWS_ODD ? run_forward<T, ROWS_ODD>(a, st)
+                                        : run_forward<T, ROWS_ANY>(a, st);
         });
     });
 }

@@ -315,7 +315,7 @@ struct Policy {
     int counted;             // its blocks
     int64_t units;
     int per_sequence, reduction, ctas, count_here;
-    float kl_coef, grad_scale, edge_high, edge_low;
+    float kl_coef, grad_scale, edge_high, edge_low;  // edges: the bounds' distance from 1
     Two log_high, log_low;   // log(1 + clip_high), log(1 - clip_low)
 };
 
@@ -438,8 +438,10 @@ template <bool VEC> __global__ void __launch_bounds__(kThreads) policy_kernel(co
                     const Two d = two_sum(lp[i], -lo[i]), edge = gains ? a.log_high : a.log_low;
                     const float past = (d.hi - edge.hi) + (d.lo - edge.lo);
                     const bool clipped = gains ? past > 0.f : past < 0.f;
-                    const float ratio = clipped ? (gains ? a.edge_high : a.edge_low) : expf(d.hi);
-                    const float gain = ad[i] * ratio;
+                    // A r as A + A (r - 1): expm1 is exact to its own size, so the sum over many
+                    // tokens whose advantages cancel has no bias from exp's last place
+                    const float above = clipped ? (gains ? a.edge_high : a.edge_low) : expm1f(d.hi);
+                    const float gain = fmaf(ad[i], above, ad[i]);
                     float slope = clipped ? 0.f : -gain, kl = 0.f;
                     if (a.ref) {
                         const float q = lr[i] - lp[i], e = expm1f(q);
@@ -668,7 +670,7 @@ extern "C" int policy_loss(const float *logp, const float *old_logp, const float
         }
         const Policy a{q, logp, old_logp, ref_logp, advantages, dlogp, partial, parts, loss, apart ? counts : nullptr, counted,
                        units, per_sequence != 0, reduction, ctas, counting && !apart, kl_coef, grad_scale,
-                       (float)(1. + clip_high), (float)(1. - clip_low), log_two(1. + clip_high), log_two(1. - clip_low)};
+                       (float)clip_high, (float)-clip_low, log_two(1. + clip_high), log_two(1. - clip_low)};
         auto *k = vec ? &policy_kernel<true> : &policy_kernel<false>;
         SPCO_LAUNCH("policy_loss", st, e = launch_clusters(k, blocks, ctas, apart, st, a));
         SPECOPTIM_CUDA(e);
