@@ -75,13 +75,14 @@ int head_logp_backward(const float *dlogp, const float *kept, const void *h, con
 
 /* Sequences of the losses below: packed one behind the other in [tokens]
  * arrays, sequence i at offsets[i] .. offsets[i + 1] - 1 (int32 or int64,
- * offset_bytes 4 or 8; not descending, within [0, tokens]).  A sequence may be
- * empty.  Tokens in front of the first and behind the last one belong to none:
+ * offset_bytes 4 or 8; not descending, within [0, tokens]).  At most 2^30 tokens
+ * and sequences.  A sequence may be empty.  Tokens in front of the first and behind the last one belong to none:
  * their dlogp is 0 and nothing else of them is used.  mask: [tokens] bytes, a
  * token counts where it is not 0 (NULL: all count); what the arrays hold at
  * tokens that do not count, infinities and NaN too, reaches no output.  Offsets
- * that break the rule are moved into it and reported as SPECOPTIM_ERR_BOUNDS by
- * the next specoptim_check_device. */
+ * that break the rule are moved into it, so that nothing outside the arrays is
+ * touched, and reported as SPECOPTIM_ERR_BOUNDS by the next
+ * specoptim_check_device; what such a call returns is not defined. */
 
 #define PREFERENCE_LOGISTIC 0
 #define PREFERENCE_HINGE 1
