@@ -28,6 +28,7 @@
 #include <string>
 
 #include "../../include/finetune.h"
+#include "f32x2.cuh"
 #include "rowvec.cuh"
 
 namespace spco {
@@ -42,41 +43,6 @@ static_assert(kMaxThreads * kMaxPieces >= (kMaxDim + 14) / 8, "the widest row at
 // How the rows lie: multiples of 16 bytes from a 16-byte boundary; not multiples,
 // but all tensors from a 16-byte boundary; anything else.
 enum Rows : int { ROWS_VEC = 0, ROWS_ODD = 1, ROWS_ANY = 2 };
-
-// Two fp32 values that one instruction works on.  These kernels have little time per
-// byte, and what they run out of is issue slots.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 pair(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 both(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ float sum2(F2 a) {
-    const float2 f = both(a);
-    return f.x + f.y;
-}
 
 // 8 values as they lie in memory
 template <typename T> struct Raw8 {
