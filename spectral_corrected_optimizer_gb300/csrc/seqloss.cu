@@ -29,9 +29,11 @@
 namespace spco {
 namespace {
 
-constexpr int kFewThreads = 128, kMiddleThreads = 256, kManyThreads = 512;  // of a block
+constexpr int kFewThreads = 128, kManyThreads = 512;  // of a block
 constexpr int kMaxCluster = 8;
-constexpr int kTile = 1024, kTileThreads = 128;  // tokens of a tile (and of a unit where there are no sequences)
+constexpr int kTile = 512, kTileThreads = 128;  // tokens of a tile: 4 per thread
+constexpr int kTileBlocks = 7;                  // an SM holds at once
+constexpr int kUnit = 1024;                     // tokens of a unit where there are no sequences
 constexpr int kMaxBlocksPerSm = 64;  // of a launch: the hardware hands blocks out as others end, which evens out long units
 
 // ---- two floats ----------------------------------------------------------------------------
@@ -78,45 +80,27 @@ __device__ __forceinline__ Two2 two_sum(F2 a, F2 b) {
     return {s, (a - (s - t)) + (b - t)};
 }
 
-// exp(x) - 1 and exp(x) - 1 - x.  Below 1 by the series of the latter, whose next term is below 2^-24 of the
-// first one; neither loses digits then, nor costs what expm1f does.
-struct Exp {
-    F2 above, rest;
-};
-__device__ __forceinline__ Exp exp_of(F2 x) {
-    const auto both_of = [](float c) { return pair(c, c); };
-    F2 p = both_of(1.f / 3628800.f);
-    p = fma2(p, x, both_of(1.f / 362880.f));
-    p = fma2(p, x, both_of(1.f / 40320.f));
-    p = fma2(p, x, both_of(1.f / 5040.f));
-    p = fma2(p, x, both_of(1.f / 720.f));
-    p = fma2(p, x, both_of(1.f / 120.f));
-    p = fma2(p, x, both_of(1.f / 24.f));
-    p = fma2(p, x, both_of(1.f / 6.f));
-    p = fma2(p, x, both_of(0.5f));
-    Exp e;
-    e.rest = p * x * x;
-    e.above = x + e.rest;
-    const float2 v = both(x);
-    if (!(fabsf(v.x) < 1.f && fabsf(v.y) < 1.f)) {
-        float2 above = both(e.above), rest = both(e.rest);
-        if (!(fabsf(v.x) < 1.f)) {
-            above.x = expm1f(v.x);
-            rest.x = above.x - v.x;
-        }
-        if (!(fabsf(v.y) < 1.f)) {
-            above.y = expm1f(v.y);
-            rest.y = above.y - v.y;
-        }
-        e = {pair(above.x, above.y), pair(rest.x, rest.y)};
-    }
-    return e;
+// exp(x) - 1 - x for |x| < 1, by its series, whose next term is below 2^-24 of the first one: neither this nor
+// x + this loses digits, and both cost less than expm1f does.
+__device__ __forceinline__ float exp_rest(float x) {
+    float p = 1.f / 3628800.f;
+    p = fmaf(p, x, 1.f / 362880.f);
+    p = fmaf(p, x, 1.f / 40320.f);
+    p = fmaf(p, x, 1.f / 5040.f);
+    p = fmaf(p, x, 1.f / 720.f);
+    p = fmaf(p, x, 1.f / 120.f);
+    p = fmaf(p, x, 1.f / 24.f);
+    p = fmaf(p, x, 1.f / 6.f);
+    p = fmaf(p, x, 0.5f);
+    return p * x * x;
 }
+// exp(x) - 1 of any x, out of line: it is rare, and its copies would crowd the instruction cache
+__device__ __noinline__ float exp_above(float x) { return expm1f(x); }
 
 // ---- the tokens ----------------------------------------------------------------------------
 
 struct Sequences {
-    const void *offsets;  // null: units of kTile tokens each
+    const void *offsets;  // null: units of kUnit tokens each
     int wide;             // 8-byte offsets
     int count, tokens;
     const uint8_t *mask;
@@ -127,8 +111,8 @@ struct Sequences {
     }
     // where sequence i begins, within the tokens
     __device__ __forceinline__ int begin(int i) const {
-        if (!offsets) return (int)min((int64_t)i * kTile, (int64_t)tokens);
-        return (int)min(max(raw(i), (int64_t)0), (int64_t)tokens);
+        if (!offsets) return (int)min((int64_t)i * kUnit, (int64_t)tokens);
+        return (int)min((uint64_t)raw(i), (uint64_t)tokens);
     }
     // whether the offsets i .. i + n keep the rule
     __device__ __forceinline__ void check(int i, int n) const {
@@ -224,22 +208,11 @@ __device__ __forceinline__ float load_peer(const float *p, uint32_t rank) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(p, rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ int load_peer(const int *p, uint32_t rank) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
-    return v;
-}
 // every thread of the cluster's CTAs
 __device__ __forceinline__ void sync_ctas() {
     __syncwarp();
     cluster_sync();
 }
-
-// How the CTAs of a launch share the units: `ctas` of a cluster take one together; or, few units (alone), the
-// launch is one cluster, each CTA has units of its own and the CTAs join their losses at the end.
-struct Share {
-    int ctas, alone;
-};
 
 // x - a, rounded once
 __device__ __forceinline__ float below(float x, const Two &a) {
@@ -253,164 +226,224 @@ __device__ __forceinline__ float below(float x, const Two &a) {
 struct Preference {
     Sequences q;
     const float *logp, *ref;
-    float *dlogp, *pair_loss, *rewards, *partial, *loss;
-    Share share;
-    int pairs;
+    float *dlogp, *pair_loss, *rewards, *loss;
+    float4 *scores;  // [pairs][slices][2]: hi, lo and count of a slice
+    int pairs, slice_bits;  // 2^slice_bits slices of a pair
+    int alone;       // the launch is one cluster, which forms the loss too
     int kind, average;
     float beta, smoothing, weight, loss_weight;  // weight: grad_scale / pairs or grad_scale
 };
 
-// What a CTA, or a warp, has of a sequence.
+// What a thread, a warp or a block has of a sequence.
 struct Score {
     Two sum;
     int count;
 };
 
-// Half of the CTA's warps have the chosen sequence, half the other one.
+// A sequence of a pair, and the pieces of it that a block has to do with.
+struct Part {
+    int from, to, first, last;
+};
+__device__ __forceinline__ Part part_of(const Preference &a, int p, int side, int slice) {
+    const int a0 = a.q.begin(2 * p), a1 = max(a0, a.q.begin(2 * p + 1)), a2 = max(a1, a.q.begin(2 * p + 2));
+    const int from = side ? a1 : a0, to = side ? a2 : a1;
+    const Pieces pieces(from, to);
+    const int64_t n = pieces.last - pieces.first;
+    return {from, to, pieces.first + (int)(n * slice >> a.slice_bits), pieces.first + (int)(n * (slice + 1) >> a.slice_bits)};
+}
+
+template <bool VEC> __device__ __forceinline__ Score score_of(const Preference &a, const Part &part, int at, int step) {
+    constexpr int U = 4;
+    F2 sum = pair(0.f, 0.f), lost = sum;
+    int count = 0;
+    for (int p0 = part.first + at; p0 < part.last; p0 += step * U) {
+        float4 x[U], r[U];
+        unsigned m[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int piece = p0 + u * step;
+            m[u] = 0;
+            if (piece >= part.last) continue;
+            m[u] = counting<VEC>(a.q.mask, piece, part.from, part.to, a.q.tokens);
+            x[u] = load4<VEC>(a.logp, piece, a.q.tokens);
+            r[u] = a.ref ? load4<VEC>(a.ref, piece, a.q.tokens) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!m[u]) continue;
+            const float d0 = counts(m[u], 0) ? x[u].x - r[u].x : 0.f, d1 = counts(m[u], 1) ? x[u].y - r[u].y : 0.f;
+            const float d2 = counts(m[u], 2) ? x[u].z - r[u].z : 0.f, d3 = counts(m[u], 3) ? x[u].w - r[u].w : 0.f;
+            const Two2 once = two_sum(sum, pair(d0, d1)), twice = two_sum(once.hi, pair(d2, d3));
+            sum = twice.hi;
+            lost = lost + (once.lo + twice.lo);
+            if (a.average) count += nonzero_bytes(m[u]);
+        }
+    }
+    const float2 hi = both(sum), lo = both(lost);
+    Score v{{hi.x, lo.x}, count};
+    add(v.sum, Two{hi.y, lo.y});
+    return v;
+}
+// Sums over lanes that differ in the bits below `lanes`.
+__device__ __forceinline__ void lanes_add(Score &v, int lanes) {
+    for (int o = lanes / 2; o >= 1; o >>= 1) {
+        add(v.sum, shuffled(v.sum, o));
+        v.count += __shfl_xor_sync(0xffffffffu, v.count, o);
+    }
+}
+// The block's sums, the first half of its warps having one sequence and the second half the other: to warp 0's
+// lanes 0 and WARPS / 2.  One barrier.
+template <int WARPS> __device__ __forceinline__ void block_scores(Score &v, Score *warps_of) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    lanes_add(v, 32);
+    if (lane == 0) warps_of[warp] = v;
+    __syncthreads();
+    if (warp) return;
+    v = warps_of[lane % WARPS];
+    lanes_add(v, WARPS / 2);
+}
+
+struct Outcome {
+    Two reward[2], delta;
+    float slope[2];  // of the loss by each sequence's tokens
+};
+__device__ __forceinline__ Outcome outcome_of(const Preference &a, const Score &chosen, const Score &other) {
+    Outcome o;
+    o.reward[0] = times(finished(chosen.sum), a.beta);
+    o.reward[1] = times(finished(other.sum), a.beta);
+    if (a.average) {
+        o.reward[0] = divided(o.reward[0], (float)max(chosen.count, 1));
+        o.reward[1] = divided(o.reward[1], (float)max(other.count, 1));
+    }
+    o.delta = o.reward[0];
+    add(o.delta, Two{-o.reward[1].hi, -o.reward[1].lo});
+    const float d = value(o.delta);
+    float slope;
+    if (a.kind == PREFERENCE_LOGISTIC) {
+        const float up = 1.f / (1.f + expf(-d)), down = 1.f / (1.f + expf(d));
+        slope = a.smoothing * up - (1.f - a.smoothing) * down;
+    } else if (a.kind == PREFERENCE_HINGE) {
+        const float gap = below(1.f, o.delta);
+        slope = gap <= 0.f ? 0.f : gap == gap ? -1.f : gap;  // NaN stays
+    } else {
+        slope = -2.f * (below(0.5f, o.delta) / a.beta) / a.beta;
+    }
+    slope *= a.beta * a.weight;
+    o.slope[0] = a.average ? slope / (float)max(chosen.count, 1) : slope;
+    o.slope[1] = a.average ? -slope / (float)max(other.count, 1) : -slope;
+    return o;
+}
+// Writes what is known of a pair; its loss.
+__device__ __forceinline__ float report(const Preference &a, int p, const Outcome &o) {
+    const float d = value(o.delta);
+    float l;
+    if (a.kind == PREFERENCE_LOGISTIC) {
+        const float soft = log1pf(expf(-fabsf(d)));
+        l = (1.f - a.smoothing) * (soft + fmaxf(-d, 0.f));
+        if (a.smoothing > 0.f) l += a.smoothing * (soft + fmaxf(d, 0.f));
+    } else if (a.kind == PREFERENCE_HINGE) {
+        const float gap = below(1.f, o.delta);
+        l = gap <= 0.f ? 0.f : gap;
+    } else {
+        const float gap = below(0.5f, o.delta) / a.beta;
+        l = gap * gap;
+    }
+    a.pair_loss[p] = l;
+    a.rewards[2 * p] = value(o.reward[0]);
+    a.rewards[2 * p + 1] = value(o.reward[1]);
+    a.q.check(2 * p, 2);
+    return l;
+}
+
+template <bool VEC> __device__ __forceinline__ void fill(const Preference &a, const Part &part, float g, int at, int step) {
+#pragma unroll 4
+    for (int piece = part.first + at; piece < part.last; piece += step) {
+        const unsigned m = counting<VEC>(a.q.mask, piece, part.from, part.to, a.q.tokens);
+        store4<VEC>(a.dlogp, piece, part.from, part.to, make_float4(counts(m, 0) ? g : 0.f, counts(m, 1) ? g : 0.f,
+                                                                    counts(m, 2) ? g : 0.f, counts(m, 3) ? g : 0.f));
+    }
+}
+
+// Short sequences: a block sums over a pair and writes its gradient.
 template <int THREADS, bool VEC> __global__ void __launch_bounds__(THREADS, 1024 / THREADS) preference_kernel(const Preference a) {
-    constexpr int HALF = THREADS / 2, WARPS = THREADS / 32, U = 4;
-    __shared__ Score warps_of[2][WARPS], own[2][2];
+    constexpr int HALF = THREADS / 2, WARPS = THREADS / 32;
+    __shared__ Score warps_of[2][WARPS];
     __shared__ float slope_of[2][2], joined;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, side = threadIdx.x / HALF;
-    const bool split = a.share.ctas > 1;
-    const int rank = split ? (int)cluster_rank() : 0;
-    const int cluster = blockIdx.x / a.share.ctas, clusters = gridDim.x / a.share.ctas;
-    const int at = rank * HALF + threadIdx.x % HALF, step = a.share.ctas * HALF;
+    const int side = threadIdx.x / HALF, at = threadIdx.x % HALF;
     grid_dependency_launch();
     zero_outside<THREADS>(a.q, 2 * a.pairs, a.dlogp);
-    float loss = 0.f;  // thread 0 of rank 0
-    Two r0{}, r1{}, delta{};  // thread 0: the pair's rewards and their difference
+    float loss = 0.f;  // thread 0
     int parity = 0;
-    for (int p = cluster; p < a.pairs; p += clusters, parity ^= 1) {
-        const int a0 = a.q.begin(2 * p), a1 = max(a0, a.q.begin(2 * p + 1)), a2 = max(a1, a.q.begin(2 * p + 2));
-        const int from = side ? a1 : a0, to = side ? a2 : a1;
-        const Pieces pieces(from, to);
+    for (int p = blockIdx.x; p < a.pairs; p += gridDim.x, parity ^= 1) {
+        const Part part = part_of(a, p, side, 0);
+        Score v = score_of<VEC>(a, part, at, HALF);
+        block_scores<WARPS>(v, warps_of[parity]);
+        Outcome o;
+        if (threadIdx.x < 32) {
+            const Score other{{__shfl_sync(0xffffffffu, v.sum.hi, WARPS / 2), __shfl_sync(0xffffffffu, v.sum.lo, WARPS / 2)},
+                              __shfl_sync(0xffffffffu, v.count, WARPS / 2)};
+            if (threadIdx.x == 0) {
+                o = outcome_of(a, v, other);
+                slope_of[parity][0] = o.slope[0];
+                slope_of[parity][1] = o.slope[1];
+            }
+        }
+        __syncthreads();
+        fill<VEC>(a, part, slope_of[parity][side], at, HALF);
+        if (threadIdx.x == 0) loss += report(a, p, o);
+    }
+    if (!a.alone) return;
+    if (threadIdx.x == 0) joined = loss;
+    sync_ctas();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        loss = 0.f;
+        for (int c = 0; c < (int)gridDim.x; ++c) loss += load_peer(&joined, c);
+        *a.loss = loss * a.loss_weight;
+    }
+    sync_ctas();  // no CTA leaves while its loss is read
+}
+
+// Long sequences are cut into slices, so that the longest one does not end last: a launch sums over the slices, the
+// next one joins a pair's slices in their order, in every block that has one of them to fill.
+constexpr int kSliceThreads = 128;
+template <bool VEC> __global__ void __launch_bounds__(kSliceThreads, 8) preference_slices_kernel(const Preference a) {
+    constexpr int HALF = kSliceThreads / 2, WARPS = kSliceThreads / 32;
+    __shared__ Score warps_of[WARPS];
+    const int p = blockIdx.x >> a.slice_bits, slice = blockIdx.x & ((1 << a.slice_bits) - 1);
+    grid_dependency_launch();
+    Score v = score_of<VEC>(a, part_of(a, p, threadIdx.x / HALF, slice), threadIdx.x % HALF, HALF);
+    block_scores<WARPS>(v, warps_of);
+    if (threadIdx.x == 0 || threadIdx.x == WARPS / 2)
+        a.scores[(int64_t)blockIdx.x * 2 + (threadIdx.x != 0)] = make_float4(v.sum.hi, v.sum.lo, __int_as_float(v.count), 0.f);
+}
+template <bool VEC> __global__ void __launch_bounds__(kSliceThreads, 8) preference_fill_kernel(const Preference a) {
+    constexpr int HALF = kSliceThreads / 2;
+    __shared__ float slope_of[2];
+    const int slices = 1 << a.slice_bits, p = blockIdx.x >> a.slice_bits, slice = blockIdx.x & (slices - 1), side = threadIdx.x / HALF;
+    const Part part = part_of(a, p, side, slice);
+    grid_dependency_wait();
+    grid_dependency_launch();
+    zero_outside<kSliceThreads>(a.q, 2 * a.pairs, a.dlogp);
+    Outcome o;
+    if (threadIdx.x < 32) {  // 16 lanes for each sequence
         Score v{};
-        F2 sum = pair(0.f, 0.f), lost = sum;
-        for (int p0 = pieces.first + at; p0 < pieces.last; p0 += step * U) {
-            float4 x[U], r[U];
-            unsigned m[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int piece = p0 + u * step;
-                m[u] = 0;
-                if (piece >= pieces.last) continue;
-                m[u] = counting<VEC>(a.q.mask, piece, from, to, a.q.tokens);
-                x[u] = load4<VEC>(a.logp, piece, a.q.tokens);
-                r[u] = a.ref ? load4<VEC>(a.ref, piece, a.q.tokens) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!m[u]) continue;
-                const float d0 = counts(m[u], 0) ? x[u].x - r[u].x : 0.f, d1 = counts(m[u], 1) ? x[u].y - r[u].y : 0.f;
-                const float d2 = counts(m[u], 2) ? x[u].z - r[u].z : 0.f, d3 = counts(m[u], 3) ? x[u].w - r[u].w : 0.f;
-                const Two2 once = two_sum(sum, pair(d0, d1)), twice = two_sum(once.hi, pair(d2, d3));
-                sum = twice.hi;
-                lost = lost + (once.lo + twice.lo);
-                if (a.average) v.count += nonzero_bytes(m[u]);
-            }
+        for (int c = threadIdx.x & 15; c < slices; c += 16) {
+            const float4 x = a.scores[((int64_t)p * slices + c) * 2 + (threadIdx.x >> 4)];
+            add(v.sum, Two{x.x, x.y});
+            v.count += __float_as_int(x.z);
         }
-        const float2 hi = both(sum), lo = both(lost);
-        v.sum = {hi.x, lo.x};
-        add(v.sum, Two{hi.y, lo.y});
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) add(v.sum, shuffled(v.sum, o));
-        if (a.average) v.count = warp_add(v.count);
-        if (lane == 0) warps_of[parity][warp] = v;
-        __syncthreads();
-        if (warp == 0) {
-            // lanes 0 and WARPS / 2 end with the two sequences' sums
-            v = warps_of[parity][lane % WARPS];
-#pragma unroll
-            for (int o = WARPS / 4; o >= 1; o >>= 1) {
-                add(v.sum, shuffled(v.sum, o));
-                v.count += __shfl_xor_sync(0xffffffffu, v.count, o);
-            }
-            if (split && (lane == 0 || lane == WARPS / 2)) own[parity][lane != 0] = v;
-        }
-        if (split) {
-            sync_ctas();  // the other CTAs' sums are there
-            if (warp == 0) {
-                v = Score{};
-                if (lane == 0 || lane == WARPS / 2)
-                    for (int c = 0; c < a.share.ctas; ++c) {
-                        const Score &o = own[parity][lane != 0];
-                        add(v.sum, Two{load_peer(&o.sum.hi, c), load_peer(&o.sum.lo, c)});
-                        v.count += load_peer(&o.count, c);
-                    }
-            }
-        }
-        if (warp == 0) {
-            v.sum = finished(v.sum);
-            const Score second{{__shfl_sync(0xffffffffu, v.sum.hi, WARPS / 2), __shfl_sync(0xffffffffu, v.sum.lo, WARPS / 2)},
-                               __shfl_sync(0xffffffffu, v.count, WARPS / 2)};
-            if (lane == 0) {
-                r0 = times(v.sum, a.beta);
-                r1 = times(second.sum, a.beta);
-                if (a.average) {
-                    r0 = divided(r0, (float)max(v.count, 1));
-                    r1 = divided(r1, (float)max(second.count, 1));
-                }
-                delta = r0;
-                add(delta, Two{-r1.hi, -r1.lo});
-                const float d = value(delta);
-                float slope;
-                if (a.kind == PREFERENCE_LOGISTIC) {
-                    const float up = 1.f / (1.f + expf(-d)), down = 1.f / (1.f + expf(d));
-                    slope = a.smoothing * up - (1.f - a.smoothing) * down;
-                } else if (a.kind == PREFERENCE_HINGE) {
-                    const float gap = below(1.f, delta);
-                    slope = gap <= 0.f ? 0.f : gap == gap ? -1.f : gap;  // NaN stays
-                } else {
-                    slope = -2.f * (below(0.5f, delta) / a.beta) / a.beta;
-                }
-                slope *= a.beta * a.weight;
-                slope_of[parity][0] = a.average ? slope / (float)max(v.count, 1) : slope;
-                slope_of[parity][1] = a.average ? -slope / (float)max(second.count, 1) : -slope;
-            }
-        }
-        __syncthreads();
-        const float g = slope_of[parity][side];
-#pragma unroll 4
-        for (int piece = pieces.first + at; piece < pieces.last; piece += step) {
-            const unsigned m = counting<VEC>(a.q.mask, piece, from, to, a.q.tokens);
-            store4<VEC>(a.dlogp, piece, from, to, make_float4(counts(m, 0) ? g : 0.f, counts(m, 1) ? g : 0.f, counts(m, 2) ? g : 0.f,
-                                                              counts(m, 3) ? g : 0.f));
-        }
-        // what nobody waits for
-        if (rank == 0 && threadIdx.x == 0) {
-            const float d = value(delta);
-            float l;
-            if (a.kind == PREFERENCE_LOGISTIC) {
-                const float soft = log1pf(expf(-fabsf(d)));
-                l = (1.f - a.smoothing) * (soft + fmaxf(-d, 0.f));
-                if (a.smoothing > 0.f) l += a.smoothing * (soft + fmaxf(d, 0.f));
-            } else if (a.kind == PREFERENCE_HINGE) {
-                const float gap = below(1.f, delta);
-                l = gap <= 0.f ? 0.f : gap;
-            } else {
-                const float gap = below(0.5f, delta) / a.beta;
-                l = gap * gap;
-            }
-            a.pair_loss[p] = l;
-            a.rewards[2 * p] = value(r0);
-            a.rewards[2 * p + 1] = value(r1);
-            loss += l;
-            a.q.check(2 * p, 2);
+        lanes_add(v, 16);
+        const Score other{{__shfl_sync(0xffffffffu, v.sum.hi, 16), __shfl_sync(0xffffffffu, v.sum.lo, 16)},
+                          __shfl_sync(0xffffffffu, v.count, 16)};
+        if (threadIdx.x == 0) {
+            o = outcome_of(a, v, other);
+            slope_of[0] = o.slope[0];
+            slope_of[1] = o.slope[1];
         }
     }
-    if (a.share.alone) {
-        if (threadIdx.x == 0) joined = loss;
-        sync_ctas();
-        if (cluster == 0 && threadIdx.x == 0) {
-            loss = 0.f;
-            for (int c = 0; c < clusters; ++c) loss += load_peer(&joined, c);
-            *a.loss = loss * a.loss_weight;
-        }
-    } else if (rank == 0 && threadIdx.x == 0) {
-        reinterpret_cast<float4 *>(a.partial)[cluster] = make_float4(loss, 0.f, 0.f, 0.f);
-    }
-    if (split || a.share.alone) sync_ctas();  // no CTA leaves while its sums are read
+    __syncthreads();
+    fill<VEC>(a, part, slope_of[side], threadIdx.x % HALF, HALF);
+    if (threadIdx.x == 0 && slice == 0) report(a, p, o);
 }
 
 // ---- policy --------------------------------------------------------------------------------
@@ -419,9 +452,10 @@ struct Policy {
     Sequences q;
     const float *logp, *old, *ref, *advantages;
     float *dlogp, *partial, *parts, *loss;
-    // by the preparing launch, where there is one: tokens that count by block, the sequence that each tile begins in,
-    // the weight of each sequence's tokens
-    int *counted, *first_of;
+    // by the preparing launch, where there is one: tokens that count by block; of the sequence that each tile begins in
+    // its number, its end, its advantage and the weight of its tokens; that weight of each sequence
+    int *counted;
+    int4 *first_of;
     float *weight_of;
     int counting_blocks, tiles;
     int per_sequence, reduction;
@@ -456,53 +490,65 @@ template <bool VEC> __device__ __forceinline__ Tokens load_tokens(const Policy &
 
 // Weighted sums over a thread's tokens: gains, divergences, clipped ones.
 struct Seen {
-    F2 gain, kl, clipped;
+    float gain, kl, clipped;
 };
 
-// Two tokens: their gradient over grad_scale; here: whether they count.
-__device__ __forceinline__ F2 two_tokens(const Policy &a, bool here0, bool here1, F2 logp, F2 old, F2 ref, F2 advantage, F2 weight,
-                                         Seen &seen) {
-    const float2 adv = both(advantage), wt = both(weight);
-    const bool up0 = adv.x >= 0.f, up1 = adv.y >= 0.f;
-    Two2 d = two_sum(logp, old * pair(-1.f, -1.f));
-    const float2 hi = both(d.hi), left = both(d.lo);
-    d.lo = pair(fabsf(hi.x) < INFINITY ? left.x : 0.f, fabsf(hi.y) < INFINITY ? left.y : 0.f);
-    const float2 past = both((d.hi - pair(up0 ? a.log_high.hi : a.log_low.hi, up1 ? a.log_high.hi : a.log_low.hi)) +
-                             (d.lo - pair(up0 ? a.log_high.lo : a.log_low.lo, up1 ? a.log_high.lo : a.log_low.lo)));
-    const bool clip0 = up0 ? past.x > 0.f : past.x < 0.f, clip1 = up1 ? past.y > 0.f : past.y < 0.f;
-    // A r as A + A (r - 1): the sum over many tokens whose advantages cancel has no bias from the last place of
-    // the exponential
-    const float2 free = both(exp_of(d.hi).above);
-    const F2 above = pair(clip0 ? (up0 ? a.edge_high : a.edge_low) : free.x, clip1 ? (up1 ? a.edge_high : a.edge_low) : free.y);
-    const float2 gain = both(fma2(advantage, above, advantage));
-    F2 slope = pair(clip0 ? 0.f : -gain.x, clip1 ? 0.f : -gain.y);
-    seen.gain = fma2(pair(here0 ? gain.x : 0.f, here1 ? gain.y : 0.f), weight, seen.gain);
-    seen.clipped = seen.clipped + pair(here0 && clip0 ? wt.x : 0.f, here1 && clip1 ? wt.y : 0.f);
-    if (a.ref) {
-        const Exp e = exp_of(ref - logp);
-        const float2 kl = both(e.rest);
-        seen.kl = fma2(pair(here0 ? kl.x : 0.f, here1 ? kl.y : 0.f), weight, seen.kl);
-        slope = fma2(pair(-a.kl_coef, -a.kl_coef), e.above, slope);
-    }
-    const float2 out = both(slope * weight);
-    return pair(here0 ? out.x : 0.f, here1 ? out.y : 0.f);
-}
-// A piece: m says which tokens count.
+// A piece's gradient, and what its tokens add to the sums; m says which of them count.
 __device__ __forceinline__ float4 four_tokens(const Policy &a, unsigned m, const Tokens &t, float4 weight, Seen &seen) {
     if (!m) return make_float4(0.f, 0.f, 0.f, 0.f);
-    const F2 scale = pair(a.grad_scale, a.grad_scale);
-    const float2 g0 = both(scale * two_tokens(a, counts(m, 0), counts(m, 1), pair(t.logp.x, t.logp.y), pair(t.old.x, t.old.y),
-                                              pair(t.ref.x, t.ref.y), pair(t.advantage.x, t.advantage.y),
-                                              pair(weight.x, weight.y), seen));
-    const float2 g1 = both(scale * two_tokens(a, counts(m, 2), counts(m, 3), pair(t.logp.z, t.logp.w), pair(t.old.z, t.old.w),
-                                              pair(t.ref.z, t.ref.w), pair(t.advantage.z, t.advantage.w),
-                                              pair(weight.z, weight.w), seen));
-    return make_float4(g0.x, g0.y, g1.x, g1.y);
+    const float lp[4] = {t.logp.x, t.logp.y, t.logp.z, t.logp.w}, old[4] = {t.old.x, t.old.y, t.old.z, t.old.w};
+    const float ref[4] = {t.ref.x, t.ref.y, t.ref.z, t.ref.w}, w[4] = {weight.x, weight.y, weight.z, weight.w};
+    const float adv[4] = {t.advantage.x, t.advantage.y, t.advantage.z, t.advantage.w};
+    Two d[4];
+    float q[4], ratio[4], kl[4], dkl[4], g[4];  // ratio: its distance from 1
+    bool near = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        d[i] = two_sum(lp[i], -old[i]);
+        ratio[i] = d[i].hi + exp_rest(d[i].hi);
+        near = near && fabsf(d[i].hi) < 1.f;
+        if (a.ref) {
+            q[i] = ref[i] - lp[i];
+            kl[i] = exp_rest(q[i]);
+            dkl[i] = q[i] + kl[i];
+            near = near && fabsf(q[i]) < 1.f;
+        }
+    }
+    if (!near) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!(fabsf(d[i].hi) < 1.f)) {
+                ratio[i] = exp_above(d[i].hi);
+                d[i] = finished(d[i]);
+            }
+            if (a.ref && !(fabsf(q[i]) < 1.f)) {
+                dkl[i] = exp_above(q[i]);
+                kl[i] = dkl[i] - q[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool here = counts(m, i), up = adv[i] >= 0.f;
+        const float past = (d[i].hi - (up ? a.log_high.hi : a.log_low.hi)) + (d[i].lo - (up ? a.log_high.lo : a.log_low.lo));
+        const bool clipped = up ? past > 0.f : past < 0.f;
+        // A r as A + A (r - 1): the sum over many tokens whose advantages cancel has no bias from the last place
+        // of the exponential
+        const float gain = fmaf(adv[i], clipped ? (up ? a.edge_high : a.edge_low) : ratio[i], adv[i]);
+        float slope = clipped ? 0.f : -gain;
+        if (a.ref) slope = fmaf(-a.kl_coef, dkl[i], slope);
+        g[i] = here ? slope * w[i] * a.grad_scale : 0.f;
+        const float wh = here ? w[i] : 0.f;
+        seen.gain = fmaf(here ? gain : 0.f, w[i], seen.gain);
+        if (a.ref) seen.kl = fmaf(here ? kl[i] : 0.f, w[i], seen.kl);
+        seen.clipped += clipped ? wh : 0.f;
+    }
+    return make_float4(g[0], g[1], g[2], g[3]);
 }
 // The block's sums, to threads 0 .. 2: -gain, kl, clipped.
 template <int WARPS> __device__ __forceinline__ float block_sums(const Seen &seen, float (*red)[3]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float v[3] = {warp_add(-sum2(seen.gain)), warp_add(sum2(seen.kl)), warp_add(sum2(seen.clipped))};
+    const float v[3] = {warp_add(-seen.gain), warp_add(seen.kl), warp_add(seen.clipped)};
     if (lane == 0)
         for (int i = 0; i < 3; ++i) red[warp][i] = v[i];
     __syncthreads();
@@ -524,8 +570,8 @@ template <int THREADS, bool VEC> __global__ void __launch_bounds__(THREADS, 1) p
         const int n = a.q.mask ? block_add<WARPS>(count_tokens(a.q.mask, b0, b1, threadIdx.x, THREADS), red) : b1 - b0;
         weight = 1.f / (float)max(n, 1);
     }
-    Seen seen{pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
-    const int units = a.q.offsets ? a.q.count : a.tiles;
+    Seen seen{0.f, 0.f, 0.f};
+    const int units = a.q.offsets ? a.q.count : (a.q.tokens + kUnit - 1) / kUnit;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const int b0 = a.q.begin(u), b1 = max(b0, a.q.begin(u + 1));
         if (a.reduction == POLICY_SEQUENCE_MEAN) {
@@ -587,18 +633,21 @@ __global__ void __launch_bounds__(kPrepareThreads) policy_prepare_kernel(const P
         // tiles that begin in the sequence, in front of the first or behind the last one
         const int t0 = s == 0 ? 0 : (from + kTile - 1) / kTile;
         const int t1 = s == a.q.count - 1 ? a.tiles : (to + kTile - 1) / kTile;
-        for (int t = t0 + (int)threadIdx.x; t < t1; t += kPrepareThreads) a.first_of[t] = s;
+        float weight = 0.f;
         if (a.reduction == POLICY_SEQUENCE_MEAN) {
             const int n = a.q.mask ? block_add<kPrepareThreads / 32>(count_tokens(a.q.mask, from, to, threadIdx.x, kPrepareThreads), red)
                                    : to - from;
-            if (threadIdx.x == 0) a.weight_of[s] = 1.f / ((float)max(n, 1) * (float)a.q.count);
+            weight = 1.f / ((float)max(n, 1) * (float)a.q.count);
+            if (threadIdx.x == 0) a.weight_of[s] = weight;
         }
+        const int4 what = make_int4(s, to, __float_as_int(a.per_sequence ? a.advantages[s] : 0.f), __float_as_int(weight));
+        for (int t = t0 + (int)threadIdx.x; t < t1; t += kPrepareThreads) a.first_of[t] = what;
         if (threadIdx.x == 0) a.q.check(s, 1);
     }
 }
 
-template <bool VEC> __global__ void __launch_bounds__(kTileThreads, 8) policy_tiles_kernel(const Policy a) {
-    constexpr int U = kTile / 4 / kTileThreads;
+template <bool VEC> __global__ void __launch_bounds__(kTileThreads, kTileBlocks) policy_tiles_kernel(const Policy a) {
+    static_assert(kTile == 4 * kTileThreads, "a piece per thread");
     __shared__ float sums_of[kTileThreads / 32][3];
     const int lane = threadIdx.x & 31;
     const bool lookup = a.per_sequence || a.reduction == POLICY_SEQUENCE_MEAN;
@@ -620,123 +669,133 @@ template <bool VEC> __global__ void __launch_bounds__(kTileThreads, 8) policy_ti
         n = a.counting_blocks ? warp_add(n) : b1 - b0;
         same = 1.f / (float)max(n, 1);
     }
-    Seen seen{pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
+    Seen seen{0.f, 0.f, 0.f};
+    // the next tile's values are on their way while one is worked on
+    struct Next {
+        Tokens t;
+        unsigned m;
+        int4 first;
+    };
+    auto fetch = [&](int tile) {
+        Next n;
+        n.m = 0;
+        if (tile >= a.tiles) return n;
+        const int piece = tile * kTileThreads + (int)threadIdx.x, at = piece * 4;
+        if (at < b1 && at + 4 > b0) {
+            n.m = counting<VEC>(a.q.mask, piece, b0, b1, a.q.tokens);
+            n.t = load_tokens<VEC>(a, piece, 0.f);
+        }
+        if (lookup) n.first = a.first_of[tile];
+        return n;
+    };
+    Next next = fetch(blockIdx.x);
     for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-        const int p0 = tile * (kTile / 4) + (int)threadIdx.x;
-        Tokens t[U];
-        unsigned m[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int piece = p0 + k * kTileThreads, at = piece * 4;
-            m[k] = 0;
-            if (at >= b1 || at + 4 <= b0) continue;
-            m[k] = counting<VEC>(a.q.mask, piece, b0, b1, a.q.tokens);
-            t[k] = load_tokens<VEC>(a, piece, 0.f);
-        }
-        int s0 = 0, s1 = 0;
+        Next now = next;
+        next = fetch(tile + gridDim.x);
+        const int piece = tile * kTileThreads + (int)threadIdx.x, at = piece * 4;
+        float4 weight = make_float4(same, same, same, same);
         if (lookup) {
-            s0 = min(max(a.first_of[tile], 0), a.q.count - 1);
-            s1 = tile + 1 < a.tiles ? min(max(a.first_of[tile + 1], s0), a.q.count - 1) : a.q.count - 1;
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int piece = p0 + k * kTileThreads, at = piece * 4;
-            if (at >= a.q.tokens) continue;
-            float4 weight = make_float4(same, same, same, same);
-            if (lookup && m[k]) {
-                int lo = s0, hi = s1;  // the last sequence that begins at or in front of the piece
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) / 2;
-                    if (a.q.begin(mid) <= at) lo = mid;
+            float w = a.reduction == POLICY_SEQUENCE_MEAN ? __int_as_float(now.first.w) : same, v = __int_as_float(now.first.z);
+            float ws[4] = {w, w, w, w}, vs[4] = {v, v, v, v};
+            if (now.m && at + 4 > now.first.y) {
+                // the piece lies in a later sequence or goes on in one: the last that begins at or in front of it, within
+                // bounds whatever the offsets were
+                const int most = a.q.count - 1, s1 = tile + 1 < a.tiles ? min(max(a.first_of[tile + 1].x, 0), most) : most;
+                int s = min(max(now.first.x, 0), s1), hi = s1;
+                while (s < hi) {
+                    const int mid = (s + hi + 1) / 2;
+                    if (a.q.begin(mid) <= at) s = mid;
                     else hi = mid - 1;
                 }
-                float w[4], v[4];
-                int s = lo, end = a.q.begin(s + 1);
+                int end = at;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    while (s < s1 && at + i >= end) end = a.q.begin(++s + 1);
-                    w[i] = a.reduction == POLICY_SEQUENCE_MEAN ? a.weight_of[s] : same;
-                    v[i] = a.per_sequence ? a.advantages[s] : 0.f;
+                    if (at + i >= end) {
+                        if (i) ++s;
+                        for (end = s < s1 ? a.q.begin(s + 1) : b1; s < s1 && at + i >= end; end = s < s1 ? a.q.begin(s + 1) : b1) ++s;
+                        if (a.reduction == POLICY_SEQUENCE_MEAN) w = a.weight_of[s];
+                        if (a.per_sequence) v = a.advantages[s];
+                        if (s == s1) end = INT32_MAX;
+                    }
+                    ws[i] = w;
+                    vs[i] = v;
                 }
-                weight = make_float4(w[0], w[1], w[2], w[3]);
-                if (a.per_sequence) t[k].advantage = make_float4(v[0], v[1], v[2], v[3]);
             }
-            const float4 g = four_tokens(a, m[k], t[k], weight, seen);
-            store4<VEC>(a.dlogp, piece, 0, a.q.tokens, g);
+            weight = make_float4(ws[0], ws[1], ws[2], ws[3]);
+            if (a.per_sequence) now.t.advantage = make_float4(vs[0], vs[1], vs[2], vs[3]);
         }
+        if (at < a.q.tokens) store4<VEC>(a.dlogp, piece, 0, a.q.tokens, four_tokens(a, now.m, now.t, weight, seen));
     }
     const float sum = block_sums<kTileThreads / 32>(seen, sums_of);
     if (threadIdx.x < 3) a.partial[(int64_t)blockIdx.x * 4 + threadIdx.x] = sum;
 }
 
-// parts[k] = weight * sum of partial[0 .. blocks)[k], loss = parts[0] + kl_coef parts[1], in two floats (a warp's
-// addition in fp64 takes 15 cycles here) and a fixed order
+// parts[k] = weight * sum of from[0 .. count)[k], loss = parts[0] + kl_coef parts[1], in two floats (a warp's addition
+// in fp64 takes 15 cycles here) and a fixed order.  KINDS values of each of `count`: 1, or 3 of 4.
 constexpr int kJoinThreads = 1024;
-__global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const float *partial, int blocks, float weight, float kl_coef,
-                                                                 float *parts, float *loss) {
-    __shared__ Two red[3][kJoinThreads / 32];
+template <int KINDS> __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const float *from, int count, float weight,
+                                                                                      float kl_coef, float *parts, float *loss) {
+    __shared__ Two red[KINDS][kJoinThreads / 32];
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Two v[3] = {};
+    Two v[KINDS] = {};
 #pragma unroll 4
-    for (int i = threadIdx.x; i < blocks; i += kJoinThreads) {
-        const float4 x = reinterpret_cast<const float4 *>(partial)[i];
-        add(v[0], Two{x.x, 0.f});
-        add(v[1], Two{x.y, 0.f});
-        add(v[2], Two{x.z, 0.f});
+    for (int i = threadIdx.x; i < count; i += kJoinThreads) {
+        if (KINDS == 1) {
+            add(v[0], Two{from[i], 0.f});
+        } else {
+            const float4 x = reinterpret_cast<const float4 *>(from)[i];
+            add(v[0], Two{x.x, 0.f});
+            add(v[KINDS > 1 ? 1 : 0], Two{x.y, 0.f});
+            add(v[KINDS > 2 ? 2 : 0], Two{x.z, 0.f});
+        }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
 #pragma unroll
-        for (int k = 0; k < 3; ++k) add(v[k], shuffled(v[k], o));
+        for (int k = 0; k < KINDS; ++k) add(v[k], shuffled(v[k], o));
     if (lane == 0)
-        for (int k = 0; k < 3; ++k) red[k][warp] = v[k];
+        for (int k = 0; k < KINDS; ++k) red[k][warp] = v[k];
     __syncthreads();
     if (warp) return;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] = red[k][lane];
+    for (int k = 0; k < KINDS; ++k) v[k] = red[k][lane];
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
 #pragma unroll
-        for (int k = 0; k < 3; ++k) add(v[k], shuffled(v[k], o));
+        for (int k = 0; k < KINDS; ++k) add(v[k], shuffled(v[k], o));
     if (lane) return;
-    for (int k = 0; k < 3; ++k) v[k] = times(finished(v[k]), weight);
-    if (parts)
-        for (int k = 0; k < 3; ++k) parts[k] = value(v[k]);
-    if (kl_coef != 0.f) add(v[0], times(v[1], kl_coef));
+    for (int k = 0; k < KINDS; ++k) v[k] = times(finished(v[k]), weight);
+    if (KINDS == 3) {
+        for (int k = 0; k < KINDS; ++k) parts[k] = value(v[k]);
+        if (kl_coef != 0.f) add(v[0], times(v[KINDS > 1 ? 1 : 0], kl_coef));
+    }
     *loss = value(v[0]);
 }
 
 // ---- launches ------------------------------------------------------------------------------
 
-// Threads of a block and CTAs for a unit.  A unit's chain of loads, sums and stores is what takes the time, and the
-// longest unit ends last: as many threads for each as the SMs hold for all of them at once, and 1024 tokens or more
-// for a CTA.  Few units of few tokens: one cluster, which needs no launch to join its losses.
-struct Cut {
-    Share share;
-    int threads;
-};
-Cut cut_of(int units, int64_t tokens) {
-    const int64_t length = tokens / std::max(units, 1), room = (int64_t)num_sms() * 2048;
-    if (units <= kMaxCluster && length <= 2048) return {{1, 1}, length > 512 ? kManyThreads : kFewThreads};
-    int threads = kFewThreads, c = 1;
-    while (threads < kManyThreads && (int64_t)units * threads * 2 <= room && length > (int64_t)threads * 4) threads *= 2;
-    while (c < kMaxCluster && (int64_t)units * c * threads * 4 <= room && length > (int64_t)c * threads * 8) c *= 2;
-    return {{c, 0}, threads};
+// Few units of few tokens: one cluster, which needs no launch to join its losses.
+bool alone(int units, int64_t tokens) { return units <= kMaxCluster && tokens <= (int64_t)std::max(units, 1) * 2048; }
+int cluster_of(int units) { return units <= 1 ? 1 : units <= 2 ? 2 : units <= 4 ? 4 : kMaxCluster; }
+
+// Slices of a pair, as a power of two: some 1024 tokens of an average one.  0: a block takes a pair.
+int slice_bits_of(int64_t pairs, int64_t tokens) {
+    if (pairs == 0 || alone((int)pairs, tokens)) return 0;
+    int bits = 0;
+    while (bits < 6 && tokens / pairs > (1024 << bits) && pairs << bits < 1 << 15) ++bits;
+    return bits;
 }
-int blocks_of(int units, const Share &s) {
-    if (s.alone) return units <= 1 ? 1 : units <= 2 ? 2 : units <= 4 ? 4 : kMaxCluster;
-    return s.ctas * std::max(1, std::min(units, num_sms() * kMaxBlocksPerSm / s.ctas));
-}
+
 template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kernel)(P...), int blocks, const Cut &cut, cudaStream_t st, A &&...args) {
+cudaError_t launch_cluster(void (*kernel)(P...), int blocks, int threads, cudaStream_t st, A &&...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(cut.threads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cut.share.alone ? blocks : cut.share.ctas;
+    attr.val.clusterDim.x = blocks;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -765,11 +824,11 @@ bool all_aligned16(std::initializer_list<const void *> p, const void *mask) {
 }
 
 // partial sums of the blocks
-int64_t partial_bytes() { return (int64_t)num_sms() * kMaxBlocksPerSm * 16; }
+int64_t partial_bytes() { return (int64_t)num_sms() * kTileBlocks * 16; }
 // and of the policy loss: counts, each tile's first sequence, each sequence's weight
 constexpr int kMostCounts = 512;
 int64_t policy_bytes(int64_t sequences, int64_t tokens) {
-    return partial_bytes() + 4 * (kMostCounts + ceil_div(tokens, kTile) + sequences);
+    return partial_bytes() + 16 * ceil_div(tokens, kTile) + 4 * (kMostCounts + sequences);
 }
 
 // log(x) in two floats
@@ -789,7 +848,7 @@ extern "C" int64_t preference_loss_workspace(int64_t pairs, int64_t tokens) {
     entry([&]() -> int {
         if (pairs < 0 || pairs > kMost / 2 || tokens < 0 || tokens > kMost)
             return fail(SPECOPTIM_ERR_INVALID_ARG, "preference_loss: pairs outside [0, 2^29] or tokens outside [0, 2^30]");
-        bytes = partial_bytes();
+        bytes = std::max<int64_t>(16, (pairs << slice_bits_of(pairs, tokens)) * 2 * 16);
         return SPECOPTIM_OK;
     });
     return bytes;
@@ -814,31 +873,43 @@ extern "C" int preference_loss(const float *logp, const float *ref_logp, const u
         if (!aligned_to(ref_logp, 4) || !aligned_to(pair_loss, 4) || !aligned_to(rewards, 4))
             return fail(SPECOPTIM_ERR_MISALIGNED, what + ": pointers must be aligned to their elements");
         if (int rc = bind_device()) return rc;
-        if (workspace_bytes < partial_bytes())
+        if (workspace_bytes < (pairs << slice_bits_of(pairs, tokens)) * 2 * 16)
             return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": the workspace is smaller than preference_loss_workspace() says");
-        const Cut cut = cut_of((int)pairs, tokens);
-        const Share share = cut.share;
-        const int blocks = blocks_of((int)pairs, share);
         const float part = mean ? 1.f / (float)std::max<int64_t>(pairs, 1) : 1.f;
+        const bool one = alone((int)pairs, tokens);
+        const int bits = slice_bits_of(pairs, tokens);
         const Preference a{{offsets, offset_bytes == 8, (int)(2 * pairs), (int)tokens, mask, stage_flag_ptr()},
-                           logp, ref_logp, dlogp, pair_loss, rewards, static_cast<float *>(workspace), loss, share, (int)pairs,
-                           kind, average != 0, beta, smoothing, grad_scale * part, part};
+                           logp, ref_logp, dlogp, pair_loss, rewards, loss, static_cast<float4 *>(workspace), (int)pairs, bits,
+                           one, kind, average != 0, beta, smoothing, grad_scale * part, part};
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         const bool vec = all_aligned16({logp, ref_logp, dlogp}, mask);
-        auto pick = [&](auto threads) {
-            constexpr int THREADS = decltype(threads)::value;
-            return vec ? &preference_kernel<THREADS, true> : &preference_kernel<THREADS, false>;
-        };
-        auto *k = cut.threads == kFewThreads      ? pick(std::integral_constant<int, kFewThreads>{})
-                  : cut.threads == kMiddleThreads ? pick(std::integral_constant<int, kMiddleThreads>{})
-                                                  : pick(std::integral_constant<int, kManyThreads>{});
         cudaError_t e = cudaSuccess;
-        SPCO_LAUNCH("preference_loss", st, e = launch_clusters(k, blocks, cut, st, a));
-        SPECOPTIM_CUDA(e);
-        if (share.alone) return SPECOPTIM_OK;
+        if (one) {
+            const bool many = tokens > pairs * 512;
+            auto *k = many ? (vec ? &preference_kernel<kManyThreads, true> : &preference_kernel<kManyThreads, false>)
+                           : (vec ? &preference_kernel<kFewThreads, true> : &preference_kernel<kFewThreads, false>);
+            SPCO_LAUNCH("preference_loss", st,
+                        e = launch_cluster(k, cluster_of((int)pairs), many ? kManyThreads : kFewThreads, st, a));
+            SPECOPTIM_CUDA(e);
+            return SPECOPTIM_OK;
+        }
+        if (bits == 0) {
+            auto *k = vec ? &preference_kernel<kFewThreads, true> : &preference_kernel<kFewThreads, false>;
+            const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(pairs, num_sms() * kMaxBlocksPerSm));
+            SPCO_LAUNCH("preference_loss", st, k<<<blocks, kFewThreads, 0, st>>>(a));
+            SPECOPTIM_LAUNCHED("preference_kernel");
+        } else {
+            const unsigned blocks = (unsigned)(pairs << bits);
+            auto *k = vec ? &preference_slices_kernel<true> : &preference_slices_kernel<false>;
+            SPCO_LAUNCH("preference_slices", st, k<<<blocks, kSliceThreads, 0, st>>>(a));
+            SPECOPTIM_LAUNCHED("preference_slices_kernel");
+            auto *f = vec ? &preference_fill_kernel<true> : &preference_fill_kernel<false>;
+            SPCO_LAUNCH("preference_loss", st, e = launch_dependent(f, dim3(blocks), dim3(kSliceThreads), 0, st, a));
+            SPECOPTIM_CUDA(e);
+        }
         SPCO_LAUNCH("loss_join", st,
-                    e = launch_dependent(loss_join_kernel, dim3(1), dim3(kJoinThreads), 0, st, a.partial, blocks / share.ctas, part,
-                                         0.f, static_cast<float *>(nullptr), loss));
+                    e = launch_dependent(loss_join_kernel<1>, dim3(1), dim3(kJoinThreads), 0, st, pair_loss, (int)pairs, part, 0.f,
+                                         static_cast<float *>(nullptr), loss));
         SPECOPTIM_CUDA(e);
         return SPECOPTIM_OK;
     });
@@ -882,20 +953,21 @@ extern "C" int policy_loss(const float *logp, const float *old_logp, const float
             return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": the workspace is smaller than policy_loss_workspace() says");
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         if (!offsets && reduction == POLICY_SEQUENCE_MEAN) reduction = POLICY_TOKEN_MEAN;
-        const int tiles = (int)ceil_div(tokens, kTile), units = offsets ? (int)sequences : tiles;
+        const int tiles = (int)ceil_div(tokens, kTile), units = (int)(offsets ? sequences : ceil_div(tokens, kUnit));
         const bool vec = all_aligned16({logp, old_logp, ref_logp, dlogp, per_sequence ? nullptr : advantages}, mask);
         float *partial = static_cast<float *>(workspace);
-        int *counted = reinterpret_cast<int *>(static_cast<char *>(workspace) + partial_bytes());
+        int4 *first_of = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + partial_bytes());
+        int *counted = reinterpret_cast<int *>(first_of + tiles);
         Policy a{{offsets, offset_bytes == 8, (int)sequences, (int)tokens, mask, stage_flag_ptr()},
-                 logp, old_logp, ref_logp, advantages, dlogp, partial, parts, loss, counted, counted + kMostCounts,
-                 reinterpret_cast<float *>(counted + kMostCounts + tiles), 0, tiles, per_sequence != 0, reduction, kl_coef,
+                 logp, old_logp, ref_logp, advantages, dlogp, partial, parts, loss, counted, first_of,
+                 reinterpret_cast<float *>(counted + kMostCounts), 0, tiles, per_sequence != 0, reduction, kl_coef,
                  grad_scale, (float)clip_high, (float)-clip_low, log_two(1. + clip_high), log_two(1. - clip_low)};
         cudaError_t e = cudaSuccess;
-        const Cut cut = cut_of(units, tokens);
-        if (cut.share.alone) {
-            auto *k = cut.threads == kManyThreads ? (vec ? &policy_few_kernel<kManyThreads, true> : &policy_few_kernel<kManyThreads, false>)
-                               : (vec ? &policy_few_kernel<kFewThreads, true> : &policy_few_kernel<kFewThreads, false>);
-            SPCO_LAUNCH("policy_loss", st, e = launch_clusters(k, blocks_of(units, cut.share), cut, st, a));
+        if (alone(units, tokens)) {
+            const bool many = tokens > (int64_t)units * 512;
+            auto *k = many ? (vec ? &policy_few_kernel<kManyThreads, true> : &policy_few_kernel<kManyThreads, false>)
+                           : (vec ? &policy_few_kernel<kFewThreads, true> : &policy_few_kernel<kFewThreads, false>);
+            SPCO_LAUNCH("policy_loss", st, e = launch_cluster(k, cluster_of(units), many ? kManyThreads : kFewThreads, st, a));
             SPECOPTIM_CUDA(e);
             return SPECOPTIM_OK;
         }
@@ -910,7 +982,7 @@ extern "C" int policy_loss(const float *logp, const float *old_logp, const float
                         policy_prepare_kernel<<<(unsigned)(a.counting_blocks + by_sequence), kPrepareThreads, 0, st>>>(a));
             SPECOPTIM_LAUNCHED("policy_prepare_kernel");
         }
-        const int blocks = std::max(1, std::min(tiles, num_sms() * kMaxBlocksPerSm));
+        const int blocks = std::max(1, std::min(tiles, num_sms() * kTileBlocks));
         auto *k = vec ? &policy_tiles_kernel<true> : &policy_tiles_kernel<false>;
         if (prepared) {
             SPCO_LAUNCH("policy_loss", st, e = launch_dependent(k, dim3(blocks), dim3(kTileThreads), 0, st, a));
@@ -920,7 +992,7 @@ extern "C" int policy_loss(const float *logp, const float *old_logp, const float
             SPECOPTIM_LAUNCHED("policy_tiles_kernel");
         }
         SPCO_LAUNCH("loss_join", st,
-                    e = launch_dependent(loss_join_kernel, dim3(1), dim3(kJoinThreads), 0, st, partial, blocks, 1.f, kl_coef, parts,
+                    e = launch_dependent(loss_join_kernel<3>, dim3(1), dim3(kJoinThreads), 0, st, partial, blocks, 1.f, kl_coef, parts,
                                          loss));
         SPECOPTIM_CUDA(e);
         return SPECOPTIM_OK;
