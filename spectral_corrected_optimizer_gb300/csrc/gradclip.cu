@@ -5,9 +5,9 @@
 //
 // The tensors' addresses and sizes travel in the launch's parameters (no copy to
 // the device that a captured graph would repeat), up to kMany tensors a launch.
-// Their values are cut into chunks of kChunk; a block takes neighbouring chunks,
+// Their memory is cut into chunks of 16 KB; a block takes neighbouring chunks,
 // whatever tensors they lie in, so many small tensors cost what one large one
-// does.  Each block leaves one partial; a second launch adds the partials in
+// does, and loads a chunk while it works on the one in front.  Each block leaves one partial; a second launch adds the partials in
 // their order, in every block that scales values by the result.
 #include <algorithm>
 #include <cstring>
@@ -21,12 +21,13 @@ namespace spco {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPieces = 4;                         // of 8 values, per thread and chunk
-constexpr int kChunk = kThreads * kPieces * 8;
+constexpr int kPieces = 4;                         // of 16 bytes, per thread and chunk
+constexpr int kChunk = kThreads * kPieces;         // pieces of a chunk
 constexpr int kFew = 64, kMany = 1024;             // tensors of a launch
-constexpr int kBlocksPerSm = 8;
+constexpr int kBlocksPerSm = 4;
 
-// Tensors of one launch.  first[i]: chunks in front of tensor i.
+// Tensors of one launch, as the 16-byte pieces of memory that they lie in: src[i] may begin inside its first piece.
+// first[i]: chunks in front of tensor i.
 template <int CAP> struct Table {
     int count, blocks;
     const void *src[CAP];
@@ -50,6 +51,10 @@ template <int CAP> __device__ __forceinline__ int tensor_of(const Table<CAP> &t,
     }
     return lo;
 }
+// Where a block's chunks begin among the launch's.
+template <int CAP> __device__ __forceinline__ int chunk_begin(const Table<CAP> &t, int block) {
+    return (int)((int64_t)t.first[t.count] * block / t.blocks);
+}
 
 // |b| or a, whichever is larger; NaN if one of them is
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -58,61 +63,153 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return m;
 }
 
-// A block's chunks: [begin, end) of the launch's.
-template <int CAP> __device__ __forceinline__ int chunk_begin(const Table<CAP> &t, int block) {
-    return (int)((int64_t)t.first[t.count] * block / t.blocks);
+// One tensor as pieces: values [0, size) lie at values [head, head + size) from `base`.
+template <typename T> struct Pieces {
+    static constexpr int V = 16 / (int)sizeof(T);
+    const T *base;
+    int64_t head, end;
+    __device__ __forceinline__ Pieces(const void *src, int64_t size) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(src);
+        base = reinterpret_cast<const T *>(a & ~uintptr_t(15));
+        head = (int64_t)((a & 15) / sizeof(T));
+        end = head + size;
+    }
+    // of `count` chunks from `chunk` on, those that are whole: [lo, hi), counted from `chunk`
+    __device__ __forceinline__ void whole_chunks(int chunk, int count, int &lo, int &hi) const {
+        const int64_t chunk_values = (int64_t)kChunk * V;
+        lo = chunk == 0 && head ? 1 : 0;
+        hi = (int)min((int64_t)count, end / chunk_values - chunk);
+        hi = max(lo, hi);
+        lo = min(lo, count);
+        hi = min(hi, count);
+    }
+    __device__ __forceinline__ bool whole(int64_t piece) const { return piece * V >= head && (piece + 1) * V <= end; }
+    // zeros where the tensor has no values
+    __device__ __forceinline__ uint4 load(int64_t piece) const {
+        if (whole(piece)) return reinterpret_cast<const uint4 *>(base)[piece];
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int64_t at = piece * V + i;
+            if (at < head || at >= end) continue;
+            if (sizeof(T) == 4) w[i % 4] = reinterpret_cast<const uint32_t *>(base)[at];
+            else w[i / 2 % 4] |= (uint32_t)reinterpret_cast<const uint16_t *>(base)[at] << (16 * (i & 1));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+__device__ __forceinline__ void piece_values(uint4 u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x);
+    v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z);
+    v[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void piece_values(uint4 u, float (&v)[8]) {
+    v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
+    v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
 }
 
-__device__ __forceinline__ bool vec_aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Values i .. i + 7 of a tensor, zeros behind its end.
-template <typename T> __device__ __forceinline__ void load_values(const T *p, int64_t i, int64_t size, bool vec, float (&v)[8]) {
-    if (vec && i + 8 <= size) {
-        load8(p + i, v);
-    } else if (i < size) {
-        load_any(Span<const T>(p, size), Span<const T>(p, size).lo + i, v);
-    } else {
+// A chunk's pieces of this thread.
+struct Loaded {
+    uint4 u[kPieces];
+};
+__device__ __forceinline__ Loaded load_whole(const uint4 *p) {
+    Loaded r;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    for (int k = 0; k < kPieces; ++k) r.u[k] = p[k * kThreads];
+    return r;
+}
+template <typename T> __device__ __forceinline__ Loaded load_part(const Pieces<T> &p, int64_t first) {
+    Loaded r;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) r.u[k] = p.load(first + k * kThreads);
+    return r;
+}
+
+// A block's chunks [c0, c1) of one tensor: f(tensor, its first chunk here, how many) for each, from the front or (BACK)
+// from the back.  The table is read once a tensor: an indexed read of a launch's parameters takes some 100 cycles.
+template <bool BACK, int CAP, typename F> __device__ __forceinline__ void each_tensor(const Table<CAP> &t, int c0, int c1, F &&f) {
+    if (c0 >= c1) return;
+    if (!BACK) {
+        for (int i = tensor_of(t, c0), c = c0; c < c1; ++i) {
+            const int end = min(c1, t.first[i + 1]);
+            f(i, c - t.first[i], end - c);
+            c = end;
+        }
+    } else {
+        for (int i = tensor_of(t, c1 - 1), c = c1; c > c0; --i) {
+            const int begin = max(c0, t.first[i]);
+            f(i, begin - t.first[i], c - begin);
+            c = begin;
+        }
     }
 }
 
-// What is added up of one chunk by one thread: squares, or the largest magnitude.
-// A square leaves fp32's range from 2^64 on and loses digits below 2^-50; where a
-// thread's values reach there, it squares them in 64 bits.  Otherwise a chunk's 32
-// squares are added in fp32 and the chunks in two floats: fp64 additions, 15 cycles for a
-// warp's, would take an eighth of the time.
-template <typename T, int KIND>
-__device__ __forceinline__ void take_chunk(const T *p, int64_t from, int64_t size, float &sum, float &lost, double &far, float &most) {
-    const bool vec = vec_aligned(p);
-    float v[kPieces][8];
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) load_values(p, from + (k * kThreads + (int)threadIdx.x) * 8, size, vec, v[k]);
+// What a thread has added up: squares in two floats, squares beyond their range, the largest magnitude.
+struct Sums {
+    float sum, lost, most;
+    double far;
+};
+// A square leaves fp32's range from 2^64 on and loses digits below 2^-50; where a thread's values reach there, it
+// squares them in 64 bits.  Otherwise a chunk's squares, at most 32, are added in fp32 and the chunks in two floats:
+// fp64 additions, 15 cycles for a warp's, would take an eighth of the time.
+template <typename T, int KIND> __device__ __forceinline__ void take(const Loaded &x, Sums &a) {
+    constexpr int V = 16 / (int)sizeof(T);
     float top = 0.f, s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k)
+    for (int k = 0; k < kPieces; ++k) {
+        float v[V];
+        piece_values(x.u[k], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            top = max_nan(top, v[k][i]);
-            if (KIND == NORM_L2) s = fmaf(v[k][i], v[k][i], s);
+        for (int i = 0; i < V; ++i) {
+            top = max_nan(top, v[i]);
+            if (KIND == NORM_L2) s = fmaf(v[i], v[i], s);
         }
-    most = max_nan(most, top);
-    if (KIND == NORM_L2) {
-        if (top < 0x1p50f && (top > 0x1p-50f || top == 0.f)) {
-            // below 2^105 a chunk: 2^22 of them stay within fp32
-            const float t = sum + s, u = t - sum;
-            lost += (sum - (t - u)) + (s - u);
-            sum = t;
-        } else {
-#pragma unroll 1
-            for (int k = 0; k < kPieces; ++k)
+    }
+    a.most = max_nan(a.most, top);
+    if (KIND != NORM_L2) return;
+    if (top < 0x1p50f && (top > 0x1p-50f || top == 0.f)) {
+        // below 2^105 a chunk: 2^22 of them stay within fp32
+        const float t = a.sum + s, u = t - a.sum;
+        a.lost += (a.sum - (t - u)) + (s - u);
+        a.sum = t;
+    } else {
+        // unrolled: pieces that a loop variable picks would live in local memory, for all chunks
 #pragma unroll
-                for (int i = 0; i < 8; ++i) far = fma((double)v[k][i], (double)v[k][i], far);
+        for (int k = 0; k < kPieces; ++k) {
+            float v[V];
+            piece_values(x.u[k], v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) a.far = fma((double)v[i], (double)v[i], a.far);
         }
     }
 }
 
-// Sum (or largest) over the block, to thread 0.
+// Neighbouring chunks of one tensor; the whole ones in a loop of their own, which loads a chunk while it takes the one in
+// front (a load behind a choice of ways would be waited for where the ways meet).
+template <int KIND, typename T> __device__ __forceinline__ void take_run(const Pieces<T> &p, int chunk, int count, Sums &a) {
+    int lo, hi;
+    p.whole_chunks(chunk, count, lo, hi);
+    const int64_t first = (int64_t)chunk * kChunk + threadIdx.x;
+    const auto part = [&](int from, int to) {
+        for (int c = from; c < to; ++c) take<T, KIND>(load_part(p, first + (int64_t)c * kChunk), a);
+    };
+    part(0, lo);
+    if (lo < hi) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(p.base) + first + (int64_t)lo * kChunk;
+        Loaded x = load_whole(q);
+        for (int n = hi - lo - 1; n > 0; --n) {
+            q += kChunk;
+            const Loaded y = load_whole(q);
+            take<T, KIND>(x, a);
+            x = y;
+        }
+        take<T, KIND>(x, a);
+    }
+    part(hi, count);
+}
+
+// Sum (or largest) over the block, to all threads.
 template <int KIND> __device__ __forceinline__ double block_join(double v, double *red) {
     const auto join = [](double a, double b) { return KIND == NORM_L2 ? a + b : (double)max_nan((float)a, (float)b); };
 #pragma unroll
@@ -125,20 +222,16 @@ template <int KIND> __device__ __forceinline__ double block_join(double v, doubl
 }
 
 template <int CAP, int KIND>
-__global__ void __launch_bounds__(kThreads) norm_parts_kernel(const __grid_constant__ Table<CAP> t, double *__restrict__ parts) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_parts_kernel(const __grid_constant__ Table<CAP> t, double *__restrict__ parts) {
     __shared__ double red[kWarps];
     grid_dependency_launch();
     const int c0 = chunk_begin(t, blockIdx.x), c1 = chunk_begin(t, blockIdx.x + 1);
-    float sum = 0.f, lost = 0.f, most = 0.f;
-    double far = 0.;
-    int i = c0 < c1 ? tensor_of(t, c0) : 0;
-    for (int c = c0; c < c1; ++c) {
-        while (c >= t.first[i + 1]) ++i;
-        const int64_t from = (int64_t)(c - t.first[i]) * kChunk;
-        if (t.type[i] == STAGE_BF16) take_chunk<bf16, KIND>(static_cast<const bf16 *>(t.src[i]), from, t.size[i], sum, lost, far, most);
-        else take_chunk<float, KIND>(static_cast<const float *>(t.src[i]), from, t.size[i], sum, lost, far, most);
-    }
-    const double v = block_join<KIND>(KIND == NORM_L2 ? far + ((double)sum + (double)lost) : (double)most, red);
+    Sums a{0.f, 0.f, 0.f, 0.};
+    each_tensor<false>(t, c0, c1, [&](int i, int chunk, int count) {
+        if (t.type[i] == STAGE_BF16) take_run<KIND>(Pieces<bf16>(t.src[i], t.size[i]), chunk, count, a);
+        else take_run<KIND>(Pieces<float>(t.src[i], t.size[i]), chunk, count, a);
+    });
+    const double v = block_join<KIND>(KIND == NORM_L2 ? a.far + ((double)a.sum + (double)a.lost) : (double)a.most, red);
     if (threadIdx.x == 0) parts[blockIdx.x] = v;
 }
 
@@ -171,56 +264,112 @@ __global__ void __launch_bounds__(kThreads) norm_join_kernel(const double *parts
     if (threadIdx.x == 0) *norm = n.value;
 }
 
-template <typename TI, typename TO>
-__device__ __forceinline__ void scale_chunk(const TI *p, TO *q, int64_t from, int64_t size, float factor) {
-    const bool vec = vec_aligned(p), whole = vec_aligned(q);
-    float v[kPieces][8];
+// Values of a piece to q, the place of its first one.  Written past L2's working set where nobody reads them again
+// here: what the norm's launch left of the gradients stays.
+template <bool KEEP> __device__ __forceinline__ void put(void *q, uint4 u) {
+    if (KEEP) *static_cast<uint4 *>(q) = u;
+    else __stcs(static_cast<uint4 *>(q), u);
+}
+template <bool KEEP, int V> __device__ __forceinline__ void put_values(float *q, const float (&v)[V]) {
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) load_values(p, from + (k * kThreads + (int)threadIdx.x) * 8, size, vec, v[k]);
+    for (int i = 0; i < V / 4; ++i)
+        put<KEEP>(q + 4 * i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                        __float_as_uint(v[4 * i + 3])));
+}
+template <bool KEEP> __device__ __forceinline__ void put_values(bf16 *q, const float (&v)[8]) {
+    put<KEEP>(q, make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
+}
+template <bool KEEP> __device__ __forceinline__ void put_values(bf16 *q, const float (&v)[4]) {
+    const uint2 u = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    if (KEEP) *reinterpret_cast<uint2 *>(q) = u;
+    else __stcs(reinterpret_cast<uint2 *>(q), u);
+}
+
+// A chunk that may be cut short, or whose values go to places that are not aligned.
+template <typename TI, typename TO>
+__device__ __forceinline__ void give_part(const Pieces<TI> &p, TO *q, int64_t first, float factor) {
+    constexpr int V = Pieces<TI>::V;
+    const Loaded x = load_part(p, first);
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-        const int64_t at = from + (k * kThreads + (int)threadIdx.x) * 8;
-        if (at >= size) continue;
+        float v[V];
+        piece_values(x.u[k], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] *= factor;
-        if (whole && at + 8 <= size) {
-            store8(q + at, v[k]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (at + i < size) q[at + i] = from_f<TO>(v[k][i]);
+        for (int i = 0; i < V; ++i) {
+            const int64_t at = (first + k * kThreads) * V + i;
+            if (at >= p.head && at < p.end) q[at] = from_f<TO>(v[i] * factor);
         }
     }
+}
+template <bool KEEP, typename TI, typename TO> __device__ __forceinline__ void give(const Loaded &x, TO *q, float factor) {
+    constexpr int V = Pieces<TI>::V;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        float v[V];
+        piece_values(x.u[k], v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= factor;
+        put_values<KEEP>(q + k * kThreads * V, v);
+    }
+}
+// Neighbouring chunks of one tensor, from the back.
+template <bool KEEP, typename TI, typename TO>
+__device__ __forceinline__ void give_run(const Pieces<TI> &p, void *dst, int chunk, int count, float factor) {
+    constexpr int V = Pieces<TI>::V, ALIGN = V * (int)sizeof(TO) < 16 ? V * (int)sizeof(TO) : 16;
+    TO *q = static_cast<TO *>(dst) - p.head;  // value `at` of the pieces goes to q[at]
+    int lo, hi;
+    p.whole_chunks(chunk, count, lo, hi);
+    if (reinterpret_cast<uintptr_t>(q) & (ALIGN - 1)) lo = hi = 0;
+    const int64_t first = (int64_t)chunk * kChunk + threadIdx.x;
+    const auto part = [&](int from, int to) {
+        for (int c = to - 1; c >= from; --c) give_part(p, q, first + (int64_t)c * kChunk, factor);
+    };
+    part(hi, count);
+    if (lo < hi) {
+        const int64_t last = first + (int64_t)(hi - 1) * kChunk;
+        const uint4 *from = reinterpret_cast<const uint4 *>(p.base) + last;
+        TO *to = q + last * V;
+        Loaded x = load_whole(from);
+        for (int n = hi - lo - 1; n > 0; --n) {
+            from -= kChunk;
+            const Loaded y = load_whole(from);
+            give<KEEP, TI>(x, to, factor);
+            to -= (int64_t)kChunk * V;
+            x = y;
+        }
+        give<KEEP, TI>(x, to, factor);
+    }
+    part(0, lo);
 }
 
 // The blocks go through their chunks from the back: what the norm's launch read last is in L2.
 template <int CAP, int KIND>
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<CAP> t, const __grid_constant__ Outs<CAP> o,
-                                                        const double *parts, int count, float scale, float max_norm,
-                                                        float *norm) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) clip_kernel(const __grid_constant__ Table<CAP> t,
+                                                                      const __grid_constant__ Outs<CAP> o, const double *parts,
+                                                                      int count, float scale, float max_norm, int in_place,
+                                                                      float *norm) {
     __shared__ double red[kWarps];
+    const int c0 = chunk_begin(t, blockIdx.x), c1 = chunk_begin(t, blockIdx.x + 1);
     grid_dependency_wait();
     const Norm n = norm_of<KIND>(parts, count, scale, red);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n.value;
     float factor = scale;
     if (!(n.value <= max_norm)) factor *= n.value < INFINITY ? max_norm / n.value : max_norm * 0x1p-64f / n.small;
-    const int c0 = chunk_begin(t, blockIdx.x), c1 = chunk_begin(t, blockIdx.x + 1);
-    int i = c0 < c1 ? tensor_of(t, c1 - 1) : 0;
-    for (int c = c1 - 1; c >= c0; --c) {
-        while (c < t.first[i]) --i;
-        if (factor == 1.f && o.dst[i] == t.src[i]) {  // in place and nothing to do: on to the tensor in front
-            c = t.first[i];
-            continue;
+    if (in_place && factor == 1.f) return;
+    each_tensor<true>(t, c0, c1, [&](int i, int chunk, int count) {
+        void *dst = o.dst[i];
+        if (t.type[i] == STAGE_BF16) {
+            const Pieces<bf16> p(t.src[i], t.size[i]);
+            if (o.type[i] == STAGE_FP32) give_run<false, bf16, float>(p, dst, chunk, count, factor);
+            else if (dst == t.src[i]) give_run<true, bf16, bf16>(p, dst, chunk, count, factor);
+            else give_run<false, bf16, bf16>(p, dst, chunk, count, factor);
+        } else {
+            const Pieces<float> p(t.src[i], t.size[i]);
+            if (o.type[i] == STAGE_BF16) give_run<false, float, bf16>(p, dst, chunk, count, factor);
+            else if (dst == t.src[i]) give_run<true, float, float>(p, dst, chunk, count, factor);
+            else give_run<false, float, float>(p, dst, chunk, count, factor);
         }
-        const int64_t from = (int64_t)(c - t.first[i]) * kChunk;
-        const bool in16 = t.type[i] == STAGE_BF16, out16 = o.type[i] == STAGE_BF16;
-        const bf16 *p16 = static_cast<const bf16 *>(t.src[i]);
-        const float *p32 = static_cast<const float *>(t.src[i]);
-        if (in16 && out16) scale_chunk(p16, static_cast<bf16 *>(o.dst[i]), from, t.size[i], factor);
-        else if (in16) scale_chunk(p16, static_cast<float *>(o.dst[i]), from, t.size[i], factor);
-        else if (out16) scale_chunk(p32, static_cast<bf16 *>(o.dst[i]), from, t.size[i], factor);
-        else scale_chunk(p32, static_cast<float *>(o.dst[i]), from, t.size[i], factor);
-    }
+    });
 }
 
 struct Call {
@@ -302,8 +451,9 @@ template <int CAP> void fill(const Call &c, int &at, Table<CAP> *t, Outs<CAP> *o
     t->first[0] = 0;
     for (; at < c.count && t->count < CAP; ++at) {
         if (c.sizes[at] == 0) continue;
-        const int64_t chunks = t->first[t->count] + ceil_div(c.sizes[at], kChunk);
-        if (chunks > INT32_MAX) break;  // one tensor has 2^27 at most
+        const int64_t b = (int64_t)type_bytes(c.types[at]), head = (int64_t)(reinterpret_cast<uintptr_t>(c.grads[at]) & 15);
+        const int64_t chunks = t->first[t->count] + ceil_div(head + c.sizes[at] * b, kChunk * 16);
+        if (chunks > INT32_MAX) break;  // one tensor has 2^28 at most
         const int k = t->count++;
         t->src[k] = c.grads[at];
         t->size[k] = c.sizes[at];
@@ -323,6 +473,8 @@ template <int CAP, int KIND> int run(const Call &c) {
     double *parts = static_cast<double *>(c.workspace);
     int total = 0, launches = 0;
     const int64_t room = workspace_of(c.count) / 8;
+    int in_place = c.outs != nullptr;
+    for (int i = 0; in_place && i < c.count; ++i) in_place = c.sizes[i] == 0 || c.outs[i] == c.grads[i];
     for (int at = 0; at < c.count;) {
         fill(c, at, &t, &o);
         if (!t.count) break;
@@ -346,7 +498,7 @@ template <int CAP, int KIND> int run(const Call &c) {
         if (!t.count) break;
         SPCO_LAUNCH("clip_grads", c.st,
                     e = launch_dependent(clip_kernel<CAP, KIND>, dim3(t.blocks), dim3(kThreads), 0, c.st, t, o, parts, total,
-                                         c.scale, c.max_norm, c.norm));
+                                         c.scale, c.max_norm, in_place, c.norm));
         SPECOPTIM_CUDA(e);
     }
     return SPECOPTIM_OK;
