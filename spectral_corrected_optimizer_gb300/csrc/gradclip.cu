@@ -126,22 +126,14 @@ template <typename T> __device__ __forceinline__ Loaded load_part(const Pieces<T
     return r;
 }
 
-// A block's chunks [c0, c1) of one tensor: f(tensor, its first chunk here, how many) for each, from the front or (BACK)
-// from the back.  The table is read once a tensor: an indexed read of a launch's parameters takes some 100 cycles.
-template <bool BACK, int CAP, typename F> __device__ __forceinline__ void each_tensor(const Table<CAP> &t, int c0, int c1, F &&f) {
+// f(tensor, its first chunk here, how many) for each tensor that chunks [c0, c1) lie in.  The table is read once a
+// tensor: an indexed read of a launch's parameters takes some 100 cycles.
+template <int CAP, typename F> __device__ __forceinline__ void each_tensor(const Table<CAP> &t, int c0, int c1, F &&f) {
     if (c0 >= c1) return;
-    if (!BACK) {
-        for (int i = tensor_of(t, c0), c = c0; c < c1; ++i) {
-            const int end = min(c1, t.first[i + 1]);
-            f(i, c - t.first[i], end - c);
-            c = end;
-        }
-    } else {
-        for (int i = tensor_of(t, c1 - 1), c = c1; c > c0; --i) {
-            const int begin = max(c0, t.first[i]);
-            f(i, begin - t.first[i], c - begin);
-            c = begin;
-        }
+    for (int i = tensor_of(t, c0), c = c0; c < c1; ++i) {
+        const int end = min(c1, t.first[i + 1]);
+        f(i, c - t.first[i], end - c);
+        c = end;
     }
 }
 
@@ -150,9 +142,9 @@ struct Sums {
     float sum, lost, most;
     double far;
 };
-// A square leaves fp32's range from 2^64 on and loses digits below 2^-50; where a thread's values reach there, it
-// squares them in 64 bits.  Otherwise a chunk's squares, at most 32, are added in fp32 and the chunks in two floats:
-// fp64 additions, 15 cycles for a warp's, would take an eighth of the time.
+// A square leaves fp32's range from 2^64 on and loses digits below 2^-50; where a thread's values reach 2^40 or stay
+// below 2^-50, it squares them in 64 bits.  Otherwise a chunk's squares, at most 32, are added in fp32 and the chunks in
+// two floats (sums of 2^44 values stay below 2^128): fp64 additions take 15 cycles for a warp's.
 template <typename T, int KIND> __device__ __forceinline__ void take(const Loaded &x, Sums &a) {
     constexpr int V = 16 / (int)sizeof(T);
     float top = 0.f, s = 0.f;
@@ -168,8 +160,7 @@ template <typename T, int KIND> __device__ __forceinline__ void take(const Loade
     }
     a.most = max_nan(a.most, top);
     if (KIND != NORM_L2) return;
-    if (top < 0x1p50f && (top > 0x1p-50f || top == 0.f)) {
-        // below 2^105 a chunk: 2^22 of them stay within fp32
+    if (top < 0x1p40f && (top > 0x1p-50f || top == 0.f)) {
         const float t = a.sum + s, u = t - a.sum;
         a.lost += (a.sum - (t - u)) + (s - u);
         a.sum = t;
@@ -209,29 +200,49 @@ template <int KIND, typename T> __device__ __forceinline__ void take_run(const P
     part(hi, count);
 }
 
-// Sum (or largest) over the block, to all threads.
-template <int KIND> __device__ __forceinline__ double block_join(double v, double *red) {
-    const auto join = [](double a, double b) { return KIND == NORM_L2 ? a + b : (double)max_nan((float)a, (float)b); };
+// What a thread or a block leaves: squares in two floats (or the largest magnitude) and those beyond their range.
+struct __align__(16) Part {
+    float sum, lost;
+    double far;
+};
+template <int KIND> __device__ __forceinline__ void join(Part &a, const Part &b) {
+    if (KIND == NORM_MAX) {
+        a.sum = max_nan(a.sum, b.sum);
+        return;
+    }
+    const float t = a.sum + b.sum, u = t - a.sum;
+    a.lost += b.lost + ((a.sum - (t - u)) + (b.sum - u));
+    a.sum = t;
+}
+// Over the block, to all threads; in a fixed order.
+template <int KIND> __device__ __forceinline__ Part block_join(Part v, Part *red) {
+    const bool far = KIND == NORM_L2 && __syncthreads_or(v.far != 0.);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o >= 1; o >>= 1) {
+        join<KIND>(v, Part{__shfl_xor_sync(0xffffffffu, v.sum, o), __shfl_xor_sync(0xffffffffu, v.lost, o), 0.});
+        if (far) v.far += __shfl_xor_sync(0xffffffffu, v.far, o);
+    }
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     v = red[0];
-    for (int i = 1; i < kWarps; ++i) v = join(v, red[i]);
+    for (int i = 1; i < kWarps; ++i) {
+        join<KIND>(v, red[i]);
+        if (far) v.far += red[i].far;
+    }
     return v;
 }
 
 template <int CAP, int KIND>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_parts_kernel(const __grid_constant__ Table<CAP> t, double *__restrict__ parts) {
-    __shared__ double red[kWarps];
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_parts_kernel(const __grid_constant__ Table<CAP> t, Part *__restrict__ parts) {
+    __shared__ Part red[kWarps];
     grid_dependency_launch();
     const int c0 = chunk_begin(t, blockIdx.x), c1 = chunk_begin(t, blockIdx.x + 1);
     Sums a{0.f, 0.f, 0.f, 0.};
-    each_tensor<false>(t, c0, c1, [&](int i, int chunk, int count) {
+    each_tensor(t, c0, c1, [&](int i, int chunk, int count) {
         if (t.type[i] == STAGE_BF16) take_run<KIND>(Pieces<bf16>(t.src[i], t.size[i]), chunk, count, a);
         else take_run<KIND>(Pieces<float>(t.src[i], t.size[i]), chunk, count, a);
     });
-    const double v = block_join<KIND>(KIND == NORM_L2 ? a.far + ((double)a.sum + (double)a.lost) : (double)a.most, red);
+    const Part v = block_join<KIND>(KIND == NORM_L2 ? Part{a.sum, a.lost, a.far} : Part{a.most, 0.f, 0.}, red);
     if (threadIdx.x == 0) parts[blockIdx.x] = v;
 }
 
@@ -240,49 +251,44 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_parts_kernel(cons
 struct Norm {
     float value, small;
 };
-template <int KIND> __device__ __forceinline__ Norm norm_of(const double *parts, int count, float scale, double *red) {
-    double v = 0.;
+template <int KIND> __device__ __forceinline__ Norm norm_of(const Part *parts, int count, float scale, Part *red) {
+    Part v{0.f, 0.f, 0.};
+#pragma unroll 4
     for (int i = threadIdx.x; i < count; i += kThreads) {
-        const double x = parts[i];
-        v = KIND == NORM_L2 ? v + x : (double)max_nan((float)v, (float)x);
+        const Part x = parts[i];
+        join<KIND>(v, x);
+        if (KIND == NORM_L2 && x.far != 0.) v.far += x.far;
     }
     v = block_join<KIND>(v, red);
-    // fp64 arithmetic is slow: for what fp32 cannot do
-    if (KIND == NORM_L2 && v > 0x1p-100 && v < 0x1p120) {
-        const float n = fabsf(scale) * sqrtf((float)v);
-        return {n, n * 0x1p-64f};
+    if (KIND == NORM_L2 && v.far != 0.) {
+        const double n = fabs((double)scale) * sqrt(v.far + ((double)v.sum + (double)v.lost));
+        return {(float)n, (float)(n * 0x1p-64)};
     }
-    const double n = fabs((double)scale) * (KIND == NORM_L2 ? sqrt(v) : v);
-    return {(float)n, (float)(n * 0x1p-64)};
+    const float n = KIND == NORM_L2 ? sqrtf(v.sum + v.lost) : v.sum;
+    return {fabsf(scale) * n, fabsf(scale) * 0x1p-64f * n};
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(kThreads) norm_join_kernel(const double *parts, int count, float scale, float *norm) {
-    __shared__ double red[kWarps];
+__global__ void __launch_bounds__(kThreads) norm_join_kernel(const Part *parts, int count, float scale, float *norm) {
+    __shared__ Part red[kWarps];
     grid_dependency_wait();
     const Norm n = norm_of<KIND>(parts, count, scale, red);
     if (threadIdx.x == 0) *norm = n.value;
 }
 
-// Values of a piece to q, the place of its first one.  Written past L2's working set where nobody reads them again
-// here: what the norm's launch left of the gradients stays.
-template <bool KEEP> __device__ __forceinline__ void put(void *q, uint4 u) {
-    if (KEEP) *static_cast<uint4 *>(q) = u;
-    else __stcs(static_cast<uint4 *>(q), u);
+// Values of a piece to q, the place of its first one.
+__device__ __forceinline__ void put_values(float *q, const float (&v)[4]) {
+    *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
 }
-template <bool KEEP, int V> __device__ __forceinline__ void put_values(float *q, const float (&v)[V]) {
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i)
-        put<KEEP>(q + 4 * i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                        __float_as_uint(v[4 * i + 3])));
+// 32 bytes as one store: two of 16 write each sector in halves (one layer's bf16 gradients to fp32: 61 us, 78 with two)
+__device__ __forceinline__ void put_values(float *q, const float (&v)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
 }
-template <bool KEEP> __device__ __forceinline__ void put_values(bf16 *q, const float (&v)[8]) {
-    put<KEEP>(q, make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
-}
-template <bool KEEP> __device__ __forceinline__ void put_values(bf16 *q, const float (&v)[4]) {
-    const uint2 u = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    if (KEEP) *reinterpret_cast<uint2 *>(q) = u;
-    else __stcs(reinterpret_cast<uint2 *>(q), u);
+__device__ __forceinline__ void put_values(bf16 *q, const float (&v)[8]) { store8(q, v); }
+__device__ __forceinline__ void put_values(bf16 *q, const float (&v)[4]) {
+    *reinterpret_cast<uint2 *>(q) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
 // A chunk that may be cut short, or whose values go to places that are not aligned.
@@ -301,7 +307,7 @@ __device__ __forceinline__ void give_part(const Pieces<TI> &p, TO *q, int64_t fi
         }
     }
 }
-template <bool KEEP, typename TI, typename TO> __device__ __forceinline__ void give(const Loaded &x, TO *q, float factor) {
+template <typename TI, typename TO> __device__ __forceinline__ void give(const Loaded &x, TO *q, float factor) {
     constexpr int V = Pieces<TI>::V;
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
@@ -309,46 +315,44 @@ template <bool KEEP, typename TI, typename TO> __device__ __forceinline__ void g
         piece_values(x.u[k], v);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] *= factor;
-        put_values<KEEP>(q + k * kThreads * V, v);
+        put_values(q + k * kThreads * V, v);
     }
 }
-// Neighbouring chunks of one tensor, from the back.
-template <bool KEEP, typename TI, typename TO>
+// Neighbouring chunks of one tensor, the whole ones in a loop that loads ahead.
+template <typename TI, typename TO>
 __device__ __forceinline__ void give_run(const Pieces<TI> &p, void *dst, int chunk, int count, float factor) {
-    constexpr int V = Pieces<TI>::V, ALIGN = V * (int)sizeof(TO) < 16 ? V * (int)sizeof(TO) : 16;
+    constexpr int V = Pieces<TI>::V, ALIGN = V * (int)sizeof(TO);  // of a piece's values
     TO *q = static_cast<TO *>(dst) - p.head;  // value `at` of the pieces goes to q[at]
     int lo, hi;
     p.whole_chunks(chunk, count, lo, hi);
     if (reinterpret_cast<uintptr_t>(q) & (ALIGN - 1)) lo = hi = 0;
     const int64_t first = (int64_t)chunk * kChunk + threadIdx.x;
     const auto part = [&](int from, int to) {
-        for (int c = to - 1; c >= from; --c) give_part(p, q, first + (int64_t)c * kChunk, factor);
+        for (int c = from; c < to; ++c) give_part(p, q, first + (int64_t)c * kChunk, factor);
     };
-    part(hi, count);
+    part(0, lo);
     if (lo < hi) {
-        const int64_t last = first + (int64_t)(hi - 1) * kChunk;
-        const uint4 *from = reinterpret_cast<const uint4 *>(p.base) + last;
-        TO *to = q + last * V;
+        const uint4 *from = reinterpret_cast<const uint4 *>(p.base) + first + (int64_t)lo * kChunk;
+        TO *to = q + (first + (int64_t)lo * kChunk) * V;
         Loaded x = load_whole(from);
         for (int n = hi - lo - 1; n > 0; --n) {
-            from -= kChunk;
+            from += kChunk;
             const Loaded y = load_whole(from);
-            give<KEEP, TI>(x, to, factor);
-            to -= (int64_t)kChunk * V;
+            give<TI>(x, to, factor);
+            to += (int64_t)kChunk * V;
             x = y;
         }
-        give<KEEP, TI>(x, to, factor);
+        give<TI>(x, to, factor);
     }
-    part(0, lo);
+    part(hi, count);
 }
 
-// The blocks go through their chunks from the back: what the norm's launch read last is in L2.
 template <int CAP, int KIND>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) clip_kernel(const __grid_constant__ Table<CAP> t,
-                                                                      const __grid_constant__ Outs<CAP> o, const double *parts,
+                                                                      const __grid_constant__ Outs<CAP> o, const Part *parts,
                                                                       int count, float scale, float max_norm, int in_place,
                                                                       float *norm) {
-    __shared__ double red[kWarps];
+    __shared__ Part red[kWarps];
     const int c0 = chunk_begin(t, blockIdx.x), c1 = chunk_begin(t, blockIdx.x + 1);
     grid_dependency_wait();
     const Norm n = norm_of<KIND>(parts, count, scale, red);
@@ -356,18 +360,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) clip_kernel(const __gr
     float factor = scale;
     if (!(n.value <= max_norm)) factor *= n.value < INFINITY ? max_norm / n.value : max_norm * 0x1p-64f / n.small;
     if (in_place && factor == 1.f) return;
-    each_tensor<true>(t, c0, c1, [&](int i, int chunk, int count) {
+    each_tensor(t, c0, c1, [&](int i, int chunk, int count) {
         void *dst = o.dst[i];
         if (t.type[i] == STAGE_BF16) {
             const Pieces<bf16> p(t.src[i], t.size[i]);
-            if (o.type[i] == STAGE_FP32) give_run<false, bf16, float>(p, dst, chunk, count, factor);
-            else if (dst == t.src[i]) give_run<true, bf16, bf16>(p, dst, chunk, count, factor);
-            else give_run<false, bf16, bf16>(p, dst, chunk, count, factor);
+            if (o.type[i] == STAGE_BF16) give_run<bf16, bf16>(p, dst, chunk, count, factor);
+            else give_run<bf16, float>(p, dst, chunk, count, factor);
         } else {
             const Pieces<float> p(t.src[i], t.size[i]);
-            if (o.type[i] == STAGE_BF16) give_run<false, float, bf16>(p, dst, chunk, count, factor);
-            else if (dst == t.src[i]) give_run<true, float, float>(p, dst, chunk, count, factor);
-            else give_run<false, float, float>(p, dst, chunk, count, factor);
+            if (o.type[i] == STAGE_BF16) give_run<float, bf16>(p, dst, chunk, count, factor);
+            else give_run<float, float>(p, dst, chunk, count, factor);
         }
     });
 }
@@ -389,7 +391,7 @@ struct Call {
 
 int64_t workspace_of(int32_t count) {
     const int64_t launches = std::max<int64_t>(1, ceil_div(count, kMany));
-    return launches * num_sms() * kBlocksPerSm * 8;
+    return launches * num_sms() * kBlocksPerSm * (int64_t)sizeof(Part);
 }
 
 // No value is written twice, and none is read after another place's was written to it.
@@ -470,9 +472,9 @@ template <int CAP> void fill(const Call &c, int &at, Table<CAP> *t, Outs<CAP> *o
 template <int CAP, int KIND> int run(const Call &c) {
     Table<CAP> t;
     Outs<CAP> o;
-    double *parts = static_cast<double *>(c.workspace);
+    Part *parts = static_cast<Part *>(c.workspace);
     int total = 0, launches = 0;
-    const int64_t room = workspace_of(c.count) / 8;
+    const int64_t room = workspace_of(c.count) / (int64_t)sizeof(Part);
     int in_place = c.outs != nullptr;
     for (int i = 0; in_place && i < c.count; ++i) in_place = c.sizes[i] == 0 || c.outs[i] == c.grads[i];
     for (int at = 0; at < c.count;) {
