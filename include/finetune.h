@@ -11,7 +11,8 @@
  * tensors aligned to their elements (16-byte aligned ones take the vectorised
  * paths), asynchronous calls on `stream` that allocate nothing, workspaces of
  * the caller's (16-byte aligned, at least the bytes that the *_workspace
- * function returns, which is -1 for sizes that the call refuses), the status
+ * function returns, which is -1 for sizes that the call refuses; it may be NULL
+ * where that is 0), the status
  * codes of specoptim.h.  No sum is formed by floating-point atomics: results
  * repeat bit for bit.  Outputs do not overlap inputs or one another unless a
  * call says that they may.

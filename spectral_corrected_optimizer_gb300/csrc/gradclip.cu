@@ -508,9 +508,9 @@ template <int CAP, int KIND> int run(const Call &c) {
 
 int run_call(const Call &c, bool clip, const char *what) {
     if (int rc = check_call(c, clip, what)) return rc;
-    if (int rc = bind_device()) return rc;
     if (c.workspace_bytes < workspace_of(c.count))
         return fail(SPECOPTIM_ERR_INVALID_ARG, std::string(what) + ": the workspace is smaller than grad_norm_workspace() says");
+    if (int rc = bind_device()) return rc;
     if (c.kind == NORM_L2) return c.count <= kFew ? run<kFew, NORM_L2>(c) : run<kMany, NORM_L2>(c);
     return c.count <= kFew ? run<kFew, NORM_MAX>(c) : run<kMany, NORM_MAX>(c);
 }

@@ -86,16 +86,34 @@ __device__ __forceinline__ bool has_target(int64_t id, int64_t ignore, int vocab
     return id != ignore && id >= 0 && id < vocab;
 }
 
+// What the backward pass of the log-probabilities has of each token: its gradient, and what the forward pass kept
+// ([3][tokens]).  Null where a loss is formed.
+struct HeadGiven {
+    const float *dlogp, *kept;
+    HeadNorm *norm;  // [row_cap]
+
+    // a token without a gradient takes no part
+    __device__ __forceinline__ bool takes_part(int t) const { return !dlogp || dlogp[t] != 0.f; }
+    // what turns row r's logits into -dlogp (softmax - onehot)
+    __device__ __forceinline__ void set(int r, int t, int tokens) const {
+        if (!dlogp) return;
+        const float g = dlogp[t];
+        norm[r] = HeadNorm{kept[t], -g * kept[tokens + t], g * kept[2 * tokens + t]};
+    }
+};
+
 // Targets among each kStretch neighbouring tokens.
 constexpr int kStretch = 4096;
 template <typename ID>
 __global__ void __launch_bounds__(kRowThreads) head_count_kernel(const ID *__restrict__ targets, int64_t ignore,
-                                                                 int vocab, int *__restrict__ counts) {
-    const ID *from = targets + (int64_t)blockIdx.x * kStretch;
+                                                                 int vocab, const HeadGiven given, int *__restrict__ counts) {
+    const int from = blockIdx.x * kStretch;
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < kStretch; i += kRowThreads)
-        n += __syncthreads_count(has_target((int64_t)from[i + threadIdx.x], ignore, vocab));
+    for (int i = 0; i < kStretch; i += kRowThreads) {
+        const int t = from + i + (int)threadIdx.x;
+        n += __syncthreads_count(has_target((int64_t)targets[t], ignore, vocab) && given.takes_part(t));
+    }
     if (threadIdx.x == 0) counts[blockIdx.x] = n;
 }
 
@@ -121,7 +139,7 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
                                                         int *__restrict__ at, int *__restrict__ target,
                                                         uint16_t *__restrict__ out, HeadRow *__restrict__ head_row,
                                                         float *__restrict__ row_loss, float *__restrict__ kept,
-                                                        unsigned *flag) {
+                                                        const HeadGiven given, unsigned *flag) {
     __shared__ int red[2][kRowWarps], own_token[kRowThreads], own_target[kRowThreads];
     __shared__ float dots[kRowWarps];
     __shared__ int held[kRowWarps];
@@ -136,13 +154,14 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
         first = whole * kStretch;
     }
 #pragma unroll 4
-    for (int t = first + threadIdx.x; t < t0; t += kRowThreads) before += has_target((int64_t)targets[t], ignore, vocab);
+    for (int t = first + threadIdx.x; t < t0; t += kRowThreads)
+        before += has_target((int64_t)targets[t], ignore, vocab) && given.takes_part(t);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     const int t = t0 + threadIdx.x;
     const int64_t id = t < t1 ? (int64_t)targets[t] : ignore;
-    const bool has = has_target(id, ignore, vocab);
-    if (id != ignore && !has) atomicExch(flag, kSiteTarget);
+    const bool known = has_target(id, ignore, vocab), has = known && given.takes_part(t);
+    if (id != ignore && !known) atomicExch(flag, kSiteTarget);
     const unsigned ballot = __ballot_sync(0xffffffffu, has);
     if (lane == 0) {
         red[0][wp] = before;
@@ -163,6 +182,7 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const ID *__rest
         target[before + k] = (int)id;
         own_token[k] = t;
         own_target[k] = (int)id;
+        given.set(before + k, t, tokens);
     } else if (t < t1) {
         if (row_loss) row_loss[t] = 0.f;
         if (kept) kept[t] = kept[tokens + t] = kept[2 * tokens + t] = 0.f;
@@ -342,32 +362,6 @@ __global__ void __launch_bounds__(kLseThreads) head_lse_kernel(const float2 *sta
     if (lane == 0) *loss = l * state->inv_count;
 }
 
-// What turns the rows' logits into -dlogp (softmax - onehot), from what the forward pass kept.
-__global__ void __launch_bounds__(256) head_weight_kernel(const float *dlogp, const float *kept, int tokens, const int *row_of,
-                                                          const HeadState *state, HeadNorm *norm) {
-    grid_dependency_launch();
-    grid_dependency_wait();
-    const int rows = state->rows;
-    for (int r = blockIdx.x * 256 + threadIdx.x; r < rows; r += gridDim.x * 256) {
-        const int t = row_of[r];
-        const float g = dlogp[t];
-        norm[r] = HeadNorm{kept[t], -g * kept[tokens + t], g * kept[2 * tokens + t]};
-    }
-}
-
-// The targets of the tokens that have a gradient, -1 for the others.
-template <typename ID>
-__global__ void __launch_bounds__(256) head_select_kernel(const ID *__restrict__ targets, int64_t ignore, int tokens, int vocab,
-                                                          const float *__restrict__ dlogp, int *__restrict__ out,
-                                                          unsigned *flag) {
-    for (int t = blockIdx.x * 256 + threadIdx.x; t < tokens; t += gridDim.x * 256) {
-        const int64_t id = (int64_t)targets[t];
-        const bool has = has_target(id, ignore, vocab);
-        if (id != ignore && !has) atomicExch(flag, kSiteTarget);
-        out[t] = has && dlogp[t] != 0.f ? (int)id : -1;
-    }
-}
-
 // dh[t] = factor * sum over the parts of the token's row; zero without a target.
 // The sums' rows are read from where dh's 16-byte pieces begin (VEC: column 0).
 template <bool VEC>
@@ -414,7 +408,7 @@ constexpr int kPieceMin = 4096;
 struct HeadPlan {
     int row_cap, ld, parts, piece, pieces, splits, dh_ld;
     int64_t off_state, off_counts, off_row_of, off_at, off_target, off_head_row, off_norm, off_block_loss, off_stats,
-        off_h, off_w, off_p0, off_p1, off_dh, off_loss, off_selected, bytes;
+        off_h, off_w, off_p0, off_p1, off_dh, off_loss, bytes;
 };
 
 // stats: the row statistics are formed; grad: the gradients
@@ -458,7 +452,6 @@ HeadPlan plan_head(int64_t tokens, int64_t vocab, int32_t dim, bool grad, bool s
         p.off_dh = take((int64_t)p.splits * cap * p.dh_ld * 4);
     }
     p.off_loss = take(4);
-    p.off_selected = stats ? 0 : take(tokens * 4);
     p.bytes = at;
     return p;
 }
@@ -484,7 +477,8 @@ struct HeadCall {
     int64_t ws_bytes;
     cudaStream_t st;
     float *kept = nullptr;   // log-probabilities instead of losses, and what their backward pass needs
-    bool backward = false;   // that pass: loss and row_loss are not there
+    const float *dlogp = nullptr, *given = nullptr;  // of that pass
+    bool backward = false;   // it is that pass: loss and row_loss are not there
 };
 
 int check_call(const HeadCall &c, const HeadPlan &p, const std::string &what) {
@@ -521,17 +515,18 @@ int run_rows(const HeadCall &c, const HeadPlan &p, bool grad, HeadGemm *g) {
     const int blocks = (int)std::max<int64_t>(1, ceil_div(tokens, share));
     const bool w_vec = c.dim % 8 == 0, h_vec = w_vec && aligned16(c.h);
     int *counts = tokens >= kCountTokens ? reinterpret_cast<int *>(c.ws + p.off_counts) : nullptr;
+    const HeadGiven given{c.dlogp, c.given, norm};
     auto rows = [&](auto id) {
         using ID = decltype(id);
         if (counts)
             SPCO_LAUNCH("head_count", c.st,
                         head_count_kernel<ID><<<tokens / kStretch, kRowThreads, 0, c.st>>>(
-                            static_cast<const ID *>(c.targets), c.ignore, vocab, counts));
+                            static_cast<const ID *>(c.targets), c.ignore, vocab, given, counts));
         SPCO_LAUNCH("head_rows", c.st,
                     head_rows_kernel<ID><<<blocks + (grad ? kPadBlocks : 0), kRowThreads, 0, c.st>>>(
                         static_cast<const ID *>(c.targets), c.ignore, tokens, vocab, c.mean, share, blocks, counts,
                         static_cast<const uint16_t *>(c.h), w, c.dim, p.row_cap, h_vec, w_vec, state, row_of, at, target,
-                        hc, head_row, c.row_loss, c.kept, stage_flag_ptr()));
+                        hc, head_row, c.row_loss, c.kept, given, stage_flag_ptr()));
     };
     if (c.id_bytes == 8) rows(int64_t{});
     else rows(int32_t{});
@@ -759,33 +754,13 @@ extern "C" int head_logp_backward(const float *dlogp, const float *kept, const v
         HeadCall c{h, w, targets, id_bytes, ignore_index, tokens, vocab, dim, 0, nullptr, nullptr,
                    static_cast<char *>(workspace), workspace_bytes, static_cast<cudaStream_t>(stream)};
         c.backward = true;
+        c.dlogp = dlogp;
+        c.given = kept;
         if (int rc = check_call(c, p, "head_logp_backward")) return rc;
         if (int rc = check_grad(c, dh, dw, dw_type, "head_logp_backward")) return rc;
         if (int rc = bind_device()) return rc;
-        // the targets of the tokens with a gradient stand in for all of them
-        int *selected = reinterpret_cast<int *>(c.ws + p.off_selected);
-        const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(tokens, 256), num_sms() * 8));
-        auto select = [&](auto id) {
-            using ID = decltype(id);
-            SPCO_LAUNCH("head_select", c.st,
-                        head_select_kernel<ID><<<blocks, 256, 0, c.st>>>(static_cast<const ID *>(targets), ignore_index,
-                                                                         (int)tokens, (int)vocab, dlogp, selected,
-                                                                         stage_flag_ptr()));
-        };
-        if (id_bytes == 8) select(int64_t{});
-        else select(int32_t{});
-        SPECOPTIM_LAUNCHED("head_select_kernel");
-        c.targets = selected;
-        c.id_bytes = 4;
-        c.ignore = -1;
         HeadGemm g;
         if (int rc = run_rows(c, p, true, &g)) return rc;
-        cudaError_t e = cudaSuccess;
-        SPCO_LAUNCH("head_weight", c.st,
-                    e = launch_dependent(head_weight_kernel, dim3(blocks), dim3(256), 0, c.st, dlogp, kept, (int)tokens,
-                                         reinterpret_cast<const int *>(c.ws + p.off_row_of), g.state,
-                                         reinterpret_cast<HeadNorm *>(c.ws + p.off_norm)));
-        SPECOPTIM_CUDA(e);
         return run_grad(c, p, &g, dh, dw, dw_type, accumulate, 1.f);
     });
 }

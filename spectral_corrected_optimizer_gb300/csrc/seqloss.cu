@@ -809,7 +809,7 @@ int check_common(int64_t count, int64_t tokens, const void *logp, const void *of
     if (count < 0 || count > kMost) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": sequences outside [0, 2^30]");
     if (tokens < 0 || tokens > kMost) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": tokens outside [0, 2^30]");
     if (offset_bytes != 4 && offset_bytes != 8) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": offset_bytes must be 4 or 8");
-    if (!loss || !workspace || (need_offsets && !offsets) || (tokens > 0 && (!logp || !dlogp)))
+    if (!loss || (need_offsets && !offsets) || (tokens > 0 && (!logp || !dlogp)))
         return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": null pointer");
     if (!aligned_to(logp, 4) || !aligned_to(offsets, offset_bytes) || !aligned_to(loss, 4) || !aligned_to(dlogp, 4) ||
         !aligned16(workspace))
@@ -823,11 +823,17 @@ bool all_aligned16(std::initializer_list<const void *> p, const void *mask) {
     return aligned_to(mask, 4);
 }
 
+// scores of the slices; none where a block has a pair
+int64_t preference_bytes(int64_t pairs, int64_t tokens) {
+    const int bits = slice_bits_of(pairs, tokens);
+    return bits ? (pairs << bits) * 2 * 16 : 0;
+}
 // partial sums of the blocks
 int64_t partial_bytes() { return (int64_t)num_sms() * kTileBlocks * 16; }
 // and of the policy loss: counts, each tile's first sequence, each sequence's weight
 constexpr int kMostCounts = 512;
-int64_t policy_bytes(int64_t sequences, int64_t tokens) {
+int64_t policy_bytes(bool by_offsets, int64_t sequences, int64_t tokens) {
+    if (alone((int)(by_offsets ? sequences : ceil_div(tokens, kUnit)), tokens)) return 0;
     return partial_bytes() + 16 * ceil_div(tokens, kTile) + 4 * (kMostCounts + sequences);
 }
 
@@ -848,7 +854,7 @@ extern "C" int64_t preference_loss_workspace(int64_t pairs, int64_t tokens) {
     entry([&]() -> int {
         if (pairs < 0 || pairs > kMost / 2 || tokens < 0 || tokens > kMost)
             return fail(SPECOPTIM_ERR_INVALID_ARG, "preference_loss: pairs outside [0, 2^29] or tokens outside [0, 2^30]");
-        bytes = std::max<int64_t>(16, (pairs << slice_bits_of(pairs, tokens)) * 2 * 16);
+        bytes = preference_bytes(pairs, tokens);
         return SPECOPTIM_OK;
     });
     return bytes;
@@ -872,9 +878,11 @@ extern "C" int preference_loss(const float *logp, const float *ref_logp, const u
         if (pairs > 0 && (!pair_loss || !rewards)) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": null pointer");
         if (!aligned_to(ref_logp, 4) || !aligned_to(pair_loss, 4) || !aligned_to(rewards, 4))
             return fail(SPECOPTIM_ERR_MISALIGNED, what + ": pointers must be aligned to their elements");
-        if (int rc = bind_device()) return rc;
-        if (workspace_bytes < (pairs << slice_bits_of(pairs, tokens)) * 2 * 16)
+        const int64_t need = preference_bytes(pairs, tokens);
+        if (need && !workspace) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": null pointer");
+        if (workspace_bytes < need)
             return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": the workspace is smaller than preference_loss_workspace() says");
+        if (int rc = bind_device()) return rc;
         const float part = mean ? 1.f / (float)std::max<int64_t>(pairs, 1) : 1.f;
         const bool one = alone((int)pairs, tokens);
         const int bits = slice_bits_of(pairs, tokens);
@@ -920,7 +928,8 @@ extern "C" int64_t policy_loss_workspace(int64_t sequences, int64_t tokens) {
     entry([&]() -> int {
         if (sequences < 0 || sequences > kMost || tokens < 0 || tokens > kMost)
             return fail(SPECOPTIM_ERR_INVALID_ARG, "policy_loss: sequences or tokens outside [0, 2^30]");
-        bytes = policy_bytes(sequences, tokens);
+        // one sequence may stand for none
+        bytes = std::max(policy_bytes(true, sequences, tokens), sequences == 1 ? policy_bytes(false, 1, tokens) : 0);
         return SPECOPTIM_OK;
     });
     return bytes;
@@ -948,9 +957,11 @@ extern "C" int policy_loss(const float *logp, const float *old_logp, const float
             return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": null pointer");
         if (!aligned_to(old_logp, 4) || !aligned_to(ref_logp, 4) || !aligned_to(advantages, 4) || !aligned_to(parts, 4))
             return fail(SPECOPTIM_ERR_MISALIGNED, what + ": pointers must be aligned to their elements");
-        if (int rc = bind_device()) return rc;
-        if (workspace_bytes < policy_bytes(sequences, tokens))
+        const int64_t need = policy_bytes(offsets != nullptr, sequences, tokens);
+        if (need && !workspace) return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": null pointer");
+        if (workspace_bytes < need)
             return fail(SPECOPTIM_ERR_INVALID_ARG, what + ": the workspace is smaller than policy_loss_workspace() says");
+        if (int rc = bind_device()) return rc;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         if (!offsets && reduction == POLICY_SEQUENCE_MEAN) reduction = POLICY_TOKEN_MEAN;
         const int tiles = (int)ceil_div(tokens, kTile), units = (int)(offsets ? sequences : ceil_div(tokens, kUnit));

@@ -172,6 +172,14 @@ def head_logp_backward(dlogp, kept, h, w, targets, ignore_index: int = -100, dty
 
 # ---------------------------------------------------------------- losses over log-probabilities
 
+def _room(nbytes, device, what):
+    """Workspace, its pointer and its size; small calls need none."""
+    if nbytes == 0:
+        return None, None, 0
+    ws, pointer = _workspace(nbytes, device, what)
+    return ws, pointer, ws.numel()
+
+
 def _per_token(t, tokens, device, name):
     return None if t is None else _matrix(t, (tokens,), torch.float32, device, name)
 
@@ -221,10 +229,10 @@ def preference_loss(logp, ref_logp, offsets, beta: float = 0.1, kind: str = "log
     pair_loss = torch.empty(pairs, dtype=torch.float32, device=device)
     rewards = torch.empty((pairs, 2), dtype=torch.float32, device=device)
     dlogp = torch.empty(tokens, dtype=torch.float32, device=device)
-    ws, wsp = _workspace(lib().preference_loss_workspace(pairs, tokens), device, "preference_loss")
+    ws, wsp, wsn = _room(lib().preference_loss_workspace(pairs, tokens), device, "preference_loss")
     _check(lib().preference_loss(lp, rp, mp, op, ob, pairs, tokens, code, beta, smoothing, average, reduction == "mean",
                                  grad_scale, loss.data_ptr(), pair_loss.data_ptr(), rewards.data_ptr(),
-                                 dlogp.data_ptr(), wsp, ws.numel(), _stream(device)), "preference_loss")
+                                 dlogp.data_ptr(), wsp, wsn, _stream(device)), "preference_loss")
     return loss, pair_loss, rewards, dlogp
 
 
@@ -266,10 +274,10 @@ def policy_loss(logp, old_logp, advantages, offsets=None, ref_logp=None, mask=No
     loss = torch.empty((), dtype=torch.float32, device=device)
     parts = torch.empty(3, dtype=torch.float32, device=device)
     dlogp = torch.empty(tokens, dtype=torch.float32, device=device)
-    ws, wsp = _workspace(lib().policy_loss_workspace(count, tokens), device, "policy_loss")
+    ws, wsp, wsn = _room(lib().policy_loss_workspace(count, tokens), device, "policy_loss")
     _check(lib().policy_loss(lp, dp, rp, mp, ap, per_sequence, op, ob, count, tokens, clip_low, clip_high, kl_coef, code,
-                             grad_scale, loss.data_ptr(), parts.data_ptr(), dlogp.data_ptr(), wsp, ws.numel(),
-                             _stream(device)), "policy_loss")
+                             grad_scale, loss.data_ptr(), parts.data_ptr(), dlogp.data_ptr(), wsp, wsn, _stream(device)),
+           "policy_loss")
     return loss, parts, dlogp
 
 
@@ -277,16 +285,12 @@ def policy_loss(logp, old_logp, advantages, offsets=None, ref_logp=None, mask=No
 
 def _tensors(tensors, device, name):
     """Host arrays of the tensors' pointers, sizes and types (kept alive by the caller), and the number of them."""
-    pointers, sizes, types = [], [], []
-    for t in tensors:
-        code = _TYPES.get(t.dtype)
+    types = [_TYPES.get(t.dtype) for t in tensors]
+    for t, code in zip(tensors, types):
         if code is None or t.device != device or not t.is_contiguous():
             _type(t.dtype, name)
             _ptr(t, device, name)
-        pointers.append(t.data_ptr())
-        sizes.append(t.numel())
-        types.append(code)
-    return array("Q", pointers), array("q", sizes), array("i", types)
+    return array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]), array("i", types)
 
 
 def _address(a):
