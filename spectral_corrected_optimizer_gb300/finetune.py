@@ -316,10 +316,10 @@ def grad_norm(grads, scale: float = 1.0, norm_type: float = 2.0, stream=None):
     """Norm (a fp32 scalar) of scale * g over the values of all tensors together, norm_type 2 or inf.
 
     grads: contiguous CUDA tensors, bf16 or fp32 each."""
+    grads = list(grads)
     if stream is not None:
         return _on(stream, grad_norm, grads, scale=scale, norm_type=norm_type)
     kind = _norm_kind(norm_type)
-    grads = list(grads)
     device = _device_of(grads)
     pointers, sizes, types = _tensors(grads, device, "grads")
     norm = torch.empty((), dtype=torch.float32, device=device)
@@ -335,15 +335,14 @@ def clip_grads(grads, max_norm: float, scale: float = 1.0, norm_type: float = 2.
     out[i] = grads[i] * scale * min(1, max_norm / norm), in place without `out`.  grads, out: contiguous CUDA tensors, bf16
     or fp32 each, out[i] of grads[i]'s shape and of either type (fp32 is what adamw takes).  A NaN norm makes all values
     NaN."""
+    grads, out = list(grads), None if out is None else list(out)
     if stream is not None:
         return _on(stream, clip_grads, grads, max_norm, scale=scale, norm_type=norm_type, out=out)
     kind = _norm_kind(norm_type)
-    grads = list(grads)
     device = _device_of(grads)
     pointers, sizes, types = _tensors(grads, device, "grads")
     out_pointers, out_types = pointers, types
     if out is not None:
-        out = list(out)
         if [t.shape for t in out] != [t.shape for t in grads]:
             raise ValueError("out must have a tensor of the same shape for each of grads")
         out_pointers, _, out_types = _tensors(out, device, "out")

@@ -733,6 +733,58 @@ def test_clipping_refuses_tensors_that_overlap():
     assert abs(float(ft().grad_norm([flat])) - 1) < 1e-6
 
 
+# ---------------------------------------------------------------- more than one round of a launch's blocks, large tensors
+
+@pytest.mark.parametrize("lengths", [[5, 6, 0, 9] * 6000, [600, 500] * 1500])
+def test_preference_loss_of_many_pairs(lengths):
+    # more pairs than a launch has blocks, and more slices than the GPU holds
+    g = gen(len(lengths))
+    offsets = make_offsets(lengths)
+    tokens = int(offsets[-1])
+    logp, r = logps(g, tokens)
+    mask = torch.rand(tokens, generator=g) < 0.8
+    got = ft().preference_loss(logp.cuda(), r.cuda(), offsets.cuda(), beta=0.125, mask=mask.cuda())
+    check_preference(got, wanted(logp, r, offsets, 0.125, "logistic", mask=mask), 0.125)
+
+
+@pytest.mark.parametrize("reduction", ["token", "sequence", "sum"])
+@pytest.mark.parametrize("lengths,per_sequence", [([90, 3, 0, 150, 7] * 1200, True), ([900, 40, 0, 1500] * 400, True),
+                                                  ([900, 40, 0, 1500] * 400, False)])
+def test_policy_loss_of_many_sequences(lengths, per_sequence, reduction):
+    # more sequences than the first launch has blocks, more tiles than the second one
+    g = gen(len(lengths))
+    offsets = make_offsets(lengths, 2)
+    tokens = int(offsets[-1]) + 700
+    logp, old, r, a = policy_inputs(g, tokens, len(lengths), per_sequence)
+    mask = torch.rand(tokens, generator=g) < 0.8
+    kwargs = dict(kl_coef=0.0625, reduction=reduction, per_sequence=per_sequence)
+    got = ft().policy_loss(logp.cuda(), old.cuda(), a.cuda(), offsets.cuda(), ref_logp=r.cuda(), mask=mask.cuda(), **kwargs)
+    check_policy(got, ref.policy(logp, old, a, offsets, r, mask, **kwargs), 0.0625)
+
+
+def test_operators_on_more_than_2_to_the_31_values():
+    rows, dim = 1 << 20, 2056
+    x = torch.empty(rows, dim, dtype=BF, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    gamma = torch.ones(dim, dtype=BF, device="cuda")
+    kept, s, y = ft().layer_norm(x, None, gamma, gamma)
+    pick = torch.tensor([0, 1, rows // 2, rows - 3, rows - 1], device="cuda")
+    stats = ft().NormStatistics(kept.mean[pick], kept.rstd[pick])
+    check_forward(stats, y[pick], x[pick].cpu(), gamma.cpu(), gamma.cpu(), 1e-5)
+    dx, dgamma, dbeta = ft().layer_norm_backward(y, x, kept, gamma, ds=x)
+    w = ref.norm_backward(y[pick].cpu(), x[pick].cpu(), x[pick].cpu(), stats.mean.cpu(), stats.rstd.cpu(), gamma.cpu())
+    inside(dx[pick], w[0], U16 * w[0].abs() + 110 * U32 * w[1])
+    # y = n + 1: dbeta is the number of rows, and so is dgamma, up to the statistics of a million normal values
+    assert bool(((dbeta / rows - 1).abs() < 0.01).all()) and bool(((dgamma / rows - 1).abs() < 0.02).all())
+    del dx, y
+    want = float(torch.sqrt(sum((c.double() ** 2).sum() for c in x.split(1 << 17))))
+    flat = x.view(-1)
+    before = flat[-5:].clone()
+    norm = ft().clip_grads([flat[:7], flat[7:]], want / 2)
+    assert abs(float(norm) / want - 1) <= 20 * U32
+    assert bool(((flat[-5:].double() - before.double() / 2).abs() <= (U16 + 24 * U32) * before.double().abs() / 2).all())
+    assert abs(float(ft().grad_norm([flat])) / want * 2 - 1) <= U16
+
+
 # ---------------------------------------------------------------- streams, graphs, together
 
 def step_inputs(seed=0):
@@ -776,7 +828,8 @@ def test_a_step_of_all_operators_against_autograd_in_64_bits():
     c = min(1.0, 1e-3 / full)
     # y, the probabilities and dh round to bf16 on the way
     rel = lambda a, b: float((a.cpu().double() - b).norm() / b.norm())  # noqa: E731
-    assert abs(float(loss) - float(total)) <= 0.01 * abs(float(total))
+    total = float(total.detach())
+    assert abs(float(loss) - total) <= 0.01 * abs(total)
     assert rel(rewards, score.detach()) <= 2 * U16
     assert abs(float(norm) / full - 1) <= 2 * U16
     for got, want in ((dx, s.grad), (dw, w64.grad * c), (dgamma, g64.grad * c), (dbeta, b64.grad * c)):
