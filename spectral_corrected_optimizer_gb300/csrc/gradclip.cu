@@ -7,8 +7,16 @@
 // the device that a captured graph would repeat), up to kMany tensors a launch.
 // Their memory is cut into chunks of 16 KB; a block takes neighbouring chunks,
 // whatever tensors they lie in, so many small tensors cost what one large one
-// does, and loads a chunk while it works on the one in front.  Each block leaves one partial; a second launch adds the partials in
-// their order, in every block that scales values by the result.
+// does, and loads a chunk while it works on the one in front.  Each block leaves one
+// partial; a second launch adds the partials in their order, in every block that
+// scales values by the result.
+//
+// Measured on a GB300 (copy bandwidth 6.78 TB/s, reading alone 7.4):
+//   norm of 1e9 bytes 142 us, 7.0 TB/s (89 % of the DRAM's cycles); of the 1B model's 4.9 GB of fp32
+//     gradients 700 us;
+//   the same clipped into other buffers 2.21 ms: 14.8 GB, read twice and written once, at 6.7 TB/s;
+//   one layer's bf16 gradients (122 MB) into fp32 86 us; 4e6 fp32 values 14 us.
+// Reading the chunks from the back, what the norm's launch left in L2 first, gained nothing.
 #include <algorithm>
 #include <cstring>
 #include <string>

@@ -1,13 +1,17 @@
 // Losses over the log-probabilities of packed sequences (include/finetune.h): paired
 // preferences, and the clipped policy ratio with a KL term; both with their gradient.
 //
-// A unit of work is a pair, or a sequence.  A cluster of 1 to 8 CTAs takes a unit:
-// it sums over the unit's tokens, the CTAs exchange their sums through distributed
-// shared memory, and each writes the gradient of its tokens.  So a unit's tokens
-// are read once from memory (the second reading, of the mask alone or of what
-// the sums needed, comes from L1 or L2), nothing waits on another cluster, and few
-// long sequences still use many SMs.  Each cluster leaves one partial of the loss;
-// a last launch of one block adds the partials in their order.
+// What a launch is cut by depends on how many sequences there are and how long:
+//   few short ones     one cluster of up to 8 CTAs, each with sequences of its own, which joins
+//                      the loss through distributed shared memory: one launch
+//   many short pairs   a block takes a pair: it sums over both sequences, half of its warps for
+//                      each, and writes their gradient
+//   long pairs         2^n slices of a pair, some 1024 tokens each: a launch sums over the
+//                      slices, the next joins them and writes the gradient
+//   many sequences     the policy's tokens need of one another only a count and an advantage,
+//   (policy loss)      so its tiles of 512 tokens lie wherever memory is cut; a launch in front
+//                      counts the mask and tells each tile the sequence that it begins in
+// A last launch of one block joins the losses, in their order.
 //
 // A thread works on 4 neighbouring tokens at a time, cut at multiples of 4 of the
 // arrays: 16-byte loads wherever a sequence begins.
@@ -17,6 +21,17 @@
 // largest partial sum.  The ratio's clipping is decided on logp - old_logp in two
 // floats against log(1 + clip_high) and log(1 - clip_low) in two floats: at the
 // bound the gradient jumps, and a rounding of the ratio would move tokens over it.
+//
+// Measured on a GB300, in a CUDA graph, inputs out of L2 (copy bandwidth 6.78 TB/s):
+//   1024 pairs of 2 x 2048 tokens on average, prompts masked: 26 us (floor 8.1): slices 16 us, of
+//     which the 38 MB that they read are 6, and the fill 9; a block's chain of offsets, loads,
+//     sums and a barrier is what takes the time (warps wait 12 of 27 cycles for loads, 6 at
+//     barriers).  By a block for each pair, whatever its length: 34; by clusters: 28.
+//   2048 rollouts of 2048 tokens, KL term, one advantage each: 30 us (floor 10.5), 13.3 million
+//     instructions, issue slots 45 % busy; by a block for each sequence 47.
+//   64 pairs of 2 x 8192 9.6 us, 2048 pairs of 2 x 100 8.5, one pair of 45 tokens 3.4;
+//   64 rollouts of 4096 tokens 8.8, 7 of 331 5.3.
+// fp64 sums of the losses alone had cost 5 us: a warp's addition takes 15 cycles here.
 #include <algorithm>
 #include <cmath>
 #include <string>
