@@ -820,7 +820,7 @@ Plan backward_plan(int64_t rows, int dim, int layout, int value_bytes, int tenso
     const int stage_bytes = p.groups * p.tile * p.slot * tensors, room = 220 * 1024;
     p.stages = std::max(1, std::min(3, room / stage_bytes));
     p.smem = std::max<int>(p.stages * stage_bytes, p.groups > 1 ? p.groups * 2 * (int)round_up(dim, 8) * 4 : 0);
-    const int per_sm = std::max(1, std::min(room / (p.smem + 3072), 512 / (p.threads * p.groups)));
+    const int per_sm = std::max(1, std::min(room / (p.smem + 3 * 1024), 512 / (p.threads * p.groups)));
     p.blocks = (int)std::min<int64_t>(ceil_div(rows, p.groups), (int64_t)num_sms() * per_sm / 8 * 8);
     p.blocks = std::max(p.blocks, 1);
     return p;
