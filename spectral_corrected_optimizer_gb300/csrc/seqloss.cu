@@ -553,7 +553,8 @@ __device__ __forceinline__ float4 four_tokens(const Policy &a, unsigned m, const
         // of the exponential
         const float gain = fmaf(adv[i], clipped ? (up ? a.edge_high : a.edge_low) : ratio[i], adv[i]);
         float slope = clipped ? 0.f : -gain;
-        if (a.ref) slope = fmaf(-a.kl_coef, dkl[i], slope);
+        // without a coefficient the divergence is only watched: 0 times one that overflows would be NaN
+        if (a.kl_coef != 0.f) slope = fmaf(-a.kl_coef, dkl[i], slope);
         g[i] = here ? slope * w[i] * a.grad_scale : 0.f;
         const float wh = here ? w[i] : 0.f;
         seen.gain = fmaf(here ? gain : 0.f, w[i], seen.gain);
