@@ -109,8 +109,9 @@ __device__ __forceinline__ float exp_rest(float x) {
     p = fmaf(p, x, 0.5f);
     return p * x * x;
 }
-// exp(x) - 1 of any x, out of line: it is rare, and its copies would crowd the instruction cache
+// exp(x) - 1 and exp(x) of any x, out of line: they are rare, and their copies would crowd the instruction cache
 __device__ __noinline__ float exp_above(float x) { return expm1f(x); }
+__device__ __noinline__ float exp_below(float x) { return expf(x); }
 
 // ---- the tokens ----------------------------------------------------------------------------
 
@@ -510,12 +511,17 @@ struct Seen {
     float gain, kl, clipped;
 };
 
+// How far logp - old lies above the bound that a gain of that sign takes.
+__device__ __forceinline__ float beyond(const Policy &a, bool up, const Two &d) {
+    return (d.hi - (up ? a.log_high.hi : a.log_low.hi)) + (d.lo - (up ? a.log_high.lo : a.log_low.lo));
+}
+
 // A piece's gradient, and what its tokens add to the sums; m says which of them count.
 __device__ __forceinline__ float4 four_tokens(const Policy &a, unsigned m, const Tokens &t, float4 weight, Seen &seen) {
     if (!m) return make_float4(0.f, 0.f, 0.f, 0.f);
     const float lp[4] = {t.logp.x, t.logp.y, t.logp.z, t.logp.w}, old[4] = {t.old.x, t.old.y, t.old.z, t.old.w};
     const float ref[4] = {t.ref.x, t.ref.y, t.ref.z, t.ref.w}, w[4] = {weight.x, weight.y, weight.z, weight.w};
-    const float adv[4] = {t.advantage.x, t.advantage.y, t.advantage.z, t.advantage.w};
+    float adv[4] = {t.advantage.x, t.advantage.y, t.advantage.z, t.advantage.w};
     Two d[4];
     float q[4], ratio[4], kl[4], dkl[4], g[4];  // ratio: its distance from 1
     bool near = true;
@@ -535,8 +541,15 @@ __device__ __forceinline__ float4 four_tokens(const Policy &a, unsigned m, const
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (!(fabsf(d[i].hi) < 1.f)) {
-                ratio[i] = exp_above(d[i].hi);
                 d[i] = finished(d[i]);
+                // A + A (r - 1) would round what is left of A to A's last place: A r goes on as an advantage whose
+                // ratio is 1.  Its sign is A's, and where it vanishes neither bound is near
+                if (d[i].hi <= -1.f && (adv[i] >= 0.f || !(beyond(a, false, d[i]) < 0.f))) {
+                    adv[i] *= exp_below(d[i].hi);
+                    ratio[i] = 0.f;
+                } else {
+                    ratio[i] = exp_above(d[i].hi);
+                }
             }
             if (a.ref && !(fabsf(q[i]) < 1.f)) {
                 dkl[i] = exp_above(q[i]);
@@ -547,7 +560,7 @@ __device__ __forceinline__ float4 four_tokens(const Policy &a, unsigned m, const
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const bool here = counts(m, i), up = adv[i] >= 0.f;
-        const float past = (d[i].hi - (up ? a.log_high.hi : a.log_low.hi)) + (d[i].lo - (up ? a.log_high.lo : a.log_low.lo));
+        const float past = beyond(a, up, d[i]);
         const bool clipped = up ? past > 0.f : past < 0.f;
         // A r as A + A (r - 1): the sum over many tokens whose advantages cancel has no bias from the last place
         // of the exponential

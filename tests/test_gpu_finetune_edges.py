@@ -45,3 +45,21 @@ def test_policy_gradient_where_the_divergence_is_only_watched(lengths, reduction
     loss, parts, dlogp = base.ft().policy_loss(*args, ref_logp=r.cuda(), reduction=reduction)
     assert bool(dlogp.isfinite().all()) and torch.equal(dlogp, alone[2]) and torch.equal(loss, alone[0])
     assert not bool(parts[1].isfinite()) and torch.equal(parts[::2], alone[1][::2])
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 700, 50001])
+@pytest.mark.parametrize("reduction", ["token", "sum"])
+@pytest.mark.parametrize("high", [0.28, INF])
+def test_policy_loss_of_tokens_whose_ratio_is_far_from_one(tokens, reduction, high):
+    # the gradient of a token is -A r of it, however small r is, and the loss of few tokens has the digits of their r
+    g = base.gen(tokens)
+    far = torch.exp(torch.rand(tokens, generator=g) * math.log(85.0))  # |d| from 1 to 85
+    old = -0.5 * torch.rand(tokens, generator=g)
+    up = torch.rand(tokens, generator=g) < 0.25
+    logp = torch.where(up, old + far.clamp_max(20.0), old - far)
+    a = torch.randn(tokens, generator=g)
+    for low, adv in ((0.2, a.abs() + 0.1), (1.0, a)):  # clip_low 1 clips no negative advantage either
+        got = base.ft().policy_loss(logp.cuda(), old.cuda(), adv.cuda(), clip_low=low, clip_high=high, reduction=reduction)
+        want = ref.policy(logp, old, adv, torch.tensor([0, tokens]), low=low, high=high, reduction=reduction)
+        base.check_policy(got, want, 0.0)
+        assert torch.equal(got[2].cpu() == 0, want["dlogp"].float() == 0)
