@@ -548,7 +548,8 @@ __device__ __forceinline__ float4 four_tokens(const Policy &a, unsigned m, const
                     adv[i] *= exp_below(d[i].hi);
                     ratio[i] = 0.f;
                 } else {
-                    ratio[i] = exp_above(d[i].hi);
+                    // 0 times a ratio that overflows would be NaN
+                    ratio[i] = adv[i] == 0.f && d[i].hi >= 1.f ? 0.f : exp_above(d[i].hi);
                 }
             }
             if (a.ref && !(fabsf(q[i]) < 1.f)) {

@@ -63,3 +63,13 @@ def test_policy_loss_of_tokens_whose_ratio_is_far_from_one(tokens, reduction, hi
         want = ref.policy(logp, old, adv, torch.tensor([0, tokens]), low=low, high=high, reduction=reduction)
         base.check_policy(got, want, 0.0)
         assert torch.equal(got[2].cpu() == 0, want["dlogp"].float() == 0)
+
+
+def test_policy_loss_of_an_advantage_of_zero_whose_ratio_overflows():
+    # nothing is clipped: 0 times the ratio is 0, as it is in 64 bits, and the other tokens keep their gradient
+    old = torch.tensor([-100.0, -1.0, -700.0])
+    logp, a = torch.tensor([0.0, -1.5, -3.0]), torch.tensor([0.0, 2.0, -0.0])
+    loss, parts, dlogp = base.ft().policy_loss(logp.cuda(), old.cuda(), a.cuda(), clip_low=1.0, clip_high=INF)
+    want = ref.policy(logp, old, a, torch.tensor([0, 3]), low=1.0, high=INF)
+    assert bool(dlogp.isfinite().all()) and dlogp.cpu()[[0, 2]].tolist() == [0.0, 0.0]
+    base.check_policy((loss, parts, dlogp), want, 0.0)
