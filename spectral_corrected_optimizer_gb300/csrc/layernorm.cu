@@ -917,9 +917,9 @@ extern "C" int64_t layernorm_backward_workspace(int64_t rows, int32_t dim) {
     int64_t bytes = -1;
     entry([&]() -> int {
         if (int rc = check_sizes(rows, dim, STAGE_BF16, "layernorm_backward")) return rc;
-        // the most blocks of any type and layout: the call's are not known yet
+        // the most blocks of any type and layout that such rows can have: the call's are not known yet
         int blocks = 1;
-        for (const int layout : {ROWS_VEC, ROWS_ODD, ROWS_ANY})
+        for (const int layout : {dim % 8 == 0 ? ROWS_VEC : ROWS_ODD, ROWS_ANY})
             for (const int value_bytes : {2, 4})
                 for (const int tensors : {2, 3})
                     blocks = std::max(blocks, backward_plan(rows, dim, layout, value_bytes, tensors).blocks);
