@@ -437,6 +437,7 @@ __device__ __forceinline__ void group_barrier(int group, int threads) {
 }
 
 constexpr int kMaxStages = 4, kMaxGroups = 8;
+constexpr uint32_t kDrainLimit = 1u << 14;  // probes of up to 4 us, for what takes microseconds
 
 // Dynamic shared memory: for each group a ring [stage][row][dy, s, ds][slot].
 template <typename T, int ROWS, int NV, int R>
@@ -495,6 +496,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
             if (tensors == 3) bulk_load(slot_of(stage, r, 2), a.ds.p + from, size[r], &full[stage]);
         }
     };
+    // The copies under way end, again with a limit, before their place is written to or left: what asked for them waits
+    // for either phase of each barrier, whichever is the one under way.
+    auto give_up = [&] {
+        if (tid == 0)
+            for (int i = 0; i < 2 * a.stages; ++i) mbar_wait_limit(&full[i / 2], i & 1, nullptr, 0u, kDrainLimit);
+        return false;
+    };
     const int64_t own_rows = first < a.rows ? (a.rows - first + a.stride - 1) / a.stride : 0;
     const int64_t tiles = (own_rows + R - 1) / R;
     if (tid == 0)
@@ -526,8 +534,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t tile = 0; tile < tiles; ++tile) {
-        // a wait that gives up leaves its code in the flag; later ones do not wait again
-        ok = ok && mbar_wait_bounded(&full[stage], phase, flag, 0x701u);
+        // a wait that gives up leaves its code in the flag; later ones do not wait again, and no further tile is asked for
+        ok = ok && (mbar_wait_bounded(&full[stage], phase, flag, 0x701u) || give_up());
         float rs[R], sums[2 * R];
         F2 c[R][NV][4], g[R][NV][4];  // s - mean and rstd gamma dy
         Raw8<T> add[R][NV];
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) layernorm_backward_kernel(cons
         }
         group_barrier(group, threads);
         // the tile is in registers: its place is for the one `stages` behind it
-        if (tid == 0 && tile + a.stages < tiles) fetch(tile + a.stages, stage);
+        if (tid == 0 && ok && tile + a.stages < tiles) fetch(tile + a.stages, stage);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r >= left) continue;
