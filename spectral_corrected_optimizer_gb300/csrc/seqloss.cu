@@ -130,7 +130,7 @@ struct Sequences {
         if (!offsets) return (int)min((int64_t)i * kUnit, (int64_t)tokens);
         return (int)min((uint64_t)raw(i), (uint64_t)tokens);
     }
-    // whether the offsets i .. i + n keep the rule
+    // whether the offsets i .. i + n keep the rule; without sequences it is the only one's to lie within the tokens
     __device__ __forceinline__ void check(int i, int n) const {
         if (!offsets) return;
         bool good = raw(i) >= 0 && raw(i + n) <= tokens;
@@ -214,6 +214,7 @@ template <int THREADS> __device__ __forceinline__ void zero_outside(const Sequen
     constexpr int kBlocks = 64;
     if (!q.offsets || blockIdx.x >= kBlocks) return;
     const int a = q.begin(0), b = max(a, q.begin(sequences));
+    if (sequences == 0 && blockIdx.x == 0 && threadIdx.x == 0) q.check(0, 0);
     const int64_t at = (int64_t)blockIdx.x * THREADS + threadIdx.x, step = (int64_t)min((int)gridDim.x, kBlocks) * THREADS;
     for (int64_t t = at; t < a; t += step) dlogp[t] = 0.f;
     for (int64_t t = b + at; t < q.tokens; t += step) dlogp[t] = 0.f;
@@ -689,6 +690,7 @@ template <bool VEC> __global__ void __launch_bounds__(kTileThreads, kTileBlocks)
     if (a.q.offsets) {
         b0 = a.q.begin(0);
         b1 = max(b0, a.q.begin(a.q.count));
+        if (a.q.count == 0 && blockIdx.x == 0 && threadIdx.x == 0) a.q.check(0, 0);
         if (!lookup && !a.counting_blocks)  // else the launch in front did
             for (int64_t s = (int64_t)blockIdx.x * kTileThreads + threadIdx.x; s < a.q.count; s += (int64_t)gridDim.x * kTileThreads)
                 a.q.check((int)s, 1);

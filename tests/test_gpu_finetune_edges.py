@@ -73,3 +73,26 @@ def test_policy_loss_of_an_advantage_of_zero_whose_ratio_overflows():
     want = ref.policy(logp, old, a, torch.tensor([0, 3]), low=1.0, high=INF)
     assert bool(dlogp.isfinite().all()) and dlogp.cpu()[[0, 2]].tolist() == [0.0, 0.0]
     base.check_policy((loss, parts, dlogp), want, 0.0)
+
+
+@pytest.mark.parametrize("tokens", [100, 5000])
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_one_offset_outside_the_tokens_is_reported(tokens, dtype):
+    # no sequences: the offset says only where they would begin
+    import spectral_corrected_optimizer_gb300 as so
+    logp, none = torch.full((tokens,), -1.0).cuda(), torch.empty(0).cuda()
+    mask = torch.ones(tokens, dtype=torch.bool).cuda()
+    for at in (-5, tokens + 1, 0, tokens):
+        offsets = torch.tensor([at], dtype=dtype).cuda()
+        for call in (lambda: base.ft().preference_loss(logp, None, offsets),
+                     lambda: base.ft().policy_loss(logp, logp, logp, offsets),
+                     lambda: base.ft().policy_loss(logp, logp, logp, offsets, mask=mask),
+                     lambda: base.ft().policy_loss(logp, logp, none, offsets, reduction="sequence", mask=mask)):
+            got = call()
+            assert float(got[0]) == 0 and bool((got[-1] == 0).all())
+            if 0 <= at <= tokens:
+                so.check_device()
+                continue
+            with pytest.raises(so.SpecOptimError, match="offsets") as e:
+                so.check_device()
+            assert e.value.code == so.ERR_BOUNDS
