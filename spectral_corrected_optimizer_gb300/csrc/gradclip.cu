@@ -9,7 +9,10 @@
 // whatever tensors they lie in, so many small tensors cost what one large one
 // does, and loads a chunk while it works on the one in front.  Each block leaves one
 // partial; a second launch adds the partials in their order, in every block that
-// scales values by the result.
+// scales values by the result.  Where one launch does not take all tensors, a launch
+// of one block adds the partials of all of them, once for the launches that scale: each
+// block of each launch would add them again, work that grows with the square of the
+// tensors (100000 of 10 values 14.5 ms so, 0.80 with the join).
 //
 // Measured on a GB300 (copy bandwidth 6.78 TB/s, reading alone 7.4):
 //   norm of 1e9 bytes 142 us, 7.0 TB/s (89 % of the DRAM's cycles); of the 1B model's 4.9 GB of fp32
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_parts_kernel(cons
 
 // The norm from all partials, the same in every block that asks.  Twice: in fp32, and
 // times 2^-64 for a norm that fp32 does not hold.
-struct Norm {
+struct __align__(16) Norm {
     float value, small;
 };
 template <int KIND> __device__ __forceinline__ Norm norm_of(const Part *parts, int count, float scale, Part *red) {
@@ -277,11 +280,13 @@ template <int KIND> __device__ __forceinline__ Norm norm_of(const Part *parts, i
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(kThreads) norm_join_kernel(const Part *parts, int count, float scale, float *norm) {
+__global__ void __launch_bounds__(kThreads) norm_join_kernel(const Part *parts, int count, float scale, float *norm, Norm *joined) {
     __shared__ Part red[kWarps];
     grid_dependency_wait();
     const Norm n = norm_of<KIND>(parts, count, scale, red);
-    if (threadIdx.x == 0) *norm = n.value;
+    if (threadIdx.x) return;
+    *norm = n.value;
+    if (joined) *joined = n;
 }
 
 // Values of a piece to q, the place of its first one.
@@ -358,13 +363,13 @@ __device__ __forceinline__ void give_run(const Pieces<TI> &p, void *dst, int chu
 template <int CAP, int KIND>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) clip_kernel(const __grid_constant__ Table<CAP> t,
                                                                       const __grid_constant__ Outs<CAP> o, const Part *parts,
-                                                                      int count, float scale, float max_norm, int in_place,
-                                                                      float *norm) {
+                                                                      int count, const Norm *joined, float scale,
+                                                                      float max_norm, int in_place, float *norm) {
     __shared__ Part red[kWarps];
     const int c0 = chunk_begin(t, blockIdx.x), c1 = chunk_begin(t, blockIdx.x + 1);
     grid_dependency_wait();
-    const Norm n = norm_of<KIND>(parts, count, scale, red);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n.value;
+    const Norm n = joined ? *joined : norm_of<KIND>(parts, count, scale, red);
+    if (!joined && blockIdx.x == 0 && threadIdx.x == 0) *norm = n.value;
     float factor = scale;
     if (!(n.value <= max_norm)) factor *= n.value < INFINITY ? max_norm / n.value : max_norm * 0x1p-64f / n.small;
     if (in_place && factor == 1.f) return;
@@ -397,9 +402,13 @@ struct Call {
     cudaStream_t st;
 };
 
+// partials of the launches that form the norm
+int64_t parts_of(int32_t count) {
+    return std::max<int64_t>(1, ceil_div(count, kMany)) * num_sms() * kBlocksPerSm;
+}
+// and the norm itself, where more than one launch scales by it
 int64_t workspace_of(int32_t count) {
-    const int64_t launches = std::max<int64_t>(1, ceil_div(count, kMany));
-    return launches * num_sms() * kBlocksPerSm * (int64_t)sizeof(Part);
+    return parts_of(count) * (int64_t)sizeof(Part) + (count > kMany ? (int64_t)sizeof(Norm) : 0);
 }
 
 // No value is written twice, and none is read after another place's was written to it.
@@ -482,7 +491,7 @@ template <int CAP, int KIND> int run(const Call &c) {
     Outs<CAP> o;
     Part *parts = static_cast<Part *>(c.workspace);
     int total = 0, launches = 0;
-    const int64_t room = workspace_of(c.count) / (int64_t)sizeof(Part);
+    const int64_t room = parts_of(c.count);
     int in_place = c.outs != nullptr;
     for (int i = 0; in_place && i < c.count; ++i) in_place = c.sizes[i] == 0 || c.outs[i] == c.grads[i];
     for (int at = 0; at < c.count;) {
@@ -495,20 +504,22 @@ template <int CAP, int KIND> int run(const Call &c) {
         ++launches;
     }
     cudaError_t e = cudaSuccess;
-    if (!c.outs || !total) {
+    const bool alone = !c.outs || !total;  // nothing to scale
+    Norm *joined = !alone && launches > 1 ? reinterpret_cast<Norm *>(parts + room) : nullptr;
+    if (alone || joined) {
         SPCO_LAUNCH("grad_norm_join", c.st,
                     e = launch_dependent(norm_join_kernel<KIND>, dim3(1), dim3(kThreads), 0, c.st, parts, total, c.scale,
-                                         c.norm));
+                                         c.norm, joined));
         SPECOPTIM_CUDA(e);
-        return SPECOPTIM_OK;
     }
+    if (alone) return SPECOPTIM_OK;
     for (int at = 0; at < c.count;) {
         if (launches > 1) fill(c, at, &t, &o);
         else at = c.count;  // the table of the norm's only launch
         if (!t.count) break;
         SPCO_LAUNCH("clip_grads", c.st,
                     e = launch_dependent(clip_kernel<CAP, KIND>, dim3(t.blocks), dim3(kThreads), 0, c.st, t, o, parts, total,
-                                         c.scale, c.max_norm, in_place, c.norm));
+                                         joined, c.scale, c.max_norm, in_place, c.norm));
         SPECOPTIM_CUDA(e);
     }
     return SPECOPTIM_OK;

@@ -96,3 +96,25 @@ def test_one_offset_outside_the_tokens_is_reported(tokens, dtype):
             with pytest.raises(so.SpecOptimError, match="offsets") as e:
                 so.check_device()
             assert e.value.code == so.ERR_BOUNDS
+
+
+# ---------------------------------------------------------------- gradient norm and clipping
+
+def test_clipping_more_tensors_than_a_launch_takes_joins_their_norm_once():
+    # each launch would join the partial sums of all of them again: work that grows with the square of the tensors
+    import spectral_corrected_optimizer_gb300 as so
+    grads = [x.cuda() for x in base.tensors(base.gen(4), [5, 3, 40] * 1100, (FP, BF))]
+    before = [x.cpu() for x in grads]
+    norm = ref.norm_of(before)
+    so.trace_enable(True)
+    try:
+        so.trace_reset()
+        got = base.ft().clip_grads(grads, norm / 2)
+        report = so.trace_report()
+    finally:
+        so.trace_enable(False)
+        so.trace_reset()
+    assert {k: v[0] for k, v in report.items()} == {"grad_norm": 4, "grad_norm_join": 1, "clip_grads": 4}
+    base.inside(got, torch.tensor(norm, dtype=torch.float64), 20 * U32 * norm)
+    for x, o in zip(before, grads):
+        base.inside(o, x.double() / 2, (base.u_of(o.dtype) + 24 * U32) * x.double().abs() / 2 + 1e-44)
