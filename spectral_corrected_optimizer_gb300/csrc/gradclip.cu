@@ -257,10 +257,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_parts_kernel(cons
     if (threadIdx.x == 0) parts[blockIdx.x] = v;
 }
 
-// The norm from all partials, the same in every block that asks.  Twice: in fp32, and
-// times 2^-64 for a norm that fp32 does not hold.
+// The norm from all partials, the same in every block that asks: in fp32, and as |scale| root unit, unit a power of two,
+// where fp32 does not hold it.
 struct __align__(16) Norm {
-    float value, small;
+    float value, root, unit;
 };
 template <int KIND> __device__ __forceinline__ Norm norm_of(const Part *parts, int count, float scale, Part *red) {
     Part v{0.f, 0.f, 0.};
@@ -272,11 +272,26 @@ template <int KIND> __device__ __forceinline__ Norm norm_of(const Part *parts, i
     }
     v = block_join<KIND>(v, red);
     if (KIND == NORM_L2 && v.far != 0.) {
-        const double n = fabs((double)scale) * sqrt(v.far + ((double)v.sum + (double)v.lost));
-        return {(float)n, (float)(n * 0x1p-64)};
+        const double n = sqrt(v.far + ((double)v.sum + (double)v.lost));  // 2^-149 to 2^148
+        const float value = (float)(fabs((double)scale) * n);
+        return n >= 1. ? Norm{value, (float)(n * 0x1p-64), 0x1p64f} : Norm{value, (float)(n * 0x1p64), 0x1p-64f};
     }
     const float n = KIND == NORM_L2 ? sqrtf(v.sum + v.lost) : v.sum;
-    return {fabsf(scale) * n, fabsf(scale) * 0x1p-64f * n};
+    return {fabsf(scale) * n, n, 1.f};
+}
+
+// What a value is multiplied by: two factors, the second one a power of two and 1 wherever fp32 holds their product.
+struct Factor {
+    float a, b;
+    __device__ __forceinline__ float operator()(float v) const { return v * a * b; }
+};
+__device__ __forceinline__ Factor factor_of(const Norm &n, float scale, float max_norm) {
+    constexpr float kLeast = 0x1p-126f;  // below, fp32 has fewer digits
+    if (n.value <= max_norm) return {scale, 1.f};
+    const float ratio = max_norm / n.value, f = scale * ratio;
+    if (n.value != n.value || (n.value < INFINITY && n.value >= kLeast && ratio >= kLeast && fabsf(f) >= kLeast)) return {f, 1.f};
+    const double x = copysign((double)max_norm, (double)scale) / ((double)n.root * (double)n.unit);
+    return fabs(x) < 0x1p-100 ? Factor{(float)(x * 0x1p100), 0x1p-100f} : Factor{(float)x, 1.f};
 }
 
 template <int KIND>
@@ -306,7 +321,7 @@ __device__ __forceinline__ void put_values(bf16 *q, const float (&v)[4]) {
 
 // A chunk that may be cut short, or whose values go to places that are not aligned.
 template <typename TI, typename TO>
-__device__ __forceinline__ void give_part(const Pieces<TI> &p, TO *q, int64_t first, float factor) {
+__device__ __forceinline__ void give_part(const Pieces<TI> &p, TO *q, int64_t first, Factor factor) {
     constexpr int V = Pieces<TI>::V;
     const Loaded x = load_part(p, first);
 #pragma unroll
@@ -316,24 +331,24 @@ __device__ __forceinline__ void give_part(const Pieces<TI> &p, TO *q, int64_t fi
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int64_t at = (first + k * kThreads) * V + i;
-            if (at >= p.head && at < p.end) q[at] = from_f<TO>(v[i] * factor);
+            if (at >= p.head && at < p.end) q[at] = from_f<TO>(factor(v[i]));
         }
     }
 }
-template <typename TI, typename TO> __device__ __forceinline__ void give(const Loaded &x, TO *q, float factor) {
+template <typename TI, typename TO> __device__ __forceinline__ void give(const Loaded &x, TO *q, Factor factor) {
     constexpr int V = Pieces<TI>::V;
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
         float v[V];
         piece_values(x.u[k], v);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= factor;
+        for (int i = 0; i < V; ++i) v[i] = factor(v[i]);
         put_values(q + k * kThreads * V, v);
     }
 }
 // Neighbouring chunks of one tensor, the whole ones in a loop that loads ahead.
 template <typename TI, typename TO>
-__device__ __forceinline__ void give_run(const Pieces<TI> &p, void *dst, int chunk, int count, float factor) {
+__device__ __forceinline__ void give_run(const Pieces<TI> &p, void *dst, int chunk, int count, Factor factor) {
     constexpr int V = Pieces<TI>::V, ALIGN = V * (int)sizeof(TO);  // of a piece's values
     TO *q = static_cast<TO *>(dst) - p.head;  // value `at` of the pieces goes to q[at]
     int lo, hi;
@@ -370,9 +385,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) clip_kernel(const __gr
     grid_dependency_wait();
     const Norm n = joined ? *joined : norm_of<KIND>(parts, count, scale, red);
     if (!joined && blockIdx.x == 0 && threadIdx.x == 0) *norm = n.value;
-    float factor = scale;
-    if (!(n.value <= max_norm)) factor *= n.value < INFINITY ? max_norm / n.value : max_norm * 0x1p-64f / n.small;
-    if (in_place && factor == 1.f) return;
+    const Factor factor = factor_of(n, scale, max_norm);
+    if (in_place && factor.a == 1.f && factor.b == 1.f) return;
     each_tensor(t, c0, c1, [&](int i, int chunk, int count) {
         void *dst = o.dst[i];
         if (t.type[i] == STAGE_BF16) {

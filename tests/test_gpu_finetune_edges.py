@@ -118,3 +118,23 @@ def test_clipping_more_tensors_than_a_launch_takes_joins_their_norm_once():
     base.inside(got, torch.tensor(norm, dtype=torch.float64), 20 * U32 * norm)
     for x, o in zip(before, grads):
         base.inside(o, x.double() / 2, (base.u_of(o.dtype) + 24 * U32) * x.double().abs() / 2 + 1e-44)
+
+
+@pytest.mark.parametrize("size,scale", [(1e37, 1.0), (3e33, 1.0), (3e33, -0.5), (1.0, 1e36), (1e-3, 3e38), (1e30, 1e20)])
+@pytest.mark.parametrize("most", [1.0, 1e-3, 1e-6])
+@pytest.mark.parametrize("norm_type", [2.0, INF])
+def test_clipping_by_factors_far_below_what_fp32_holds(size, scale, most, norm_type):
+    # max_norm / norm leaves fp32's normal range, the clipped values do not
+    x = (torch.randn(20000, generator=base.gen(3)) * size).float()
+    x[5] = size * 3
+    scale, most = (float(torch.tensor(v)) for v in (scale, most))
+    norm = ref.norm_of([x], scale, norm_type)
+    want = x.double() * (scale * most / norm)
+    for dtype in (FP, BF):
+        out = torch.empty_like(x, dtype=dtype, device="cuda")
+        got = base.ft().clip_grads([x.cuda()], most, scale=scale, norm_type=norm_type, out=[out])
+        if norm < 3.4e38:
+            base.inside(got, torch.tensor(norm, dtype=torch.float64), 20 * U32 * norm)
+        else:
+            assert float(got) == INF
+        base.inside(out, want, (base.u_of(dtype) + 24 * U32) * want.abs() + 1e-44)
