@@ -14,7 +14,8 @@ The losses return their gradient with respect to the log-probabilities, which
 head_logp_backward takes.  Every operation runs in the library's CUDA kernels.
 Outputs and workspaces come from torch's caching allocator.  With `stream`
 given, a call allocates and runs on that stream and marks its inputs as used
-there; waiting for the inputs and for the outputs is the caller's.
+there; waiting for the inputs and for the outputs is the caller's.  Tensors are on
+the current device; calls on another one's are refused.
 """
 from __future__ import annotations
 

@@ -13,7 +13,8 @@ a training pipeline's end stages, beside the masked boundary between them.
 Every operation runs in the library's CUDA kernels.  Outputs and workspaces
 come from torch's caching allocator.  With `stream` given, a call allocates and
 runs on that stream and marks its inputs as used there; waiting for the inputs
-and for the outputs is the caller's, as with any work on two streams.
+and for the outputs is the caller's, as with any work on two streams.  Tensors
+are on the current device; calls on another one's are refused.
 """
 from __future__ import annotations
 
@@ -72,6 +73,9 @@ def _matrix(t, shape, dtype, device, name):
 
 
 def _stream(device):
+    """The current stream of the call's device, which has to be the current one: kernels are launched there."""
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, torch._C._cuda_getDevice()))
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 

@@ -27,3 +27,18 @@ def test_layernorm_workspace_of_every_narrow_width(lib):
     sizes = eval(run.stdout)
     # at least one partial of both vectors, rows padded to 8 values
     assert all(n >= 2 * 4 * (-(-dim // 8) * 8) for n, dim in zip(sizes, 3 * list(range(1, 18)))), sizes
+
+
+def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch):
+    # the library launches on the current device, whose kernels must not be given another one's memory
+    torch = pytest.importorskip("torch")
+    from spectral_corrected_optimizer_gb300 import finetune, stage_ends
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 100 + index, raising=False)
+    assert finetune._stream is stage_ends._stream and finetune._stream(torch.device("cuda", 0)) == 100
+    with pytest.raises(ValueError, match="tensors are on cuda:1, the current device is cuda:0"):
+        finetune._stream(torch.device("cuda", 1))
+    # every operator of both modules asks for its stream there
+    for module in (finetune, stage_ends):
+        text = open(module.__file__).read()
+        assert text.count("_check(lib()") == text.count("_stream(device))") and text.count("_cuda_getCurrentRawStream") <= 1
