@@ -28,3 +28,18 @@ def test_a_ring_that_gives_up_a_wait_lets_its_copies_end():
     drain = re.search(r"auto give_up = \[&\] \{\s*if \(tid == 0\)\s*for \(int i = 0; i < 2 \* a\.stages; \+\+i\) "
                       r"mbar_wait_limit\(&full\[i / 2\], i & 1, nullptr, 0u, kDrainLimit\);\s*return false;\s*\};", body)
     assert drain and body.count("mbar_wait") == 2 and "if (tid == 0)\n        for (int i = 0; i < a.stages && i < tiles; ++i) fetch(i, i);" in body
+
+
+def test_kernels_that_wait_for_the_launch_in_front_read_it_with_plain_loads():
+    # as test_stage_ends_sources.py has it for the others; what these read with __ldg are inputs of the call, complete
+    # before its first, ordinary launch
+    for name in ("layernorm.cu", "seqloss.cu", "gradclip.cu"):
+        text = source(name)
+        kernels = re.findall(r"__global__ void([^;{]*)\{(.*?)\n\}\n", text, re.S)
+        waiting = [(head, body) for head, body in kernels if "grid_dependency_wait()" in body]
+        assert len(kernels) >= 3 and waiting, name
+        for head, body in waiting:
+            assert not re.search(r"const [\w ]+\*\s*__restrict__", head), (name, head)
+            assert "__ldg" not in body and ".nc." not in body, (name, head)
+        assert set(re.findall(r"__ldg\(([\w.]+)", text)) <= {"a.mean", "a.rstd"}, name
+        assert "kLasting" not in text, name

@@ -138,3 +138,87 @@ def test_clipping_by_factors_far_below_what_fp32_holds(size, scale, most, norm_t
         else:
             assert float(got) == INF
         base.inside(out, want, (base.u_of(dtype) + 24 * U32) * want.abs() + 1e-44)
+
+
+# ---------------------------------------------------------------- widths and sizes at the borders of the launches' rules
+
+@pytest.mark.parametrize("rows,dim", [(33, 4081), (33, 4083), (33, 4090), (17, 8177), (17, 8178), (17, 8185), (17, 8186)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_layer_norm_of_odd_widths_at_the_borders_of_a_thread_s_pieces(rows, dim, dtype):
+    # a row that begins anywhere between two 16-byte boundaries has (dim + 14) / 8 pieces: 512 of them is one for each
+    # thread, 1024 two
+    base.test_layer_norm_and_its_backward(rows, dim, dtype, True)
+    base.test_layer_norm_and_its_backward(rows, dim, dtype, False)
+
+
+def test_head_logp_backward_of_more_tokens_than_are_listed_by_one_launch():
+    # from 65536 tokens on those that take part are counted in stretches first, by target and by gradient
+    g = base.gen(5)
+    tokens, vocab, dim = 70001, 50, 8
+    h, w = base.randn(g, (tokens, dim), BF), base.randn(g, (vocab, dim), BF, 0.5)
+    target = torch.randint(0, vocab, (tokens,), generator=g)
+    target[::3] = -100
+    dlogp = base.randn(g, (tokens,), FP, 1 / tokens)
+    dlogp[torch.rand(tokens, generator=g) < 0.3] = 0.0
+    _, kept = base.ft().head_logp(h.cuda(), w.cuda(), target.cuda())
+    dh, dw = base.ft().head_logp_backward(dlogp.cuda(), kept, h.cuda(), w.cuda(), target.cuda())
+    want = base.stage_ends_ref.head(h, w, target, mean=False)
+    base.check_weighted(dh, dw, dlogp, want, h, w)
+
+
+def test_gradients_of_the_norm_s_vectors_over_a_million_rows():
+    rows, dim = 1 << 20, 264
+    g = torch.Generator("cuda").manual_seed(2)
+    x, dy = (torch.empty(rows, dim, dtype=BF, device="cuda").normal_(generator=g) for _ in range(2))
+    gamma = torch.ones(dim, dtype=BF, device="cuda")
+    kept, s, _ = base.ft().layer_norm(x, None, gamma)
+    _, dgamma, dbeta = base.ft().layer_norm_backward(dy, s, kept, gamma)
+    sums = torch.zeros(4, dim, dtype=torch.float64, device="cuda")
+    for i in range(0, rows, 1 << 16):
+        at = slice(i, i + (1 << 16))
+        d = dy[at].double()
+        n = d * (x[at].double() - kept.mean[at, None].double()) * kept.rstd[at, None].double()
+        for k, t in enumerate((n, n.abs(), d, d.abs())):
+            sums[k] += t.sum(0)
+    # the rows are shared out to at least 152 groups of threads: a column's thread adds at most that share of them, and what
+    # the threads leave is added in fewer than 20 steps, the roundings of a term among them
+    steps = -(-rows // 152) + 20
+    assert bool(((dgamma.double() - sums[0]).abs() <= steps * U32 * sums[1]).all())
+    assert bool(((dbeta.double() - sums[2]).abs() <= steps * U32 * sums[3]).all())
+
+
+def test_losses_of_as_many_tokens_as_a_call_may_have():
+    tokens = 1 << 30
+    g = torch.Generator("cuda").manual_seed(4)
+    logp, old = (torch.empty(tokens, device="cuda").uniform_(-2, 0, generator=g) for _ in range(2))
+    a = torch.empty(tokens, device="cuda").normal_(generator=g)
+    half = tokens // 2 - 5
+    offsets = torch.tensor([3, half, tokens - 1], device="cuda")
+    chunks = [slice(i, i + (1 << 26)) for i in range(0, tokens, 1 << 26)]
+    at = torch.tensor([0, 2, 3, 4, half - 1, half, half + 1, tokens - 3, tokens - 2, tokens - 1], device="cuda")
+    # one pair, scores of half a billion differences each: the sums are kept to 2^-44 and rounded once
+    beta = 2.0 ** -12
+    loss, pair_loss, rewards, dlogp = base.ft().preference_loss(logp, old, offsets, beta=beta)
+    score = torch.stack([sum((logp[s].double() - old[s].double()).sum() for s in [slice(o, min(o + (1 << 26), e)) for o in
+                             range(b, e, 1 << 26)]) for b, e in ((3, half), (half, tokens - 1))])
+    size = beta * tokens  # |difference| <= 2, and its rounding u32 of it
+    base.inside(rewards[0], beta * score.cpu(), U32 * (size + 4 * (beta * score.cpu()).abs()))
+    delta = beta * float(score[0] - score[1])
+    slope = beta / (1 + math.exp(delta))
+    off = 2 * U32 * size  # of delta, and of the slope in parts of 1 / 4 of it
+    want = torch.tensor([0, 0, -slope, -slope, -slope, slope, slope, slope, slope, 0], dtype=torch.float64)
+    base.inside(dlogp[at], want, (beta * 0.25 * off + 16 * U32 * slope) * (want != 0))
+    assert abs(float(loss) - math.log1p(math.exp(-delta))) <= off + 8 * U32 * float(loss)
+    del dlogp
+    loss, parts, dlogp = base.ft().policy_loss(logp, old, a)
+    gain, clipped = 0.0, 0
+    for s in chunks:
+        d, x = logp[s].double() - old[s].double(), a[s].double()
+        far = torch.where(x >= 0, d > math.log1p(0.2), d < math.log1p(-0.2))
+        gain += float((x * torch.where(far, torch.where(x >= 0, 1.2, 0.8).double(), torch.exp(d))).sum())
+        clipped += int(far.sum())
+        slope = torch.where(far, 0.0, -x * torch.exp(d)) / tokens
+        assert bool(((dlogp[s].double() - slope).abs() <= 13 * U32 * slope.abs() + 1e-44).all())
+    # a thread adds at most 7885 terms of magnitude |a| exp(2) / tokens at most, 13 steps between threads
+    steps = (7885 + 13) * U32
+    assert abs(float(loss) + gain / tokens) <= steps * math.exp(2) and abs(float(parts[2]) - clipped / tokens) <= steps
