@@ -34,7 +34,9 @@ extern "C" {
  *   y = (s - mean) * rstd * gamma + beta.
  * x, r, s, y: [rows][dim], gamma, beta: [dim], all of `type` (STAGE_BF16 or
  * STAGE_FP32); mean, rstd: [rows] fp32.  r NULL: s = x, and s is not written (it
- * may be NULL).  beta NULL: none.  s may be x or r.  dim <= 32768. */
+ * may be NULL).  beta NULL: none.  s may be x or r.  dim <= 32768.  Statistics are
+ * fp32: where the squares of a row leave its range (differences from the mean of
+ * 1e17 in wide rows, 1e19 in narrow ones), rstd is 0. */
 int layernorm_forward(const void *x, const void *r, const void *gamma, const void *beta, int32_t type, float eps,
                       void *s, void *y, float *mean, float *rstd, int64_t rows, int32_t dim, void *stream);
 
@@ -83,7 +85,8 @@ int head_logp_backward(const float *dlogp, const float *kept, const void *h, con
  * tokens that do not count, infinities and NaN too, reaches no output.  Offsets
  * that break the rule are moved into it, so that nothing outside the arrays is
  * touched, and reported as SPECOPTIM_ERR_BOUNDS by the next
- * specoptim_check_device; what such a call returns is not defined. */
+ * specoptim_check_device; what such a call returns is not defined.  Without
+ * sequences the rule is that the only offset lies within [0, tokens]. */
 
 #define PREFERENCE_LOGISTIC 0
 #define PREFERENCE_HINGE 1
@@ -120,7 +123,9 @@ int preference_loss(const float *logp, const float *ref_logp, const uint8_t *mas
  * gradient of grad_scale * loss, dlogp [tokens] fp32, is
  *   weight (-A r [not clipped] + kl_coef (1 - exp(q))),
  * a token being clipped where r lies beyond the bound that gain takes; that is
- * decided on logp - old_logp to twice fp32's digits.  advantages: [tokens], or
+ * decided on logp - old_logp to twice fp32's digits.  A r has fp32's digits however
+ * small r is, and is 0 where A is 0 and r overflows.  With kl_coef 0 and ref_logp
+ * the divergence is only reported: it reaches neither loss nor dlogp.  advantages: [tokens], or
  * [sequences] with per_sequence.  offsets NULL: all tokens are one sequence
  * (sequences is 1).  parts: aggregate(-gain), aggregate(kl), aggregate(clipped);
  * loss: one fp32.  Without a token that counts all are 0. */
@@ -149,7 +154,8 @@ int grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *typ
  * are the same (in place); apart from that outs overlap neither one another nor
  * any of grads, which is checked.  A NaN among the values makes every value NaN,
  * an infinity makes finite values 0 and infinite ones NaN; a norm of finite values
- * that is beyond fp32 is returned as infinity, but scales them by what it is. */
+ * that is beyond fp32 is returned as infinity, but scales them by what it is, and
+ * max_norm / norm may lie far below fp32's range. */
 int clip_grads(const void *const *grads, const int64_t *sizes, const int32_t *types, void *const *outs,
                const int32_t *out_types, int32_t count, float scale, float max_norm, int32_t kind, float *norm,
                void *workspace, int64_t workspace_bytes, void *stream);

@@ -18,7 +18,13 @@
 //   norm of 1e9 bytes 142 us, 7.0 TB/s (89 % of the DRAM's cycles); of the 1B model's 4.9 GB of fp32
 //     gradients 700 us;
 //   the same clipped into other buffers 2.21 ms: 14.8 GB, read twice and written once, at 6.7 TB/s;
-//   one layer's bf16 gradients (122 MB) into fp32 86 us; 4e6 fp32 values 14 us.
+//   one layer's bf16 gradients (122 MB) into fp32 89 us, 5.5 TB/s; 33 for the norm and 62 for the
+//     scaling where each launch is timed by itself; 4e6 fp32 values 14 us;
+//   2.5e8 fp32 values in place 473 us, into another buffer 470, bf16 248 and 246.
+// Values that lie otherwise between two 16-byte boundaries than where they are written to (bf16 into
+// fp32: between 16 and 32) are written one by one: 2.5e8 fp32 values 711 us, bf16 780, bf16 into fp32
+// 1141 (334 where they lie alike), fp32 into bf16 538 (383).  Buffers of their own lie alike.
+// The norm of squares spills 20 bytes a thread (4 of the other norm).
 // Reading the chunks from the back, what the norm's launch left in L2 first, gained nothing.
 #include <algorithm>
 #include <cstring>
@@ -308,7 +314,8 @@ __global__ void __launch_bounds__(kThreads) norm_join_kernel(const Part *parts, 
 __device__ __forceinline__ void put_values(float *q, const float (&v)[4]) {
     *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
 }
-// 32 bytes as one store: two of 16 write each sector in halves (one layer's bf16 gradients to fp32: 61 us, 78 with two)
+// 32 bytes as one store: two of 16 write each sector in halves (scaling one layer's bf16 gradients to fp32, the launch by
+// itself: 62 us, 78 with two)
 __device__ __forceinline__ void put_values(float *q, const float (&v)[8]) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
                  "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])

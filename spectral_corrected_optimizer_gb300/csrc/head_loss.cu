@@ -22,9 +22,9 @@
 // steps 1 and 3 from what was kept (6 N V D), with d times -dlogp_i: the factor goes into
 // the normalisation that turns logits into probabilities, so a weighted d is rounded to
 // bf16 once, like any other, and the products do not know of it.  Tokens whose dlogp is 0
-// are left out in step 1.  4096 tokens, half of them without a target, V = 128256, D = 2048: 2.06
-// ms, 1.57 PFLOP/s (1.66 ms at the burst rate); 333 tokens over 50001 x 1000: 97 us, two of them
-// the listing.
+// are left out in step 1.  4096 tokens, half of them without a target, V = 128256, D = 2048: 2.03
+// to 2.13 ms, 1.52 to 1.59 PFLOP/s (1.67 ms at the burst rate); 333 tokens over 50001 x 1000: 98
+// us, two of them the listing.
 //
 // A piece's logits are formed twice, 8 N V D operations where keeping [N][V] would take
 // 6: that is the price of not keeping them, and of rounding a probability once (bf16,

@@ -23,8 +23,9 @@
 // row's first piece belong to the row in front.  The rows of a group lie a
 // multiple of 8 rows apart, so ph is the same for all of them.
 //
-// Rows off a 16-byte boundary (ROWS_ANY) and rows above 8192 values take a backward pass of two
-// kernels that read them twice each.
+// Rows off a 16-byte boundary (ROWS_ANY) and rows of more than 1024 pieces take a backward pass of
+// two kernels: one reads them twice, the other once more.  Those are rows above 8192 values, and odd
+// ones from 8186 on, which may begin in the last value of a piece (16384 x 8190: 613 us, x 8192 181).
 //
 // All statistics and sums are fp32; s, y and dx are rounded once to their type.
 //
@@ -34,9 +35,13 @@
 //   backward 177 us, 6.08 TB/s (90 %): 240 instructions a warp and row, issue slots 55 % busy at
 //     16 warps an SM, which the ring leaves; from registers instead of a second reading of shared
 //     memory 177, with it 212 to 219.
-// fp32 32768 x 2048 159 and 171 us.  Without ds the backward pass takes 163 (73 %), without r the
-// forward pass 104 (77 %): a row's chain.  Odd rows cost instructions: 32768 x 2046 166 and 218 us
-// (80 at the copy's rate).  Narrow rows too: 65536 x 64 20 and 31 (5).
+// fp32 32768 x 2048 159 and 171 us.  Without ds the backward pass takes 164 (73 %), without r the
+// forward pass 104 (77 %): a row's chain.  Odd rows cost instructions: 32768 x 2046 166 and 219 us
+// (80 at the copy's rate).  Narrow rows too: 65536 x 64 21 and 31 (5).
+// Bytes that spill, a thread: odd and unaligned bf16 rows of up to 2 pieces 96 to 132 forward (64
+// registers, for two blocks an SM); fp32 forward 432 with 4 pieces and 848 to 1036 with 8 or 9; odd
+// rows of 2 pieces backward 176 (bf16) and 280 (fp32); the other kernels 68 at most, but for the odd
+// bf16 rows of 9 pieces (136).
 #include <algorithm>
 #include <string>
 
@@ -214,7 +219,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Whether a row is loaded while the one in front is worked on.  Pays where the registers allow it: cold,
 // with / without, bf16 65536 x 2048 163 / 168 us, 32768 x 4096 164 / 171, fp32 32768 x 2048 158 / 164; more
-// pieces of fp32, or rows that are shifted into place, spill (fp32 16384 x 4096 with 4 pieces 202 / 176).
+// pieces of fp32, or rows that are shifted into place, spill without it already, and more with it (fp32
+// 16384 x 4096 with 4 pieces 202 / 176).
 template <typename T> constexpr bool loads_ahead(int rows, int nv) {
     return rows == ROWS_VEC && nv * (int)sizeof(T) <= 8;
 }

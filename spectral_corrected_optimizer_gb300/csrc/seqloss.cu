@@ -28,10 +28,12 @@
 //     sums and a barrier is what takes the time (warps wait 12 of 27 cycles for loads, 6 at
 //     barriers).  By a block for each pair, whatever its length: 34; by clusters: 28.
 //   2048 rollouts of 2048 tokens, KL term, one advantage each: 30 us (floor 10.5), 13.3 million
-//     instructions, issue slots 45 % busy; by a block for each sequence 47.
+//     instructions, issue slots 47 % busy; by a block for each sequence 47.
 //   64 pairs of 2 x 8192 9.6 us, 2048 pairs of 2 x 100 8.5, one pair of 45 tokens 3.4;
 //   64 rollouts of 4096 tokens 8.8, 7 of 331 5.3.
 // fp64 sums of the losses alone had cost 5 us: a warp's addition takes 15 cycles here.
+// At the blocks an SM that their bounds ask for, the slices spill 16 bytes a thread (44 where the
+// arrays are not aligned) and the tiles 20 (4).
 #include <algorithm>
 #include <cmath>
 #include <string>

@@ -246,7 +246,7 @@ def policy_loss(logp, old_logp, advantages, offsets=None, ref_logp=None, mask=No
     offsets).  offsets: int32 or int64 [sequences + 1], where each sequence begins and the last ends (None: all tokens are
     one).  mask: bool or uint8 [tokens], the tokens that count.  reduction: "token" (mean over them), "sequence" (mean of
     the sequences' means) or "sum".  parts (fp32 [3]): the policy part of the loss, the KL divergence and the clipped share,
-    aggregated alike; loss = parts[0] + kl_coef * parts[1].  dlogp is the gradient of grad_scale * loss, 0 at tokens that
+    aggregated alike; loss = parts[0] + kl_coef * parts[1] (with kl_coef 0 the divergence is only reported).  dlogp is the gradient of grad_scale * loss, 0 at tokens that
     do not count.  per_sequence says which advantages are given; it is needed only where tokens and sequences are as many."""
     if stream is not None:
         return _on(stream, policy_loss, logp, old_logp, advantages, offsets=offsets, ref_logp=ref_logp, mask=mask,
